@@ -21,6 +21,9 @@ HGA_ERR_CUDA = -4
 HGA_ERR_TIMEOUT = -5
 HGA_ERR_WORKSPACE = -6
 HGA_ERR_TOO_LARGE = -7
+HGA_ERR_PAGES = -8
+HGA_PACKED_FILL_TAIL = 1
+HGA_PACKED_CLEAR_STATUS = 2
 HGA_NOALLOC_MAX_ROWS = 1 << 20
 HGA_F32 = 0
 HGA_BF16 = 1
@@ -31,7 +34,9 @@ EXPORTS = ("hga_workspace_size", "hga_route_launches", "hga_build_summaries", "h
            "hga_attn_bwd_preprocess", "hga_attn_bwd_dkdv", "hga_attn_bwd_dq", "hga_attn_bwd_noalloc",
            "hga_noalloc_read_status", "hga_tier_cache_config", "hga_route_chunks", "hga_gcache_plan",
            "hga_gcache_fetch", "hga_route_groups_cached", "hga_tier_plan", "hga_tier_gather",
-           "hga_read_status", "hga_strerror", "hga_version")
+           "hga_packed_workspace_size", "hga_packed_attn_fwd", "hga_packed_attn_bwd", "hga_pages_workspace_size",
+           "hga_pages_reserve", "hga_pages_write", "hga_paged_attn", "hga_pages_fork", "hga_pages_free",
+           "hga_pages_compact", "hga_pages_copy", "hga_read_status", "hga_strerror", "hga_version")
 
 
 class HGAConfig(ctypes.Structure):
@@ -45,6 +50,23 @@ class HGAConfig(ctypes.Structure):
 
     def __repr__(self):
         return "HGAConfig(" + ", ".join(f"{n}={getattr(self, n)}" for n, _ in self._fields_) + ")"
+
+
+class PackedConfig(ctypes.Structure):
+    """Mirror of ``hga_packed_config_t``."""
+    _fields_ = [("Hq", ctypes.c_int32), ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32), ("n_seqs", ctypes.c_int32),
+                ("total", ctypes.c_int64), ("q_stride_t", ctypes.c_int64), ("q_stride_h", ctypes.c_int64),
+                ("k_stride_t", ctypes.c_int64), ("k_stride_h", ctypes.c_int64), ("v_stride_t", ctypes.c_int64),
+                ("v_stride_h", ctypes.c_int64), ("dtype", ctypes.c_int32), ("flags", ctypes.c_int32),
+                ("softmax_scale", ctypes.c_float), ("reserved", ctypes.c_int32), ("wait_limit_ns", ctypes.c_int64)]
+
+
+class PagesConfig(ctypes.Structure):
+    """Mirror of ``hga_pages_config_t``."""
+    _fields_ = [("n_layers", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32), ("max_seqs", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("dtype", ctypes.c_int32), ("layer_stride", ctypes.c_int64),
+                ("page_stride", ctypes.c_int64), ("wait_limit_ns", ctypes.c_int64)]
 
 
 class HGAError(RuntimeError):
@@ -66,6 +88,7 @@ def load() -> ctypes.CDLL:
                            "`python -m hierarchical_kv_routing_tok_b200.build` (nvcc, sm_100a)")
     lib = ctypes.CDLL(LIB_PATH)
     P, C = ctypes.c_void_p, ctypes.POINTER(HGAConfig)
+    K, G, I, L = ctypes.POINTER(PackedConfig), ctypes.POINTER(PagesConfig), ctypes.c_int32, ctypes.c_int64
     sig = {
         "hga_workspace_size": [C, ctypes.POINTER(ctypes.c_size_t)],
         "hga_route_launches": [C, ctypes.c_int, ctypes.POINTER(ctypes.c_int32)],
@@ -87,6 +110,17 @@ def load() -> ctypes.CDLL:
         "hga_route_groups_cached": [C, P, P, P, ctypes.c_int32, P, P, P, P],
         "hga_tier_plan": [C, P, P, P, P, P, P],
         "hga_tier_gather": [C, P, P, P, P, P, P, P],
+        "hga_packed_workspace_size": [K, ctypes.POINTER(ctypes.c_size_t)],
+        "hga_packed_attn_fwd": [K, P, P, P, P, P, P, P, P],
+        "hga_packed_attn_bwd": [K, P, P, P, P, P, P, P, P, P, P, P, P],
+        "hga_pages_workspace_size": [G, I, ctypes.POINTER(ctypes.c_size_t)],
+        "hga_pages_reserve": [G, I, P, P, P, P, P, P, P, P],
+        "hga_pages_write": [G, I, I, P, P, P, L, P, L, L, P, L, L, P, P, P, P, P, P],
+        "hga_paged_attn": [G, I, I, I, ctypes.c_float, P, P, L, P, P, P, P, P, P, P, P],
+        "hga_pages_fork": [G, I, P, P, P, P, P, P, P, P, P],
+        "hga_pages_free": [G, I, P, P, P, P, P, P],
+        "hga_pages_compact": [G, P, P, P, P, P, P, P, P],
+        "hga_pages_copy": [G, I, P, P, P, P, P, P],
         "hga_read_status": [P, P, ctypes.POINTER(ctypes.c_int32)],
         "hga_strerror": [ctypes.c_int],
         "hga_version": [],
@@ -226,6 +260,58 @@ def tier_plan(cfg, group_idx, used_groups, n_used, compact_idx, workspace, strea
 
 def tier_gather(cfg, k_hist, v_hist, used_groups, n_used, k_cache, v_cache, stream=0) -> None:
     _call("hga_tier_gather", ctypes.byref(cfg), k_hist, v_hist, used_groups, n_used, k_cache, v_cache, stream)
+
+
+def packed_workspace_size(cfg: PackedConfig) -> int:
+    out = ctypes.c_size_t(0)
+    _call("hga_packed_workspace_size", ctypes.byref(cfg), ctypes.byref(out))
+    return int(out.value)
+
+
+def packed_attn_fwd(cfg, q, k, v, cu_seqlens, o, lse, workspace, stream=0) -> None:
+    _call("hga_packed_attn_fwd", ctypes.byref(cfg), q, k, v, cu_seqlens, o, lse, workspace, stream)
+
+
+def packed_attn_bwd(cfg, q, k, v, cu_seqlens, o, lse, d_o, dq, dk, dv, workspace, stream=0) -> None:
+    _call("hga_packed_attn_bwd", ctypes.byref(cfg), q, k, v, cu_seqlens, o, lse, d_o, dq, dk, dv, workspace, stream)
+
+
+def pages_workspace_size(cfg: PagesConfig, Hq: int) -> int:
+    out = ctypes.c_size_t(0)
+    _call("hga_pages_workspace_size", ctypes.byref(cfg), int(Hq), ctypes.byref(out))
+    return int(out.value)
+
+
+def pages_reserve(cfg, n, rows, add, pos, table, seq_len, ref, workspace, stream=0) -> None:
+    _call("hga_pages_reserve", ctypes.byref(cfg), n, rows, add, pos, table, seq_len, ref, workspace, stream)
+
+
+def pages_write(cfg, layer, n, rows, pos, cu_new, total, k_new, k_stride_t, k_stride_h, v_new, v_stride_t, v_stride_h,
+                table, seq_len, k_pool, v_pool, workspace, stream=0) -> None:
+    _call("hga_pages_write", ctypes.byref(cfg), layer, n, rows, pos, cu_new, total, k_new, k_stride_t, k_stride_h,
+          v_new, v_stride_t, v_stride_h, table, seq_len, k_pool, v_pool, workspace, stream)
+
+
+def paged_attn(cfg, layer, n, Hq, softmax_scale, rows, q, q_stride_n, table, seq_len, k_pool, v_pool, o, lse,
+               workspace, stream=0) -> None:
+    _call("hga_paged_attn", ctypes.byref(cfg), layer, n, Hq, softmax_scale, rows, q, q_stride_n, table, seq_len,
+          k_pool, v_pool, o, lse, workspace, stream)
+
+
+def pages_fork(cfg, n, src, dst, table, seq_len, ref, k_pool, v_pool, workspace, stream=0) -> None:
+    _call("hga_pages_fork", ctypes.byref(cfg), n, src, dst, table, seq_len, ref, k_pool, v_pool, workspace, stream)
+
+
+def pages_free(cfg, n, rows, table, seq_len, ref, workspace, stream=0) -> None:
+    _call("hga_pages_free", ctypes.byref(cfg), n, rows, table, seq_len, ref, workspace, stream)
+
+
+def pages_compact(cfg, table, seq_len, ref, k_pool, v_pool, n_used, workspace, stream=0) -> None:
+    _call("hga_pages_compact", ctypes.byref(cfg), table, seq_len, ref, k_pool, v_pool, n_used, workspace, stream)
+
+
+def pages_copy(cfg, n, src, dst, k_pool, v_pool, workspace, stream=0) -> None:
+    _call("hga_pages_copy", ctypes.byref(cfg), n, src, dst, k_pool, v_pool, workspace, stream)
 
 
 def read_status(workspace, stream=0) -> int:

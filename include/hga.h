@@ -68,7 +68,7 @@
 extern "C" {
 #endif
 
-#define HGA_VERSION 3
+#define HGA_VERSION 4
 
 /* Symbols of the shared library (built with hidden default visibility). */
 #if defined(__GNUC__)
@@ -85,7 +85,8 @@ enum hga_status {
   HGA_ERR_CUDA = -4,        /* kernel launch failed                         */
   HGA_ERR_TIMEOUT = -5,     /* a device-side bounded wait expired           */
   HGA_ERR_WORKSPACE = -6,   /* workspace pointer missing                    */
-  HGA_ERR_TOO_LARGE = -7    /* beyond the fixed scratch of hga_attn_bwd_noalloc */
+  HGA_ERR_TOO_LARGE = -7,   /* beyond the fixed scratch of hga_attn_bwd_noalloc */
+  HGA_ERR_PAGES = -8        /* a paged cache has too few free pages         */
 };
 
 enum hga_dtype { HGA_F32 = 0, HGA_BF16 = 1 };
@@ -372,8 +373,134 @@ HGA_API int hga_route_groups_cached(const hga_config_t* cfg, const float* qb, co
                                     const int32_t* slot_of, int32_t cap_chunks, const float* gcache,
                                     int32_t* group_idx, void* workspace, void* stream);
 
+/* ---------------------------------------------------------------- dense readout: packed prompts
+ * The pages train with the routing and read out without it ("dense readout", review: the router
+ * is disabled for evaluation and generation): causal attention over the whole prompt.  Here over
+ * a packed batch: n_seqs sequences of any lengths (0 and 1 included), one after another in one
+ * tensor of `total` rows; sequence s is the rows cu_seqlens[s] .. cu_seqlens[s+1] - 1, and its
+ * token t attends its tokens 0..t:
+ *   o_t = sum_{u<=t} softmax_u(scale * q_t . k_u) v_u,   lse_t = log sum_{u<=t} exp(scale * q_t . k_u)
+ * Rows at or past cu_seqlens[n_seqs] belong to no sequence: their inputs are not used (whatever
+ * they hold) and their outputs are left as they were, or filled (flags).  What one sequence holds
+ * never reaches another one; a non-finite value of v reaches only the rows that attend it.  (In
+ * the backward pass a non-finite value may reach any gradient of its own sequence.)
+ *
+ * Types and layouts: q [total, Hq, D], k, v [total, Hkv, D] with D contiguous and the strides of
+ * the two outer dimensions given in elements, multiples of 16 bytes, at least D (0: contiguous
+ * [total, H, D]).  Slices of one fused projection and head-major tensors are such layouts.  o,
+ * d_o, dq [total, Hq, D] and dk, dv [total, Hkv, D] are contiguous; lse [Hq, total] float32.
+ * Query head h uses KV head h / (Hq / Hkv).  cu_seqlens: n_seqs + 1 int32 on the device, from 0,
+ * not decreasing, at most total; if it is not, no sequence is computed (all rows count as rows of
+ * no sequence) and HGA_ERR_ARG is recorded in the workspace status word.
+ * bf16 runs on the tensor cores, float32 on the CUDA cores in float32 arithmetic.
+ * total <= 2^31 - 1 - 256; total = 0 or n_seqs = 0 is a valid empty problem.
+ * Two calls that may overlap in time need two workspaces. */
+enum hga_packed_flags {
+  HGA_PACKED_FILL_TAIL = 1,   /* rows of no sequence: o, dq, dk, dv zeros, lse -inf */
+  HGA_PACKED_CLEAR_STATUS = 2 /* clear the status word first: a workspace need not be zeroed */
+};
+typedef struct hga_packed_config {
+  int32_t Hq, Hkv, D, n_seqs;
+  int64_t total;
+  int64_t q_stride_t, q_stride_h, k_stride_t, k_stride_h, v_stride_t, v_stride_h;
+  int32_t dtype, flags;
+  float softmax_scale;      /* 0: 1 / sqrt(D) */
+  int32_t reserved;         /* 0 */
+  int64_t wait_limit_ns;    /* as in hga_config_t */
+} hga_packed_config_t;
+
+/* Bytes of workspace of the two calls below (status word, work lists, delta rows). */
+HGA_API int hga_packed_workspace_size(const hga_packed_config_t* cfg, size_t* bytes_out);
+
+HGA_API int hga_packed_attn_fwd(const hga_packed_config_t* cfg, const void* q, const void* k, const void* v,
+                                const int32_t* cu_seqlens, void* o, float* lse, void* workspace, void* stream);
+
+/* Gradients for dL/do = d_o, given the forward's o and lse.  dk and dv of a KV head sum over its
+ * query heads.  Bitwise reproducible (no atomics on sums). */
+HGA_API int hga_packed_attn_bwd(const hga_packed_config_t* cfg, const void* q, const void* k, const void* v,
+                                const int32_t* cu_seqlens, const void* o, const float* lse, const void* d_o,
+                                void* dq, void* dk, void* dv, void* workspace, void* stream);
+
+/* ---------------------------------------------------------------- dense readout: paged K/V cache
+ * Generation without the router: every new token attends the exact K/V of its whole sequence, held
+ * in pages of `page` tokens that sequences take as they grow and may share.
+ *   k_pool, v_pool [n_layers, n_pages, Hkv, page, D], dtype; layer_stride and page_stride in
+ *       elements (0: contiguous; else multiples of 16 bytes), a page of a layer contiguous
+ *   table   int32 [max_seqs, max_pages]: page of each sequence row's tokens page * c ..
+ *   seq_len int32 [max_seqs]: tokens of each sequence row (0: the row is free)
+ *   ref     int32 [n_pages]: sequences that hold the page (0: the page is free)
+ * all in device memory, owned by the caller, seq_len and ref zero at first.  The calls read and
+ * change them on the stream: a decode step has no host synchronisation and can be captured into a
+ * CUDA graph.  A sequence's begun last page is never shared (hga_pages_fork copies it).
+ *
+ * A call that changes the integers (reserve, fork, free, copy) checks its whole list first: with
+ * any bad entry (a row outside [0, max_seqs), a row twice in the list, a length beyond
+ * max_pages * page, a page outside the pool, ...) it changes nothing and records HGA_ERR_ARG in the
+ * workspace status word; with too few free pages it changes nothing and records HGA_ERR_PAGES.
+ * Free pages are taken lowest id first, for the entries in their order.
+ * page: 16, 32, 64 or 128.  max_seqs <= 8192, n_pages <= 2^20, n (entries of a call) <= 8192.
+ * Calls on one cache or one workspace must not overlap in time. */
+typedef struct hga_pages_config {
+  int32_t n_layers, n_pages, page, Hkv, D;
+  int32_t max_seqs, max_pages, dtype;
+  int64_t layer_stride, page_stride;
+  int64_t wait_limit_ns;    /* as in hga_config_t */
+} hga_pages_config_t;
+
+/* Bytes of workspace of the calls below, for attention with up to Hq query heads.  Zero-filled once. */
+HGA_API int hga_pages_workspace_size(const hga_pages_config_t* cfg, int32_t Hq, size_t* bytes_out);
+
+/* Room for add[i] >= 0 new tokens behind sequence row rows[i]: takes the pages, adds to seq_len, and
+ * sets pos[i] to the position of the first new token.  When nothing is changed, pos[i] = -1.
+ *   rows, add, pos: int32 [n] on the device. */
+HGA_API int hga_pages_reserve(const hga_pages_config_t* cfg, int32_t n, const int32_t* rows, const int32_t* add,
+                              int32_t* pos, int32_t* table, int32_t* seq_len, int32_t* ref, void* workspace,
+                              void* stream);
+
+/* Writes new K/V rows of one layer into their pages: packed rows k_new, v_new [total, Hkv, D]
+ * (strides as in hga_packed_config), of which rows cu_new[i] .. cu_new[i+1] - 1 become the tokens
+ * pos[i] .. of sequence row rows[i].  Entries with pos < 0 are left out.  A token outside its
+ * sequence's length or with a page outside the pool is left out and HGA_ERR_ARG recorded. */
+HGA_API int hga_pages_write(const hga_pages_config_t* cfg, int32_t layer, int32_t n, const int32_t* rows,
+                            const int32_t* pos, const int32_t* cu_new, int64_t total, const void* k_new,
+                            int64_t k_stride_t, int64_t k_stride_h, const void* v_new, int64_t v_stride_t,
+                            int64_t v_stride_h, const int32_t* table, const int32_t* seq_len, void* k_pool,
+                            void* v_pool, void* workspace, void* stream);
+
+/* Attention of one new token per sequence: query i attends the seq_len[rows[i]] cached tokens of its
+ * row in `layer`.  A row may appear more than once; an empty row gives o = 0, lse = -inf.
+ *   q [n, Hq, D] (stride q_stride_n elements between tokens, 0: contiguous), o [n, Hq, D]
+ *   contiguous, lse [n, Hq] float32.  Hq a multiple of Hkv, Hq / Hkv <= 128.
+ * A bad row, length or page id records HGA_ERR_ARG; the tokens it concerns are left out. */
+HGA_API int hga_paged_attn(const hga_pages_config_t* cfg, int32_t layer, int32_t n, int32_t Hq, float softmax_scale,
+                           const int32_t* rows, const void* q, int64_t q_stride_n, const int32_t* table,
+                           const int32_t* seq_len, const void* k_pool, const void* v_pool, void* o, float* lse,
+                           void* workspace, void* stream);
+
+/* Branches: sequence row dst[i], which must be empty, becomes a copy of row src[i]: full pages are
+ * shared (ref + 1), a begun last page is copied in every layer into a free page.  One source may be
+ * forked many times in a call; a row that is a destination may not be a source. */
+HGA_API int hga_pages_fork(const hga_pages_config_t* cfg, int32_t n, const int32_t* src, const int32_t* dst,
+                           int32_t* table, int32_t* seq_len, int32_t* ref, void* k_pool, void* v_pool,
+                           void* workspace, void* stream);
+
+/* Ends sequences: their pages lose one reference each, their length becomes 0. */
+HGA_API int hga_pages_free(const hga_pages_config_t* cfg, int32_t n, const int32_t* rows, const int32_t* table,
+                           int32_t* seq_len, int32_t* ref, void* workspace, void* stream);
+
+/* Moves the pages in use to the front of the pool: with n_used pages in use, the i-th free page below
+ * n_used takes the content of the i-th used page at or above it, and tables and ref follow.
+ * *n_used (device int32) is the number of pages in use: pages at or past it are free. */
+HGA_API int hga_pages_compact(const hga_pages_config_t* cfg, int32_t* table, const int32_t* seq_len, int32_t* ref,
+                              void* k_pool, void* v_pool, int32_t* n_used, void* workspace, void* stream);
+
+/* Copies pages src[i] -> dst[i] in every layer (integers untouched).  No page may be twice a
+ * destination, or both source and destination. */
+HGA_API int hga_pages_copy(const hga_pages_config_t* cfg, int32_t n, const int32_t* src, const int32_t* dst,
+                           void* k_pool, void* v_pool, void* workspace, void* stream);
+
 /* Synchronises `stream`, copies the workspace status word to *status_out
- * (HGA_OK, HGA_ERR_TIMEOUT or HGA_ERR_ARG, see Workspace above) and clears it.  Returns HGA_ERR_CUDA if the
+ * (HGA_OK, HGA_ERR_TIMEOUT, HGA_ERR_ARG or HGA_ERR_PAGES, see Workspace above) and clears it.  Returns HGA_ERR_CUDA if the
  * copy itself fails. */
 HGA_API int hga_read_status(void* workspace, void* stream, int32_t* status_out);
 

@@ -1,0 +1,319 @@
+"""Causal attention over packed sequences (hga_packed_attn_fwd / _bwd) on the GPU against the float64
+reference, with the bounds of readout_ref."""
+import math
+
+import pytest
+import torch
+
+import readout_ref as R
+
+pytestmark = pytest.mark.gpu
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture(scope="module")
+def hga():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    import hierarchical_kv_routing_tok_b200 as H
+    H.load()
+    return H
+
+
+def ends(lens):
+    e = [0]
+    for n in lens:
+        e.append(e[-1] + n)
+    return torch.tensor(e, dtype=torch.int32, device="cuda")
+
+
+def rows(gen, T, heads, layout, dtype):
+    mk = lambda *s: torch.randn(*s, generator=gen, device="cuda").to(dtype)
+    if layout == "fused":
+        return list(mk(T, sum(heads), 128).split(heads, dim=1))
+    if layout == "heads":
+        return [mk(h, T, 128).transpose(0, 1) for h in heads]
+    if layout == "wide":                   # rows of a wider buffer, every tensor at another offset
+        return [mk(T, h + 2, 136)[:, 1:h + 1, 8:] for h in heads]
+    return [mk(T, h, 128) for h in heads]
+
+
+def make(lens, Hq, Hkv, dtype, layout="tokens", tail=0, seed=0):
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    T = sum(lens) + tail
+    q, k, v = rows(gen, T, [Hq, Hkv, Hkv], layout, dtype)
+    d_o = torch.randn(T, Hq, 128, generator=gen, device="cuda").to(dtype)
+    return q, k, v, d_o
+
+
+def run(hga, q, k, v, d_o, cu, scale=None):
+    leaves = [x.detach().requires_grad_() for x in (q, k, v)]
+    o, lse = hga.packed_attention(*leaves, cu, softmax_scale=scale)
+    dq, dk, dv = torch.autograd.grad(o, leaves, d_o)
+    return {"o": o.detach(), "lse": lse, "dq": dq, "dk": dk, "dv": dv}
+
+
+def check_all(got, ref):
+    for name in ("o", "lse", "dq", "dk", "dv"):
+        R.check(got[name], ref, name)
+
+
+LENS = [[1], [2, 1], [63, 64, 65], [127, 0, 128, 1, 129], [300], [0, 0, 5], [255, 257, 33], [513, 2, 700]]
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("lens", LENS, ids=str)
+def test_lengths(hga, dtype, lens):
+    q, k, v, d_o = make(lens, 8, 2, dtype)
+    check_all(run(hga, q, k, v, d_o, ends(lens)), R.packed(q, k, v, lens, d_o=d_o))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("Hq,Hkv", [(1, 1), (3, 3), (2, 1), (3, 1), (5, 1), (6, 1), (7, 1), (8, 1), (12, 1), (16, 1), (6, 2),
+                                    (32, 8), (40, 1)])
+def test_heads(hga, dtype, Hq, Hkv):
+    lens = [150, 1, 0, 77, 260]
+    q, k, v, d_o = make(lens, Hq, Hkv, dtype, seed=Hq)
+    check_all(run(hga, q, k, v, d_o, ends(lens)), R.packed(q, k, v, lens, d_o=d_o))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("layout", ["fused", "heads", "wide"])
+def test_layouts_and_tail(hga, dtype, layout):
+    lens = [129, 70, 3]
+    q, k, v, d_o = make(lens, 4, 2, dtype, layout, tail=9)
+    for x in (q, k, v, d_o):               # rows of no sequence: whatever they hold
+        x[sum(lens):] = math.nan
+    check_all(run(hga, q, k, v, d_o, ends(lens)),
+              R.packed(*(x.nan_to_num() for x in (q, k, v)), lens, d_o=d_o.nan_to_num()))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_long_ragged(hga, dtype):
+    lens = [2100, 40, 1025, 1, 333]
+    q, k, v, d_o = make(lens, 4, 1, dtype, "fused", tail=100)
+    check_all(run(hga, q, k, v, d_o, ends(lens)), R.packed(q, k, v, lens, d_o=d_o))
+
+
+def test_many_sequences(hga):
+    """More sequences than the plan keeps in shared memory."""
+    lens = [(7 * i) % 4 for i in range(5000)]
+    q, k, v, d_o = make(lens, 2, 1, BF16)
+    got = run(hga, q, k, v, d_o, ends(lens))
+    starts = ends(lens).tolist()
+    for i in list(range(40)) + [2500, 4094, 4095, 4096, 4097, 4998, 4999]:
+        a, b = starts[i], starts[i + 1]
+        if a < b:
+            ref = R.packed(q[a:b], k[a:b], v[a:b], [b - a], d_o=d_o[a:b])
+            for name in ("o", "dq", "dk", "dv"):
+                R.check(got[name][a:b], ref, name)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("scale", [0.02, 0.5])
+def test_scale(hga, dtype, scale):
+    lens = [200, 31]
+    q, k, v, d_o = make(lens, 4, 2, dtype, seed=3)
+    check_all(run(hga, q, k, v, d_o, ends(lens), scale), R.packed(q, k, v, lens, scale=scale, d_o=d_o))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_sequences_do_not_mix(hga, dtype):
+    """NaN and infinities in one sequence change no bit of the others."""
+    lens = [100, 61, 190, 5]
+    q, k, v, d_o = make(lens, 4, 2, dtype)
+    clean = run(hga, q, k, v, d_o, ends(lens))
+    for x, bad in ((q, math.nan), (k, math.inf), (v, -math.inf), (d_o, math.nan)):
+        x[100:161] = bad
+    got = run(hga, q, k, v, d_o, ends(lens))
+    keep = torch.ones(sum(lens), dtype=torch.bool, device="cuda")
+    keep[100:161] = False
+    for name in ("o", "dq", "dk", "dv"):
+        assert torch.equal(got[name][keep], clean[name][keep]), name
+    assert torch.equal(got["lse"][:, keep], clean["lse"][:, keep])
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("Hq,Hkv", [(4, 1), (2, 2)])
+@pytest.mark.parametrize("at", [0, 63, 130, 299])
+def test_non_finite_value_reaches_only_later_rows(hga, dtype, Hq, Hkv, at):
+    """v of token `at` not finite: rows before it keep their bits, rows from it on get inf / nan there."""
+    lens = [10, 300, 4]
+    q, k, v, _ = make(lens, Hq, Hkv, dtype, seed=at)
+    cu = ends(lens)
+    clean, lse0 = hga.packed_attention(q, k, v, cu)
+    v[10 + at, 0, 5] = math.inf
+    v[10 + at, 0, 77] = math.nan
+    o, lse = hga.packed_attention(q, k, v, cu)
+    assert torch.equal(lse, lse0)
+    hit = torch.zeros_like(o, dtype=torch.bool)
+    hit[10 + at:310, :Hq // Hkv, 5] = True
+    hit[10 + at:310, :Hq // Hkv, 77] = True
+    assert torch.equal(o[~hit], clean[~hit])
+    assert (o[10 + at:310, :Hq // Hkv, 5] == math.inf).all()
+    assert o[10 + at:310, :Hq // Hkv, 77].isnan().all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_extreme_scores(hga, dtype):
+    """Scores of several thousand: the running maximum keeps the sums finite."""
+    lens = [400]
+    q, k, v, d_o = make(lens, 2, 1, dtype)
+    q *= 64
+    k *= 32
+    o, lse = hga.packed_attention(q, k, v, ends(lens))
+    ref = R.packed(q, k, v, lens)
+    assert torch.isfinite(o).all()
+    R.check(o, ref, "o")
+    R.check(lse, ref, "lse")
+
+
+def test_given_outputs_keep_their_tail(hga):
+    """Outputs that the caller gives: rows of no sequence are left as they were."""
+    for dtype in (F32, BF16):
+        lens = [70, 0, 59]
+        q, k, v, d_o = make(lens, 4, 2, dtype, tail=21)
+        cu, n = ends(lens), sum(lens)
+        cfg = hga.make_packed_config(q, k, v, cu)
+        ws = torch.zeros(hga._capi.packed_workspace_size(cfg), dtype=torch.uint8, device="cuda")
+        o, dq, dk, dv = (torch.full(x.shape, 7.0, dtype=dtype, device="cuda") for x in (q, q, k, v))
+        lse = torch.full((4, n + 21), 7.0, device="cuda")
+        hga.packed_attn_fwd(cfg, q, k, v, cu, o, lse, ws)
+        hga.packed_attn_bwd(cfg, q, k, v, cu, o, lse, d_o, dq, dk, dv, ws)
+        ref = R.packed(q, k, v, lens, d_o=d_o)
+        for name, x in (("o", o), ("dq", dq), ("dk", dk), ("dv", dv)):
+            assert (x[n:] == 7).all(), name
+            x[n:] = 0
+            R.check(x, ref, name)
+        assert (lse[:, n:] == 7).all()
+        assert hga.read_status(ws) == 0
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("bad", [[1, 5, 9], [0, 6, 5], [0, 4, 99], [0, -3, 9]], ids=str)
+def test_invalid_bounds_are_recorded(hga, dtype, bad):
+    """A cu_seqlens that is not valid computes nothing and is recorded."""
+    q, k, v, d_o = make([9], 4, 2, dtype)
+    cu = torch.tensor(bad, dtype=torch.int32, device="cuda")
+    cfg = hga.make_packed_config(q, k, v, cu)
+    ws = torch.zeros(hga._capi.packed_workspace_size(cfg), dtype=torch.uint8, device="cuda")
+    o, lse = hga.packed_attn_fwd(cfg, q, k, v, cu, workspace=ws)
+    assert hga.read_status(ws) == hga._capi.HGA_ERR_ARG
+    assert not o.any() and (lse == -math.inf).all()
+    grads = hga.packed_attn_bwd(cfg, q, k, v, cu, o, lse, d_o, workspace=ws)
+    assert hga.read_status(ws) == hga._capi.HGA_ERR_ARG
+    assert not any(g.any() for g in grads)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_empty(hga, dtype):
+    for T, cu in ((0, [0]), (0, [0, 0, 0]), (6, [0]), (6, [0, 0])):
+        q, k, v, d_o = make([T], 4, 2, dtype)
+        got = run(hga, q, k, v, d_o, torch.tensor(cu, dtype=torch.int32, device="cuda"))
+        assert not got["o"].any() and not got["dq"].any() and not got["dk"].any() and not got["dv"].any()
+        assert (got["lse"] == -math.inf).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_reproducible_on_another_stream_and_in_a_graph(hga, dtype):
+    lens = [260, 1, 129, 64]
+    q, k, v, d_o = make(lens, 8, 2, dtype)
+    cu = ends(lens)
+    want = run(hga, q, k, v, d_o, cu)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = run(hga, q, k, v, d_o, cu)
+    torch.cuda.current_stream().wait_stream(side)
+    for n in want:
+        assert torch.equal(got[n], want[n]), n
+    cfg = hga.make_packed_config(q, k, v, cu)
+    ws = torch.zeros(hga._capi.packed_workspace_size(cfg), dtype=torch.uint8, device="cuda")
+    o, lse = torch.zeros_like(want["o"]), torch.zeros_like(want["lse"])
+    dq, dk, dv = (torch.zeros_like(want[n]) for n in ("dq", "dk", "dv"))
+
+    def step():
+        hga.packed_attn_fwd(cfg, q, k, v, cu, o, lse, ws)
+        hga.packed_attn_bwd(cfg, q, k, v, cu, o, lse, d_o, dq, dk, dv, ws)
+
+    with torch.cuda.stream(side):
+        step()
+    side.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step()
+    # the graph follows the tensors' content: other lengths, other values
+    lens2 = [3, 300, 0, 140]
+    cu.copy_(ends(lens2))
+    q.copy_(q.flip(0))
+    for _ in range(2):
+        for x in (o, dq, dk, dv):
+            x.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        ref = R.packed(q, k, v, lens2, d_o=d_o)
+        for n, x in (("o", o), ("dq", dq), ("dk", dk), ("dv", dv)):
+            R.check(x[:443], {n: ref[n][:443], "e_" + n: ref["e_" + n][:443]}, n)
+    assert hga.read_status(ws) == 0
+
+
+def test_gradient_against_differences(hga):
+    """Directional derivatives of the float32 forward: a central difference of step h of a loss computed from
+    float32 outputs is off by h^2 f'''/6 and by the outputs' error over h; with |direction| = 1, h = 0.05 the
+    float64 reference's own difference shows the first, the output bounds give the second."""
+    lens = [90, 33]
+    q, k, v, d_o = make(lens, 4, 2, F32)
+    cu = ends(lens)
+    got = run(hga, q, k, v, d_o, cu)
+    h = 0.05
+    for i, name in enumerate(("dq", "dk", "dv")):
+        d = torch.randn(got[name].shape, generator=torch.Generator(device="cuda").manual_seed(i), device="cuda")
+        d /= d.norm()
+        loss, exact, err = [], [], 0.0
+        for s in (1, -1):
+            args = [x + s * h * d if j == i else x for j, x in enumerate((q, k, v))]
+            ref = R.packed(*args, lens)
+            exact.append((ref["o"] * d_o.double()).sum().item())
+            err += (ref["e_o"] * d_o.double().abs()).sum().item()
+            loss.append((hga.packed_attention(*args, cu)[0].double() * d_o.double()).sum().item())
+        along = (got[name].double() * d.double()).sum().item()
+        truncation = abs((exact[0] - exact[1]) / (2 * h) - (R.packed(q, k, v, lens, d_o=d_o)[name] * d.double()).sum().item())
+        assert abs((loss[0] - loss[1]) / (2 * h) - along) <= truncation + err / (2 * h) + 1e-6
+
+
+def test_broadcast_gradient(hga):
+    """d_o of a sum (stride 0) and k, v that feed two calls: gradients add up."""
+    lens = [65, 20]
+    q, k, v, _ = make(lens, 4, 2, F32)
+    cu = ends(lens)
+    leaves = [x.detach().requires_grad_() for x in (q, k, v)]
+    o1, _ = hga.packed_attention(*leaves, cu)
+    o2, _ = hga.packed_attention(*leaves, cu)
+    (o1.sum() + o2.sum()).backward()
+    once = run(hga, q, k, v, torch.ones_like(q), cu)
+    for x, n in zip(leaves, ("dq", "dk", "dv")):
+        assert torch.equal(x.grad, 2 * once[n])
+
+
+def test_cuda_cores_agree(hga, monkeypatch):
+    """bf16 on the CUDA cores (asked for by the environment) keeps the same bounds."""
+    monkeypatch.setenv("HGA_ATTN_PATH", "cuda_cores")
+    lens = [130, 1, 77]
+    q, k, v, d_o = make(lens, 6, 2, BF16, "fused", tail=3)
+    check_all(run(hga, q, k, v, d_o, ends(lens)), R.packed(q, k, v, lens, d_o=d_o))
+
+
+def test_refusals(hga):
+    q, k, v, d_o = make([9], 4, 2, BF16)
+    cu = ends([9])
+    for args in ((q.half(), k.half(), v.half(), cu), (q, k.float(), v, cu), (q, k, v[:8], cu), (q[:, :3], k, v, cu),
+                 (q, k, v, cu.long()), (q, k, v, cu.cpu()), (q.cpu(), k, v, cu), (q[..., :64], k, v, cu),
+                 (q, k[:, :1].expand(-1, 2, -1), v, cu), (q.transpose(1, 2).contiguous().transpose(1, 2), k, v, cu)):
+        with pytest.raises((ValueError, RuntimeError)):
+            hga.packed_attention(*args)
+    cfg = hga.make_packed_config(q, k, v, cu)
+    with pytest.raises(ValueError):
+        hga.packed_attn_fwd(cfg, q, k, v, cu, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):
+        hga.packed_attn_fwd(cfg, q, k, v, cu, o=torch.empty_like(q))
