@@ -1,0 +1,70 @@
+// What the tensor-core kernels of packed attention share.
+//
+// A query tile has 128 rows = pk query heads of one KV head x 128 / pk tokens (row r: token r / pk, head
+// r % pk), so that short sequences and the causal diagonal waste few rows and each K/V tile serves pk
+// heads.  pk is the largest power of two, up to 8, that divides the query heads per KV head.
+#pragma once
+
+#include <cuda.h>
+
+#include "packed_common.cuh"
+#include "tc_common.cuh"
+
+namespace hga {
+namespace packed {
+
+constexpr int kBN = 128;                          // keys per tile
+constexpr uint32_t kHalfBytes = 128 * 128;        // one 64-dim half of a 128-row bf16 tile
+constexpr uint32_t kTileBytes = 2 * kHalfBytes;
+constexpr float kLog2eF = 1.4426950408889634f;
+
+inline int packed_heads(int G) { return G % 8 == 0 ? 8 : G % 4 == 0 ? 4 : G % 2 == 0 ? 2 : 1; }
+
+// bf16 map of a [total, H, 128] tensor with element strides; boxes of {64 dims, heads, tokens}, 128-byte
+// swizzle (a box lands as tokens x heads rows of 128 bytes).  Coordinates: (dim, head, token).
+bool make_map_packed(CUtensorMap* m, const void* base, int H, int64_t total, Strided s, int heads, int tokens);
+
+// Work unit u of a list of query tiles: units = head units of a tile, side by side, tiles heaviest first.
+// CTA c of G takes the units c, 2G-1-c, 2G+c, ... : a snake over the list, which deals out the long ones
+// evenly.
+__device__ __forceinline__ int64_t unit_of_cta(int k, int c, int G) {
+  const int64_t round = k >> 1;
+  return (k & 1) ? (2 * round + 2) * G - 1 - c : 2 * round * G + c;
+}
+
+// A bf16 tile (128 rows, two 64-dim halves) in shared memory made safe for a product in which some of its
+// rows meet zeros: rows at or past `rows` become zeros, and with `scan` so do values that are not finite.
+// Called by a warp; returns (warp-uniform) whether the scan found any.  0x7f80: an exponent of all ones.
+__device__ __forceinline__ bool clean_tile(uint32_t tile, int n_rows, uint32_t half_bytes, int rows, bool scan) {
+  const int lane = threadIdx.x & 31;
+  bool found = false;
+  const int chunks = n_rows * 8;                  // 16-byte pieces of a half
+  for (int h = 0; h < 2; ++h) {
+    const uint32_t base = tile + h * half_bytes;
+#pragma unroll 4
+    for (int x = (scan ? 0 : max(rows, 0) * 8) + lane; x < chunks; x += 32) {
+      const uint32_t a = base + x * 16;
+      uint32_t w[4] = {0u, 0u, 0u, 0u};
+      if ((x >> 3) < rows) {
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a));
+        uint32_t any = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) any |= ((w[e] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
+        if (any == 0) continue;
+        found = true;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const uint32_t m = ((w[e] & 0x7f807f80u) + 0x00800080u) & 0x80008000u;   // the halves not finite
+          if (m & 0x8000u) w[e] &= 0xffff0000u;
+          if (m & 0x80000000u) w[e] &= 0x0000ffffu;
+        }
+      }
+      asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]) : "memory");
+    }
+  }
+  tc::fence_proxy_async_smem();
+  return __any_sync(0xffffffffu, found);
+}
+
+}  // namespace packed
+}  // namespace hga

@@ -1,0 +1,464 @@
+// Causal attention over packed sequences, forward, on the tensor cores (tcgen05, bf16).
+//
+//   o_t = sum_{u<=t} softmax_u(scale q_t.k_u) v_u,   lse_t = log sum_{u<=t} exp(scale q_t.k_u)
+// with the online softmax: running maximum m and sum l per row, o rescaled when m grows by more than 2^8.
+//
+// Bound by the tensor pipe (two 128 x 128 x 128 products per tile) and, about as much, by the exponentials
+// (16 per clock and SM).  A unit is two query tiles of 128 rows (packed_tc.cuh) that share their K/V tiles of
+// 128 keys.  One CTA per SM walks the units of the work list, heaviest first; barriers and rings count tiles
+// across units, so the next unit's loads and first products run under the epilogue of the current one.
+// Warps: 0 loads Q and K, 2 loads V (TMA, rings of 3 and 2), 1 issues the products, 4-7 and 8-11 are the
+// softmax of the two tiles (thread = row), 3 cleans the V tiles that masked rows meet: on the causal
+// diagonal p = 0 meets values that the row does not attend, and 0 * inf is not 0.  Values there that are not
+// finite become 0 before the product, and the epilogue adds them to the rows that do attend them.
+// TMEM: S_0 S_1 O_0 O_1 (128 columns each); P_i as bf16 over the first half of S_i.  Issue order S_0 S_1 |
+// PV_0 S_0' PV_1 S_1' | ...: S_i(j+1) complete implies PV_i(j) complete, so no barrier guards the rescale.
+#include <cuda_bf16.h>
+
+#include "packed_tc.cuh"
+
+namespace hga {
+namespace packed {
+
+using namespace tc;
+
+namespace {
+
+constexpr float kRescaleThreshold = 8.f;   // log2 units
+constexpr int KS = 3, VS = 2;              // ring stages
+constexpr int kThreads = 384;
+
+struct FwdParams {
+  int Hq, Hkv, G, pk, tp;                  // tp: tokens per query tile, 128 / pk
+  int hu;                                  // head units: Hkv * G / pk
+  int64_t total;
+  float scale_log2;
+  const __nv_bfloat16* v;                  // for the values that are not finite
+  Strided vs;
+  __nv_bfloat16* o;
+  float* lse;
+  const Header* hdr;
+  const Tile* list;
+  int fill_tail;
+  int* status;
+  uint64_t wait_ns;
+};
+
+struct FwdSmem {
+  static constexpr uint32_t kQ = 0;
+  static constexpr uint32_t kK = kQ + 2 * kTileBytes;
+  static constexpr uint32_t kV = kK + KS * kTileBytes;
+  static constexpr uint32_t kBar = kV + VS * kTileBytes;
+  // q_full, q_empty, k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], v_clean[VS], s_full[2], p_full[2],
+  // o_full[2], mma_done
+  static constexpr int kNumBars = 2 + 2 * KS + 3 * VS + 6 + 1;
+  static constexpr uint32_t kMisc = kBar + 8 * kNumBars;        // TMEM address, abort, flags of 4 units
+  static constexpr uint32_t kBytes = kMisc + 32;
+};
+static_assert(FwdSmem::kBytes + 1024 <= 227 * 1024, "shared memory");
+
+struct Unit {
+  int start, len, t0, h0, kh;
+  int T[2], Tmax;                          // key tiles of the two query tiles
+};
+
+__device__ __forceinline__ bool load_unit(const FwdParams& p, int64_t n_units, int k, Unit* x) {
+  const int64_t u = unit_of_cta(k, blockIdx.x, gridDim.x);
+  if (u >= n_units) return false;
+  const int4 w = __ldg(reinterpret_cast<const int4*>(p.list) + u / p.hu);
+  const int hu = (int)(u % p.hu), per = p.G / p.pk;
+  x->start = w.x;
+  x->len = w.y;
+  x->t0 = w.z;
+  x->kh = hu / per;
+  x->h0 = x->kh * p.G + (hu % per) * p.pk;
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int64_t first = (int64_t)w.z + i * p.tp;
+    x->T[i] = first < w.y ? (int)((min(first + p.tp, (int64_t)w.y) - 1) / kBN) + 1 : 0;
+  }
+  x->Tmax = max(x->T[0], x->T[1]);
+  return true;
+}
+
+__global__ void __launch_bounds__(kThreads, 1)
+    packed_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                         const __grid_constant__ CUtensorMap tm_v, const FwdParams p) {
+  using L = FwdSmem;
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const uint32_t sbase = smem_u32(smem);
+  auto BAR = [&](int i) { return sbase + L::kBar + 8u * (uint32_t)i; };
+  const uint32_t q_full = BAR(0), q_empty = BAR(1);
+  auto k_full = [&](int s) { return BAR(2 + s); };
+  auto k_empty = [&](int s) { return BAR(2 + KS + s); };
+  auto v_full = [&](int s) { return BAR(2 + 2 * KS + s); };
+  auto v_empty = [&](int s) { return BAR(2 + 2 * KS + VS + s); };
+  auto v_clean = [&](int s) { return BAR(2 + 2 * KS + 2 * VS + s); };
+  auto s_full = [&](int i) { return BAR(2 + 2 * KS + 3 * VS + i); };
+  auto p_full = [&](int i) { return BAR(4 + 2 * KS + 3 * VS + i); };
+  auto o_full = [&](int i) { return BAR(6 + 2 * KS + 3 * VS + i); };
+  const uint32_t mma_done = BAR(8 + 2 * KS + 3 * VS);
+  uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
+  // whether a unit's diagonal tiles hold values that are not finite: unit k in slot k mod 4 (the cleaner is at
+  // most two units ahead of the epilogue, the V ring having two stages)
+  volatile int* not_finite = reinterpret_cast<volatile int*>(smem + L::kMisc + 8);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+  if (threadIdx.x == 0) {
+    mbar_init(q_full, 1);
+    mbar_init(q_empty, 1);
+    for (int s = 0; s < KS; ++s) {
+      mbar_init(k_full(s), 1);
+      mbar_init(k_empty(s), 1);
+    }
+    for (int s = 0; s < VS; ++s) {
+      mbar_init(v_full(s), 1);
+      mbar_init(v_empty(s), 1);
+      mbar_init(v_clean(s), 1);
+    }
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(s_full(i), 1);
+      mbar_init(p_full(i), 4);
+      mbar_init(o_full(i), 1);
+    }
+    mbar_init(mma_done, 1);
+    *abort_flag = 0;
+    mbar_fence_init();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(tmem_slot), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = *tmem_slot;
+  if (threadIdx.x == 0) pdl_trigger();
+  pdl_wait();                              // the work list comes from the kernel before
+  const int64_t n_units = (int64_t)p.hdr->n_tiles[0] * p.hu;
+  Unit x;
+
+  if (warp == 0 || warp == 2) {
+    // ======================= TMA producers: warp 0 Q and K, warp 2 V
+    if (lane == 0) {
+      const bool kv = warp == 2;
+      const CUtensorMap* map = kv ? &tm_v : &tm_k;
+      const int NS = kv ? VS : KS;
+      int64_t J = 0;
+      bool ok = true;
+      int loads = 0;
+      for (int k = 0; ok && load_unit(p, n_units, k, &x); ++k) {
+        if (!kv) {
+          if (k > 0 && !(ok = mbar_wait(q_empty, (k - 1) & 1, abort_flag, p.status, p.wait_ns))) break;
+          mbar_arrive_expect_tx(q_full, 2 * kTileBytes);
+          for (int i = 0; i < 2; ++i)
+            for (int h = 0; h < 2; ++h)
+              tma_load_3d(sbase + L::kQ + i * kTileBytes + h * kHalfBytes, &tm_q, 64 * h, x.h0,
+                          x.start + x.t0 + i * p.tp, q_full);
+          ++loads;
+        }
+        for (int j = 0; j < x.Tmax; ++j, ++J) {
+          const int s = (int)(J % NS);
+          const uint32_t full = kv ? v_full(s) : k_full(s), empty = kv ? v_empty(s) : k_empty(s);
+          if (!(ok = mbar_wait(empty, (uint32_t)((J / NS) & 1) ^ 1, abort_flag, p.status, p.wait_ns))) break;
+          mbar_arrive_expect_tx(full, kTileBytes);
+          const uint32_t dst = sbase + (kv ? L::kV : L::kK) + s * kTileBytes;
+          tma_load_3d(dst, map, 0, x.kh, x.start + j * kBN, full);
+          tma_load_3d(dst + kHalfBytes, map, 64, x.kh, x.start + j * kBN, full);
+        }
+      }
+      // every load of this warp has landed before the CTA may exit
+      for (int64_t j = J > NS ? J - NS : 0; j < J; ++j)
+        drain_wait(kv ? v_full((int)(j % NS)) : k_full((int)(j % NS)), (uint32_t)((j / NS) & 1), p.status);
+      if (loads) drain_wait(q_full, (loads - 1) & 1, p.status);
+    }
+    __syncwarp();
+  } else if (warp == 3) {
+    // ======================= cleaner of the V tiles at or behind the unit's first token
+    int64_t J = 0;
+    bool ok = true;
+    for (int k = 0; ok && load_unit(p, n_units, k, &x); ++k) {
+      const int jd = x.t0 / kBN;
+      bool any = false;
+      for (int j = 0; j < x.Tmax; ++j, ++J) {           // (every tile is waited for: a parity names only the
+        const int s = (int)(J % VS);                    // current phase and the one before)
+        ok = mbar_wait_w(v_full(s), (uint32_t)((J / VS) & 1), abort_flag, p.status, p.wait_ns);
+        if (!ok) break;
+        if (j < jd) continue;
+        any |= clean_tile(sbase + L::kV + s * kTileBytes, kBN, kHalfBytes, x.len - j * kBN, true);
+        if (lane == 0) not_finite[k & 3] = any;         // (the first query tile may end before the second)
+        __syncwarp();
+        if (lane == 0) mbar_arrive(v_clean(s));
+      }
+    }
+  } else if (warp == 1) {
+    // ======================= MMA issuer: the whole warp runs the loop, one elected lane issues
+    constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kBN, false);
+    constexpr uint32_t idesc_pv = idesc_bf16_f32(128, kD, true);
+    uint64_t qd[2][8], kd[8], vd[8];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) kmajor_descs(qd[i], sbase + L::kQ + i * kTileBytes, kHalfBytes, 1024);
+    int64_t J = 0;
+    int np[2] = {0, 0};                    // P tiles taken of each query tile
+    int cleaned[VS] = {0, 0};              // cleaned tiles taken from each V stage
+    bool ok = true;
+    for (int k = 0; ok && load_unit(p, n_units, k, &x); ++k) {
+      ok = mbar_wait_w(q_full, k & 1, abort_flag, p.status, p.wait_ns) &&
+           mbar_wait_w(k_full((int)(J % KS)), (uint32_t)((J / KS) & 1), abort_flag, p.status, p.wait_ns);
+      if (!ok) break;
+      tc_fence_after();
+      kmajor_descs(kd, sbase + L::kK + (int)(J % KS) * kTileBytes, kHalfBytes, 1024);
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        if (x.T[i] == 0) continue;
+#pragma unroll
+        for (int ks = 0; ks < 8; ++ks) mma_ss_w(tmem + i * 128, qd[i][ks], kd[ks], idesc_qk, ks > 0);
+        mma_commit_w(s_full(i));
+      }
+      mma_commit_w(k_empty((int)(J % KS)));
+      if (x.Tmax == 1) mma_commit_w(q_empty);
+      const int jd = x.t0 / kBN;
+      for (int j = 0; j < x.Tmax; ++j, ++J) {
+        const int s = (int)(J % VS);
+        if (j >= jd) {
+          ok = mbar_wait_w(v_clean(s), cleaned[s] & 1, abort_flag, p.status, p.wait_ns);
+          ++cleaned[s];
+        } else {
+          ok = mbar_wait_w(v_full(s), (uint32_t)((J / VS) & 1), abort_flag, p.status, p.wait_ns);
+        }
+        if (!ok) break;
+        tc_fence_after();
+        mnmajor_descs<8>(vd, sbase + L::kV + s * kTileBytes, kHalfBytes, 1024);
+        const int sn = (int)((J + 1) % KS);
+        bool have_k = false;               // the next K tile has landed
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+          if (j >= x.T[i]) continue;
+          ok = mbar_wait_w(p_full(i), np[i] & 1, abort_flag, p.status, p.wait_ns);
+          if (!ok) break;
+          ++np[i];
+          tc_fence_after();
+#pragma unroll
+          for (int ks = 0; ks < 8; ++ks)
+            mma_ts_w(tmem + 256 + i * 128, tmem + i * 128 + ks * 8, vd[ks], idesc_pv, (j > 0 || ks > 0));
+          if (j + 1 < x.T[i]) {
+            if (!have_k) {
+              ok = mbar_wait_w(k_full(sn), (uint32_t)(((J + 1) / KS) & 1), abort_flag, p.status, p.wait_ns);
+              if (!ok) break;
+              tc_fence_after();
+              kmajor_descs(kd, sbase + L::kK + sn * kTileBytes, kHalfBytes, 1024);
+              have_k = true;
+            }
+#pragma unroll
+            for (int ks = 0; ks < 8; ++ks) mma_ss_w(tmem + i * 128, qd[i][ks], kd[ks], idesc_qk, ks > 0);
+            mma_commit_w(s_full(i));
+          } else {
+            mma_commit_w(o_full(i));       // the last product of this query tile
+          }
+        }
+        if (!ok) break;
+        mma_commit_w(v_empty(s));
+        if (j + 1 < x.Tmax) {
+          mma_commit_w(k_empty(sn));
+          if (j + 2 == x.Tmax) mma_commit_w(q_empty);      // the unit's last S products are issued
+        }
+      }
+    }
+    mma_commit_w(mma_done);
+    drain_wait(mma_done, 0, p.status);
+  } else if (warp >= 4) {
+    // ======================= softmax and epilogue, one warpgroup per query tile
+    if (p.fill_tail) {
+      const int64_t worker = (int64_t)blockIdx.x * 256 + (threadIdx.x - 128), workers = (int64_t)gridDim.x * 256;
+      fill_tail_rows(p.o, p.Hq, p.hdr->end, p.total, worker, workers);
+      fill_tail_lse(p.lse, p.Hq, p.hdr->end, p.total, worker, workers);
+    }
+    const int i = (warp - 4) >> 2;
+    const int quarter = warp & 3;
+    const int r = quarter * 32 + lane;                  // row of the query tile = TMEM lane
+    const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
+    const uint32_t tS = tmem + lane_off + i * 128;
+    const uint32_t tO = tmem + lane_off + 256 + i * 128;
+    const bool o_v8 = (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;
+    int ns = 0, no = 0;                                 // S tiles, outputs taken
+    bool ok = true;
+    for (int k = 0; ok && load_unit(p, n_units, k, &x); ++k) {
+      const int T = x.T[i];
+      if (T == 0) continue;
+      const int t_pos = x.t0 + i * p.tp + r / p.pk;     // (rows past the sequence compute, and store nothing)
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < T; ++j, ++ns) {
+        ok = mbar_wait_w(s_full(i), ns & 1, abort_flag, p.status, p.wait_ns);
+        if (!ok) break;
+        tc_fence_after();
+        const int nvalid = t_pos - j * kBN + 1;         // keys of this tile that the row attends
+        // the whole 128-column row in one TMEM round trip
+        uint32_t v[128];
+        tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
+        tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
+        tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&v[64]));
+        tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&v[96]));
+        tmem_wait_ld();
+        if (nvalid < kBN) {
+#pragma unroll
+          for (int e = 0; e < kBN; ++e)
+            if (e >= nvalid) v[e] = __float_as_uint(-INFINITY);
+        }
+        float mx0 = -INFINITY, mx1 = -INFINITY;         // of the raw products (the scale is positive)
+#pragma unroll
+        for (int e = 0; e < kBN; e += 2) {
+          mx0 = fmaxf(mx0, __uint_as_float(v[e]));
+          mx1 = fmaxf(mx1, __uint_as_float(v[e + 1]));
+        }
+        const float mx = fmaxf(mx0, mx1) * p.scale_log2;
+        // move the reference only when the maximum grows by more than 2^8
+        const bool need = mx > m + kRescaleThreshold || (m == -INFINITY && mx > -INFINITY);
+        const float mnew = need ? mx : m;
+        const float alpha = need ? ex2(m - mnew) : 1.f; // m = -inf -> 0
+        if (j > 0 && __any_sync(0xffffffffu, need)) {
+#pragma unroll 1
+          for (int cc = 0; cc < 4; ++cc) {
+            uint32_t o[32];
+            tmem_ld32(tO + cc * 32, o);
+            tmem_wait_ld();
+#pragma unroll
+            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tmem_st32(tO + cc * 32, o);
+          }
+        }
+        l *= alpha;
+        m = mnew;
+        const float mref = (m == -INFINITY) ? 0.f : m;
+        // probabilities, their sum in float32, and as bf16 (the product's operand type) over S
+        float rs0 = 0.f, rs1 = 0.f;
+#pragma unroll
+        for (int cc = 0; cc < 4; ++cc) {
+          uint32_t pk[16];
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float p0 = ex2(fmaf(__uint_as_float(v[cc * 32 + e]), p.scale_log2, -mref));
+            const float p1 = ex2(fmaf(__uint_as_float(v[cc * 32 + e + 1]), p.scale_log2, -mref));
+            rs0 += p0;
+            rs1 += p1;
+            pk[e >> 1] = pack_bf16(p0, p1);
+          }
+          tmem_st16(tS + cc * 16, pk);
+        }
+        l += rs0 + rs1;
+        tmem_wait_st();
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(p_full(i));
+      }
+      if (ok) ok = mbar_wait_w(o_full(i), no & 1, abort_flag, p.status, p.wait_ns);
+      ++no;
+      if (!ok) break;
+      tc_fence_after();
+      const float inv = 1.f / l;
+      const bool store = t_pos < x.len;
+      const int h = x.h0 + r % p.pk;
+      const int64_t row = (int64_t)x.start + t_pos;
+      const bool fix = not_finite[k & 3] != 0;
+#pragma unroll 1
+      for (int cc = 0; cc < 4; ++cc) {
+        uint32_t v[32];
+        tmem_ld32(tO + cc * 32, v);
+        tmem_wait_ld();
+        if (fix && store) {
+          // values of the diagonal tiles that were set to 0 for the product: each adds itself
+          for (int u = x.t0 / kBN * kBN; u <= t_pos; ++u) {
+            const __nv_bfloat16* vr = p.v + ((int64_t)x.start + u) * p.vs.t + x.kh * p.vs.h + cc * 32;
+#pragma unroll
+            for (int e = 0; e < 32; ++e) {
+              const float y = __bfloat162float(vr[e]);
+              if (!isfinite(y)) v[e] = __float_as_uint(__uint_as_float(v[e]) + y);
+            }
+          }
+        }
+        uint32_t pk[16];
+#pragma unroll
+        for (int e = 0; e < 32; e += 2)
+          pk[e >> 1] = pack_bf16(__uint_as_float(v[e]) * inv, __uint_as_float(v[e + 1]) * inv);
+        if (store) {
+          // 64 bytes of the row: whole 32-byte sectors when o is 32-byte aligned
+          __nv_bfloat16* dst = p.o + (row * p.Hq + h) * kD + cc * 32;
+          if (o_v8) {
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 16 * y),
+                           "r"(pk[8 * y]), "r"(pk[8 * y + 1]), "r"(pk[8 * y + 2]), "r"(pk[8 * y + 3]),
+                           "r"(pk[8 * y + 4]), "r"(pk[8 * y + 5]), "r"(pk[8 * y + 6]), "r"(pk[8 * y + 7])
+                           : "memory");
+          } else {
+            uint4* d4 = reinterpret_cast<uint4*>(dst);
+#pragma unroll
+            for (int y = 0; y < 4; ++y) d4[y] = make_uint4(pk[4 * y], pk[4 * y + 1], pk[4 * y + 2], pk[4 * y + 3]);
+          }
+        }
+      }
+      if (store) p.lse[h * p.total + row] = (m + __log2f(l)) * 0.6931471805599453f;
+      tc_fence_before();
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+}  // namespace
+
+// ------------------------------------------------------------------------------------ host side
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                                  const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+bool make_map_packed(CUtensorMap* m, const void* base, int H, int64_t total, Strided s, int heads, int tokens) {
+  static EncodeTiledFn enc = nullptr;      // resolved once; the driver symbol never changes
+  if (!enc) {
+    void* ptr = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      return false;
+    enc = reinterpret_cast<EncodeTiledFn>(ptr);
+  }
+  cuuint64_t dims[3] = {(cuuint64_t)kD, (cuuint64_t)H, (cuuint64_t)total};
+  cuuint64_t strides[2] = {(cuuint64_t)s.h * 2, (cuuint64_t)s.t * 2};
+  cuuint32_t box[3] = {64, (cuuint32_t)heads, (cuuint32_t)tokens};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+int fwd_tile(int G) { return 256 / packed_heads(G); }
+
+cudaError_t launch_fwd_tc(const void* q, const void* k, const void* v, void* o, float* lse, const Header* hdr,
+                          const Tile* list, const Problem& p, cudaStream_t st) {
+  const int pk = packed_heads(p.G);
+  CUtensorMap mq, mk, mv;
+  if (!make_map_packed(&mq, q, p.Hq, p.total, p.q, pk, 128 / pk) || !make_map_packed(&mk, k, p.Hkv, p.total, p.k, 1, kBN) ||
+      !make_map_packed(&mv, v, p.Hkv, p.total, p.v, 1, kBN))
+    return cudaErrorInvalidValue;
+  FwdParams a{p.Hq, p.Hkv, p.G, pk, 128 / pk, p.Hkv * (p.G / pk), p.total, p.scale * kLog2eF,
+              static_cast<const __nv_bfloat16*>(v), p.v, static_cast<__nv_bfloat16*>(o), lse, hdr, list, p.fill_tail,
+              p.status, p.wait_ns};
+  int dev = 0, sms = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  if (e != cudaSuccess) return e;
+  const size_t smem = FwdSmem::kBytes + 1024;
+  e = cudaFuncSetAttribute(packed_fwd_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  const int64_t units = list_capacity(p.total, p.n_seqs, fwd_tile(p.G)) * a.hu;
+  return launch_dependent(packed_fwd_tc_kernel, dim3((unsigned)(units < 1 ? 1 : units < sms ? units : sms)),
+                          dim3(kThreads), smem, st, 1, mq, mk, mv, a);
+}
+
+}  // namespace packed
+}  // namespace hga

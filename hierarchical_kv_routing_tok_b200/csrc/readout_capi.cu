@@ -90,7 +90,7 @@ hga::packed::Problem packed_problem(const hga_packed_config_t* c, void* ws) {
 
 // Workspace: [status word | header | two work lists | delta rows].
 size_t list_bytes(const hga_packed_config_t* c) {
-  return round256((size_t)(hga::packed::list_capacity(c->total, c->n_seqs, hga::packed::kSimtTile) + 1) *
+  return round256((size_t)(hga::packed::list_capacity(c->total, c->n_seqs, hga::packed::kLeastTile) + 1) *
                   sizeof(hga::packed::Tile));
 }
 struct PackedWorkspace {
@@ -111,6 +111,9 @@ size_t packed_bytes(const hga_packed_config_t* c) {
   return hga::kStatusBytes + sizeof(hga::packed::Header) + 2 * list_bytes(c) +
          round256((size_t)c->Hq * c->total * sizeof(float));
 }
+
+// bf16 runs on the tensor cores.
+bool packed_tc(const hga_packed_config_t* c) { return c->dtype == HGA_BF16 && !force_cuda_cores(); }
 
 // ---------------------------------------------------------------- pages
 int check_pages(const hga_pages_config_t* c) {
@@ -197,10 +200,12 @@ int hga_packed_attn_fwd(const hga_packed_config_t* cfg, const void* q, const voi
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const hga::packed::Problem p = packed_problem(cfg, workspace);
   const PackedWorkspace w = packed_workspace(cfg, workspace);
-  const hga::packed::ListSpec list{hga::packed::kSimtTile, 0, w.lists[0]};
+  const bool tc = packed_tc(cfg);
+  const hga::packed::ListSpec list{tc ? hga::packed::fwd_tile(p.G) : hga::packed::kSimtTile, 0, w.lists[0]};
   cudaError_t e = hga::packed::launch_plan(cu_seqlens, cfg->n_seqs, cfg->total, 1, &list, w.hdr, p.status,
                                            (cfg->flags & HGA_PACKED_CLEAR_STATUS) != 0, st);
   if (e != cudaSuccess || cfg->total == 0) return from_cuda(e);
+  if (tc) return from_cuda(hga::packed::launch_fwd_tc(q, k, v, o, lse, w.hdr, w.lists[0], p, st));
   return from_cuda(
       hga::packed::launch_fwd_simt(cfg->dtype == HGA_BF16, q, k, v, o, lse, w.hdr, w.lists[0], p, st));
 }
