@@ -34,6 +34,12 @@ constexpr int kLeastTile = 16; // no kernel's tiles are shorter
 cudaError_t launch_fwd_tc(const void* q, const void* k, const void* v, void* o, float* lse, const Header* hdr,
                           const Tile* list, const Problem& p, cudaStream_t st);
 
+int dq_tile(int G);            // tokens per unit of the tensor-core dQ
+constexpr int kKeyTile = 128;  // keys per CTA of the tensor-core dK, dV
+cudaError_t launch_bwd_tc(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* d_o,
+                          float* delta, void* dq, void* dk, void* dv, const Header* hdr, const Tile* by_query,
+                          const Tile* by_key, const Problem& p, cudaStream_t st);
+
 // Rows of no sequence: zeros in a [total, H, 128] output, -inf in lse [H, total].  Called by every
 // thread of a grid of kernels that share the work by (worker, workers).
 template <typename T>

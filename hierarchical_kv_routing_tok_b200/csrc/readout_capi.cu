@@ -221,11 +221,16 @@ int hga_packed_attn_bwd(const hga_packed_config_t* cfg, const void* q, const voi
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const hga::packed::Problem p = packed_problem(cfg, workspace);
   const PackedWorkspace w = packed_workspace(cfg, workspace);
-  const hga::packed::ListSpec lists[2] = {{hga::packed::kSimtTile, 0, w.lists[0]},
-                                          {hga::packed::kSimtTile, 1, w.lists[1]}};
+  const bool tc = packed_tc(cfg);
+  const hga::packed::ListSpec lists[2] = {
+      {tc ? hga::packed::dq_tile(p.G) : hga::packed::kSimtTile, 0, w.lists[0]},
+      {tc ? hga::packed::kKeyTile : hga::packed::kSimtTile, 1, w.lists[1]}};
   cudaError_t e = hga::packed::launch_plan(cu_seqlens, cfg->n_seqs, cfg->total, 2, lists, w.hdr, p.status,
                                            (cfg->flags & HGA_PACKED_CLEAR_STATUS) != 0, st);
   if (e != cudaSuccess || cfg->total == 0) return from_cuda(e);
+  if (tc)
+    return from_cuda(hga::packed::launch_bwd_tc(q, k, v, o, lse, d_o, w.delta, dq, dk, dv, w.hdr, w.lists[0],
+                                                w.lists[1], p, st));
   return from_cuda(hga::packed::launch_bwd_simt(cfg->dtype == HGA_BF16, q, k, v, o, lse, d_o, w.delta, dq, dk, dv,
                                                 w.hdr, w.lists[0], w.lists[1], p, st));
 }
