@@ -17,39 +17,47 @@ from . import _capi as C
 from .api import _need, read_status
 
 _DT = {torch.float32: C.HGA_F32, torch.bfloat16: C.HGA_BF16}
+_STEP = {torch.float32: 4, torch.bfloat16: 8}          # elements of 16 bytes
 _D = 128
 
-
-def _on(t: torch.Tensor):
-    """Launches go to the current stream of the tensor's device, which must be the current device."""
-    if t.device.index == torch.cuda.current_device():
-        return contextlib.nullcontext()
-    return torch.cuda.device(t.device)
+# The checks below read each property of a tensor once, by the cheapest accessor: a decode step's kernel takes
+# about as long as a handful of Python calls.
+_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _stream(t: torch.Tensor) -> int:
-    return torch.cuda.current_stream(t.device).cuda_stream
+def _on(dev: int):
+    """Launches go to the current stream of the tensors' device, which must be the current device."""
+    return _NO_CONTEXT if torch._C._cuda_getDevice() == dev else torch.cuda.device(dev)
 
 
-def _same_device(dev: torch.device, **tensors) -> None:
-    for name, t in tensors.items():
-        if t.device != dev:
-            raise ValueError(f"{name} is on {t.device}, expected {dev}")
+_NO_CONTEXT = contextlib.nullcontext()
 
 
-def _strides(t: torch.Tensor, name: str, T: int, H: int, dtype) -> tuple[int, int]:
+def _flat(t: torch.Tensor, name: str, shape, dtype, dev: int) -> None:
+    """t is contiguous, of this shape and type, on CUDA device dev."""
+    if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or t.shape != shape:
+        if dev < 0 or not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.get_device() != dev:
+            raise ValueError(f"{name} is on {t.device}, expected cuda:{dev}")
+        _need(t, name, shape, dtype)
+
+
+def _strides(t: torch.Tensor, name: str, T: int, H: int, dtype, dev: int) -> tuple[int, int]:
     """Element strides of [T, H, 128] for the library: rows of contiguous elements, 16-byte steps."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
-    if tuple(t.shape) != (T, H, _D):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(T, H, _D)}")
-    if t.dtype != dtype:
+    if t.get_device() != dev or dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor" if not t.is_cuda else f"{name} is on {t.device}, expected cuda:{dev}")
+    if t.dtype is not dtype:
         raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.shape != (T, H, _D):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(T, H, _D)}")
     st, sh, sd = t.stride()
-    step = 16 // t.element_size()
-    st = st if T > 1 else H * _D          # (the stride of a single element means nothing)
-    sh = sh if H > 1 else _D
-    if T and (sd != 1 or st < _D or sh < _D or st % step or sh % step or t.data_ptr() % 16):
+    if T <= 1:                            # (the stride of a single element means nothing)
+        st = H * _D
+    if H == 1:
+        sh = _D
+    step = _STEP[dtype]
+    if T and (sd != 1 or st < _D or sh < _D or st % step or sh % step or t.data_ptr() & 15):
         raise ValueError(f"{name}: rows of {_D} contiguous elements at 16-byte steps are needed, got strides "
                          f"{tuple(t.stride())}")
     return st, sh
@@ -59,89 +67,34 @@ def make_packed_config(q, k, v, cu_seqlens, softmax_scale: float | None = None, 
                        wait_limit_ns: int = 0) -> C.PackedConfig:
     """Configuration of packed attention from q [total, Hq, 128], k, v [total, Hkv, 128] and cu_seqlens
     [n_seqs + 1] int32; checks the tensors.  q, k and v may be strided (rows contiguous, 16-byte steps)."""
-    if q.dtype not in _DT:
-        raise ValueError(f"unsupported dtype {q.dtype}")
+    dtype, dev = q.dtype, q.get_device()
+    if dtype not in _DT:
+        raise ValueError(f"unsupported dtype {dtype}")
     if q.dim() != 3 or k.dim() != 3:
         raise ValueError("q and k must be [total, heads, 128]")
-    T, Hq = q.shape[0], q.shape[1]
+    T, Hq, _ = q.shape
     Hkv = k.shape[1]
     if Hkv < 1 or Hq < 1 or Hq % Hkv:
         raise ValueError(f"{Hq} query heads cannot share {Hkv} KV heads")
-    qs, ks, vs = (_strides(t, n, T, h, q.dtype) for t, n, h in ((q, "q", Hq), (k, "k", Hkv), (v, "v", Hkv)))
-    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 1:
+    qt, qh = _strides(q, "q", T, Hq, dtype, dev)
+    kt, kh = _strides(k, "k", T, Hkv, dtype, dev)
+    vt, vh = _strides(v, "v", T, Hkv, dtype, dev)
+    if cu_seqlens.dim() != 1 or cu_seqlens.shape[0] < 1:
         raise ValueError("cu_seqlens must be [n_seqs + 1]")
-    _need(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32)
-    _same_device(q.device, k=k, v=v, cu_seqlens=cu_seqlens)
-    return C.PackedConfig(Hq, Hkv, _D, cu_seqlens.numel() - 1, T, *qs, *ks, *vs, _DT[q.dtype], flags,
+    _flat(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32, dev)
+    return C.PackedConfig(Hq, Hkv, _D, cu_seqlens.shape[0] - 1, T, qt, qh, kt, kh, vt, vh, _DT[dtype], flags,
                           float(softmax_scale or 0.0), 0, wait_limit_ns)
 
 
-def _packed_workspace(cfg, device) -> torch.Tensor:
-    """Not zeroed: for calls with HGA_PACKED_CLEAR_STATUS."""
-    return torch.empty(C.packed_workspace_size(cfg), dtype=torch.uint8, device=device)
-
-
-def _check_packed_workspace(cfg, workspace, q) -> None:
+def _workspace(cfg, workspace, dev: int, flags: int):
+    """The caller's workspace (zeroed once, checked), or a new one whose status the call clears."""
     n = C.packed_workspace_size(cfg)
-    if not workspace.is_cuda or workspace.dtype != torch.uint8 or not workspace.is_contiguous() \
+    if workspace is None:
+        return torch.empty(n, dtype=torch.uint8, device=dev), flags | C.HGA_PACKED_CLEAR_STATUS
+    if workspace.get_device() != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous() \
             or workspace.numel() < n:
-        raise ValueError(f"workspace must be a contiguous CUDA uint8 tensor of at least {n} bytes")
-    _same_device(q.device, workspace=workspace)
-
-
-def packed_attn_fwd(cfg, q, k, v, cu_seqlens, o=None, lse=None, workspace=None):
-    """Forward.  Rows of no sequence are left as they were in a given o / lse, and hold zeros / -inf in a new
-    one.  workspace: at least ``_capi.packed_workspace_size(cfg)`` bytes, zeroed once (``read_status``
-    tells of a cu_seqlens that is not valid); without one the call makes its own."""
-    T, Hq = q.shape[0], q.shape[1]
-    flags = cfg.flags
-    if o is None and lse is None:
-        flags |= C.HGA_PACKED_FILL_TAIL
-        o = torch.empty(T, Hq, _D, dtype=q.dtype, device=q.device)
-        lse = torch.empty(Hq, T, dtype=torch.float32, device=q.device)
-    elif o is None or lse is None:
-        raise ValueError("o and lse are given together or not at all")
-    else:
-        _need(o, "o", (T, Hq, _D), q.dtype)
-        _need(lse, "lse", (Hq, T), torch.float32)
-        _same_device(q.device, o=o, lse=lse)
-    if workspace is None:
-        flags |= C.HGA_PACKED_CLEAR_STATUS
-        workspace = _packed_workspace(cfg, q.device)
-    else:
-        _check_packed_workspace(cfg, workspace, q)
-    with _on(q):
-        C.packed_attn_fwd(_with_flags(cfg, flags), q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(),
-                          o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), _stream(q))
-    return o, lse
-
-
-def packed_attn_bwd(cfg, q, k, v, cu_seqlens, o, lse, d_o, dq=None, dk=None, dv=None, workspace=None):
-    """Gradients (contiguous) for d_o, from the forward's o and lse.  Rows of no sequence: as in
-    ``packed_attn_fwd`` (zeros in new gradients)."""
-    T, Hq, Hkv = q.shape[0], q.shape[1], k.shape[1]
-    flags = cfg.flags
-    if dq is None and dk is None and dv is None:
-        flags |= C.HGA_PACKED_FILL_TAIL
-        dq = torch.empty(T, Hq, _D, dtype=q.dtype, device=q.device)
-        dk = torch.empty(T, Hkv, _D, dtype=q.dtype, device=q.device)
-        dv = torch.empty(T, Hkv, _D, dtype=q.dtype, device=q.device)
-    elif dq is None or dk is None or dv is None:
-        raise ValueError("dq, dk and dv are given together or not at all")
-    for t, n, h in ((o, "o", Hq), (d_o, "d_o", Hq), (dq, "dq", Hq), (dk, "dk", Hkv), (dv, "dv", Hkv)):
-        _need(t, n, (T, h, _D), q.dtype)
-    _need(lse, "lse", (Hq, T), torch.float32)
-    _same_device(q.device, k=k, v=v, cu_seqlens=cu_seqlens, o=o, lse=lse, d_o=d_o, dq=dq, dk=dk, dv=dv)
-    if workspace is None:
-        flags |= C.HGA_PACKED_CLEAR_STATUS
-        workspace = _packed_workspace(cfg, q.device)
-    else:
-        _check_packed_workspace(cfg, workspace, q)
-    with _on(q):
-        C.packed_attn_bwd(_with_flags(cfg, flags), q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(),
-                          o.data_ptr(), lse.data_ptr(), d_o.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-                          workspace.data_ptr(), _stream(q))
-    return dq, dk, dv
+        raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {n} bytes on cuda:{dev}")
+    return workspace, flags
 
 
 def _with_flags(cfg, flags: int):
@@ -152,6 +105,52 @@ def _with_flags(cfg, flags: int):
     return out
 
 
+def packed_attn_fwd(cfg, q, k, v, cu_seqlens, o=None, lse=None, workspace=None):
+    """Forward.  Rows of no sequence are left as they were in a given o / lse, and hold zeros / -inf in a new
+    one.  workspace: at least ``_capi.packed_workspace_size(cfg)`` bytes, zeroed once (``read_status``
+    tells of a cu_seqlens that is not valid); without one the call makes its own."""
+    T, Hq, dev, flags = cfg.total, cfg.Hq, q.get_device(), cfg.flags
+    if o is None and lse is None:
+        flags |= C.HGA_PACKED_FILL_TAIL
+        o = torch.empty((T, Hq, _D), dtype=q.dtype, device=q.device)
+        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
+    elif o is None or lse is None:
+        raise ValueError("o and lse are given together or not at all")
+    else:
+        _flat(o, "o", (T, Hq, _D), q.dtype, dev)
+        _flat(lse, "lse", (Hq, T), torch.float32, dev)
+    workspace, flags = _workspace(cfg, workspace, dev, flags)
+    with _on(dev):
+        C.packed_attn_fwd(_with_flags(cfg, flags), q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(),
+                          o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), _raw_stream(dev))
+    return o, lse
+
+
+def packed_attn_bwd(cfg, q, k, v, cu_seqlens, o, lse, d_o, dq=None, dk=None, dv=None, workspace=None):
+    """Gradients (contiguous) for d_o, from the forward's o and lse.  Rows of no sequence: as in
+    ``packed_attn_fwd`` (zeros in new gradients)."""
+    T, Hq, Hkv, dev, flags = cfg.total, cfg.Hq, cfg.Hkv, q.get_device(), cfg.flags
+    if dq is None and dk is None and dv is None:
+        flags |= C.HGA_PACKED_FILL_TAIL
+        dq = torch.empty((T, Hq, _D), dtype=q.dtype, device=q.device)
+        dk = torch.empty((T, Hkv, _D), dtype=q.dtype, device=q.device)
+        dv = torch.empty((T, Hkv, _D), dtype=q.dtype, device=q.device)
+    elif dq is None or dk is None or dv is None:
+        raise ValueError("dq, dk and dv are given together or not at all")
+    else:
+        for t, n, h in ((dq, "dq", Hq), (dk, "dk", Hkv), (dv, "dv", Hkv)):
+            _flat(t, n, (T, h, _D), q.dtype, dev)
+    _flat(o, "o", (T, Hq, _D), q.dtype, dev)
+    _flat(d_o, "d_o", (T, Hq, _D), q.dtype, dev)
+    _flat(lse, "lse", (Hq, T), torch.float32, dev)
+    workspace, flags = _workspace(cfg, workspace, dev, flags)
+    with _on(dev):
+        C.packed_attn_bwd(_with_flags(cfg, flags), q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(),
+                          o.data_ptr(), lse.data_ptr(), d_o.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
+                          workspace.data_ptr(), _raw_stream(dev))
+    return dq, dk, dv
+
+
 class _PackedAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, cu_seqlens, softmax_scale):
@@ -160,14 +159,17 @@ class _PackedAttention(torch.autograd.Function):
         ctx.cfg = cfg
         ctx.save_for_backward(q, k, v, cu_seqlens, o, lse)
         ctx.mark_non_differentiable(lse)
+        ctx.set_materialize_grads(False)
         return o, lse
 
     @staticmethod
     @torch.autograd.function.once_differentiable
     def backward(ctx, d_o, _dlse):
+        if d_o is None:
+            return None, None, None, None, None
         q, k, v, cu_seqlens, o, lse = ctx.saved_tensors
         d_o = d_o.contiguous()
-        if d_o.data_ptr() % 16:
+        if d_o.data_ptr() & 15:
             d_o = d_o.clone()
         dq, dk, dv = packed_attn_bwd(ctx.cfg, q, k, v, cu_seqlens, o, lse, d_o)
         return dq, dk, dv, None, None
@@ -181,7 +183,9 @@ def packed_attention(q, k, v, cu_seqlens, softmax_scale: float | None = None):
 
     q, k and v may be strided (slices of a fused projection, transposed head-major tensors); float32 or
     bfloat16."""
-    return _PackedAttention.apply(q, k, v, cu_seqlens, softmax_scale)
+    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
+        return _PackedAttention.apply(q, k, v, cu_seqlens, softmax_scale)
+    return packed_attn_fwd(make_packed_config(q, k, v, cu_seqlens, softmax_scale), q, k, v, cu_seqlens)
 
 
 class PagedKVCache:
@@ -209,10 +213,12 @@ class PagedKVCache:
                 raise ValueError(f"{name} must be a CUDA tensor")
             if P and L and not t[0, 0].is_contiguous():
                 raise ValueError(f"{name}: a page of a layer must be contiguous")
-        _need(page_table, "page_table", page_table.shape, torch.int32)
-        _need(seq_len, "seq_len", (page_table.shape[0],), torch.int32)
-        _need(ref_count, "ref_count", (P,), torch.int32)
-        _same_device(k_pool.device, v_pool=v_pool, page_table=page_table, seq_len=seq_len, ref_count=ref_count)
+        dev = k_pool.get_device()
+        if v_pool.get_device() != dev:
+            raise ValueError(f"v_pool is on {v_pool.device}, expected {k_pool.device}")
+        _flat(page_table, "page_table", page_table.shape, torch.int32, dev)
+        _flat(seq_len, "seq_len", (page_table.shape[0],), torch.int32, dev)
+        _flat(ref_count, "ref_count", (P,), torch.int32, dev)
         data = Hkv * page * D
         page_stride = k_pool.stride(1) if P > 1 else data
         layer_stride = k_pool.stride(0) if L > 1 else 0
@@ -221,6 +227,7 @@ class PagedKVCache:
         self.k_pool, self.v_pool = k_pool, v_pool
         self.page_table, self.seq_len, self.ref_count = page_table, seq_len, ref_count
         self.device, self.dtype, self.max_q_heads = k_pool.device, k_pool.dtype, max_q_heads
+        self._dev = dev
         self.workspace = torch.zeros(C.pages_workspace_size(self.cfg, max_q_heads), dtype=torch.uint8,
                                      device=k_pool.device)
         self._ints = (page_table.data_ptr(), seq_len.data_ptr(), ref_count.data_ptr())
@@ -235,15 +242,13 @@ class PagedKVCache:
                 for s in ((max_seqs, -(-max_seq_len // page)), (max_seqs,), (n_pages,))]
         return cls(*pools, *ints, **kw)
 
-    def _entries(self, **lists) -> int:
-        n = None
-        for name, t in lists.items():
-            if t.dim() != 1 or (n is not None and t.shape[0] != n):
-                raise ValueError(f"{name} has shape {tuple(t.shape)}, expected ({'n' if n is None else n},)")
-            n = t.shape[0]
-            _need(t, name, (n,), torch.int32)
-        _same_device(self.device, **lists)
-        return n
+    def _entries(self, t, name: str, n: int = -1) -> int:
+        """An int32 list of n entries (of any number: -1); returns their number."""
+        shape = t.shape
+        if len(shape) != 1 or (n >= 0 and shape[0] != n):
+            raise ValueError(f"{name} has shape {tuple(shape)}, expected ({n if n >= 0 else 'n'},)")
+        _flat(t, name, shape, torch.int32, self._dev)
+        return shape[0]
 
     def _layer(self, layer: int) -> int:
         if not 0 <= layer < self.cfg.n_layers:
@@ -251,13 +256,14 @@ class PagedKVCache:
         return layer
 
     def _call(self, fn, *args) -> None:
-        with _on(self.k_pool):
-            fn(self.cfg, *args, self._ws, _stream(self.k_pool))
+        with _on(self._dev):
+            fn(self.cfg, *args, self._ws, _raw_stream(self._dev))
 
     def reserve(self, rows, add) -> torch.Tensor:
         """Room for add[i] tokens behind sequence row rows[i] (int32 [n]): takes the pages, grows seq_len.
         Returns pos [n], the position of each entry's first new token (-1: nothing was changed)."""
-        n = self._entries(rows=rows, add=add)
+        n = self._entries(rows, "rows")
+        self._entries(add, "add", n)
         pos = torch.empty_like(rows)
         self._call(C.pages_reserve, n, rows.data_ptr(), add.data_ptr(), pos.data_ptr(), *self._ints)
         return pos
@@ -265,32 +271,34 @@ class PagedKVCache:
     def write(self, layer: int, k, v, cu_new, rows, pos) -> None:
         """K/V rows of one layer into reserved places: rows cu_new[i] .. cu_new[i+1] - 1 of k, v [total, Hkv,
         128] (may be strided) become the tokens pos[i] .. of sequence row rows[i]."""
-        n = self._entries(rows=rows, pos=pos)
-        T = k.shape[0]
-        ks, vs = (_strides(t, name, T, self.cfg.Hkv, self.dtype) for t, name in ((k, "k"), (v, "v")))
-        _need(cu_new, "cu_new", (n + 1,), torch.int32)
-        _same_device(self.device, k=k, v=v, cu_new=cu_new)
+        n = self._entries(rows, "rows")
+        self._entries(pos, "pos", n)
+        self._entries(cu_new, "cu_new", n + 1)
+        T, Hkv = k.shape[0], self.cfg.Hkv
+        kt, kh = _strides(k, "k", T, Hkv, self.dtype, self._dev)
+        vt, vh = _strides(v, "v", T, Hkv, self.dtype, self._dev)
         self._call(C.pages_write, self._layer(layer), n, rows.data_ptr(), pos.data_ptr(), cu_new.data_ptr(), T,
-                   k.data_ptr(), *ks, v.data_ptr(), *vs, *self._ints[:2], *self._pools)
+                   k.data_ptr(), kt, kh, v.data_ptr(), vt, vh, *self._ints[:2], *self._pools)
 
     def attend(self, layer: int, q, rows, softmax_scale: float | None = None, o=None, lse=None):
         """Attention of one new token per sequence: q [n, Hq, 128] (rows may be strided), query i over all
         cached tokens of sequence row rows[i].  Returns (o [n, Hq, 128], lse [n, Hq] float32); an empty row
         gives zeros and -inf."""
-        n = self._entries(rows=rows)
+        n = self._entries(rows, "rows")
         if q.dim() != 3 or q.shape[1] > self.max_q_heads:
             raise ValueError(f"q must be [n, heads, 128] with at most {self.max_q_heads} heads")
         Hq = q.shape[1]
-        sn, sh = _strides(q, "q", n, Hq, self.dtype)
+        sn, sh = _strides(q, "q", n, Hq, self.dtype, self._dev)
         if sh != _D or sn < Hq * _D:
             raise ValueError(f"q: the heads of a token must be contiguous, got strides {tuple(q.stride())}")
         if o is None:
-            o = torch.empty(n, Hq, _D, dtype=q.dtype, device=q.device)
+            o = torch.empty((n, Hq, _D), dtype=self.dtype, device=self.device)
+        else:
+            _flat(o, "o", (n, Hq, _D), self.dtype, self._dev)
         if lse is None:
-            lse = torch.empty(n, Hq, dtype=torch.float32, device=q.device)
-        _need(o, "o", (n, Hq, _D), self.dtype)
-        _need(lse, "lse", (n, Hq), torch.float32)
-        _same_device(self.device, q=q, o=o, lse=lse)
+            lse = torch.empty((n, Hq), dtype=torch.float32, device=self.device)
+        else:
+            _flat(lse, "lse", (n, Hq), torch.float32, self._dev)
         self._call(C.paged_attn, self._layer(layer), n, Hq, float(softmax_scale or 0.0), rows.data_ptr(),
                    q.data_ptr(), sn, *self._ints[:2], *self._pools, o.data_ptr(), lse.data_ptr())
         return o, lse
@@ -298,12 +306,13 @@ class PagedKVCache:
     def fork(self, src, dst) -> None:
         """Empty sequence rows dst[i] become copies of rows src[i]: full pages are shared, a begun last page is
         copied in every layer."""
-        n = self._entries(src=src, dst=dst)
+        n = self._entries(src, "src")
+        self._entries(dst, "dst", n)
         self._call(C.pages_fork, n, src.data_ptr(), dst.data_ptr(), *self._ints, *self._pools)
 
     def free(self, rows) -> None:
         """Ends sequences: length 0, and their pages lose a reference."""
-        n = self._entries(rows=rows)
+        n = self._entries(rows, "rows")
         self._call(C.pages_free, n, rows.data_ptr(), *self._ints)
 
     def compact(self) -> torch.Tensor:
@@ -314,11 +323,12 @@ class PagedKVCache:
 
     def copy_pages(self, src, dst) -> None:
         """Copies the K/V of pages src[i] to pages dst[i] in every layer; table and counts stay."""
-        n = self._entries(src=src, dst=dst)
+        n = self._entries(src, "src")
+        self._entries(dst, "dst", n)
         self._call(C.pages_copy, n, src.data_ptr(), dst.data_ptr(), *self._pools)
 
     def status(self) -> int:
         """Status of the calls since the last one (synchronises): HGA_OK, HGA_ERR_ARG, HGA_ERR_PAGES or
         HGA_ERR_TIMEOUT."""
-        with _on(self.k_pool):
+        with _on(self._dev):
             return read_status(self.workspace)
