@@ -86,11 +86,12 @@ def make_packed_config(q, k, v, cu_seqlens, softmax_scale: float | None = None, 
                           float(softmax_scale or 0.0), 0, wait_limit_ns)
 
 
-def _workspace(cfg, workspace, dev: int, flags: int):
+def _workspace(cfg, workspace, q, flags: int):
     """The caller's workspace (zeroed once, checked), or a new one whose status the call clears."""
     n = C.packed_workspace_size(cfg)
     if workspace is None:
-        return torch.empty(n, dtype=torch.uint8, device=dev), flags | C.HGA_PACKED_CLEAR_STATUS
+        return q.new_empty(n, dtype=torch.uint8), flags | C.HGA_PACKED_CLEAR_STATUS
+    dev = q.get_device()
     if workspace.get_device() != dev or workspace.dtype != torch.uint8 or not workspace.is_contiguous() \
             or workspace.numel() < n:
         raise ValueError(f"workspace must be a contiguous uint8 tensor of at least {n} bytes on cuda:{dev}")
@@ -112,14 +113,14 @@ def packed_attn_fwd(cfg, q, k, v, cu_seqlens, o=None, lse=None, workspace=None):
     T, Hq, dev, flags = cfg.total, cfg.Hq, q.get_device(), cfg.flags
     if o is None and lse is None:
         flags |= C.HGA_PACKED_FILL_TAIL
-        o = torch.empty((T, Hq, _D), dtype=q.dtype, device=q.device)
-        lse = torch.empty((Hq, T), dtype=torch.float32, device=q.device)
+        o = q.new_empty((T, Hq, _D))
+        lse = q.new_empty((Hq, T), dtype=torch.float32)
     elif o is None or lse is None:
         raise ValueError("o and lse are given together or not at all")
     else:
         _flat(o, "o", (T, Hq, _D), q.dtype, dev)
         _flat(lse, "lse", (Hq, T), torch.float32, dev)
-    workspace, flags = _workspace(cfg, workspace, dev, flags)
+    workspace, flags = _workspace(cfg, workspace, q, flags)
     with _on(dev):
         C.packed_attn_fwd(_with_flags(cfg, flags), q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(),
                           o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), _raw_stream(dev))
@@ -132,9 +133,9 @@ def packed_attn_bwd(cfg, q, k, v, cu_seqlens, o, lse, d_o, dq=None, dk=None, dv=
     T, Hq, Hkv, dev, flags = cfg.total, cfg.Hq, cfg.Hkv, q.get_device(), cfg.flags
     if dq is None and dk is None and dv is None:
         flags |= C.HGA_PACKED_FILL_TAIL
-        dq = torch.empty((T, Hq, _D), dtype=q.dtype, device=q.device)
-        dk = torch.empty((T, Hkv, _D), dtype=q.dtype, device=q.device)
-        dv = torch.empty((T, Hkv, _D), dtype=q.dtype, device=q.device)
+        dq = q.new_empty((T, Hq, _D))
+        dk = q.new_empty((T, Hkv, _D))
+        dv = q.new_empty((T, Hkv, _D))
     elif dq is None or dk is None or dv is None:
         raise ValueError("dq, dk and dv are given together or not at all")
     else:
@@ -143,7 +144,7 @@ def packed_attn_bwd(cfg, q, k, v, cu_seqlens, o, lse, d_o, dq=None, dk=None, dv=
     _flat(o, "o", (T, Hq, _D), q.dtype, dev)
     _flat(d_o, "d_o", (T, Hq, _D), q.dtype, dev)
     _flat(lse, "lse", (Hq, T), torch.float32, dev)
-    workspace, flags = _workspace(cfg, workspace, dev, flags)
+    workspace, flags = _workspace(cfg, workspace, q, flags)
     with _on(dev):
         C.packed_attn_bwd(_with_flags(cfg, flags), q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(),
                           o.data_ptr(), lse.data_ptr(), d_o.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
@@ -151,10 +152,13 @@ def packed_attn_bwd(cfg, q, k, v, cu_seqlens, o, lse, d_o, dq=None, dk=None, dv=
     return dq, dk, dv
 
 
+_NEW = C.HGA_PACKED_FILL_TAIL | C.HGA_PACKED_CLEAR_STATUS      # of calls with outputs and workspace of their own
+
+
 class _PackedAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, cu_seqlens, softmax_scale):
-        cfg = make_packed_config(q, k, v, cu_seqlens, softmax_scale)
+        cfg = make_packed_config(q, k, v, cu_seqlens, softmax_scale, _NEW)
         o, lse = packed_attn_fwd(cfg, q, k, v, cu_seqlens)
         ctx.cfg = cfg
         ctx.save_for_backward(q, k, v, cu_seqlens, o, lse)
@@ -185,7 +189,7 @@ def packed_attention(q, k, v, cu_seqlens, softmax_scale: float | None = None):
     bfloat16."""
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
         return _PackedAttention.apply(q, k, v, cu_seqlens, softmax_scale)
-    return packed_attn_fwd(make_packed_config(q, k, v, cu_seqlens, softmax_scale), q, k, v, cu_seqlens)
+    return packed_attn_fwd(make_packed_config(q, k, v, cu_seqlens, softmax_scale, _NEW), q, k, v, cu_seqlens)
 
 
 class PagedKVCache:
@@ -292,11 +296,11 @@ class PagedKVCache:
         if sh != _D or sn < Hq * _D:
             raise ValueError(f"q: the heads of a token must be contiguous, got strides {tuple(q.stride())}")
         if o is None:
-            o = torch.empty((n, Hq, _D), dtype=self.dtype, device=self.device)
+            o = q.new_empty((n, Hq, _D))
         else:
             _flat(o, "o", (n, Hq, _D), self.dtype, self._dev)
         if lse is None:
-            lse = torch.empty((n, Hq), dtype=torch.float32, device=self.device)
+            lse = q.new_empty((n, Hq), dtype=torch.float32)
         else:
             _flat(lse, "lse", (n, Hq), torch.float32, self._dev)
         self._call(C.paged_attn, self._layer(layer), n, Hq, float(softmax_scale or 0.0), rows.data_ptr(),
