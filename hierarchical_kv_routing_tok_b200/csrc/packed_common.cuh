@@ -21,21 +21,19 @@ struct Problem {
   uint64_t wait_ns;
 };
 
-constexpr int kSimtTile = 64;   // tokens per tile of the CUDA-core kernels
-
-cudaError_t launch_fwd_simt(bool bf16, const void* q, const void* k, const void* v, void* o, float* lse,
-                            const Header* hdr, const Tile* list, const Problem& p, cudaStream_t st);
-cudaError_t launch_bwd_simt(bool bf16, const void* q, const void* k, const void* v, const void* o, const float* lse,
-                            const void* d_o, float* delta, void* dq, void* dk, void* dv, const Header* hdr,
-                            const Tile* by_query, const Tile* by_key, const Problem& p, cudaStream_t st);
-
-int fwd_tile(int G);           // tokens per unit of the tensor-core forward
+constexpr int kF32Tile = 64;   // tokens per tile of the float32 kernels
+constexpr int kKeyTile = 128;  // keys per CTA of the bf16 dK, dV kernel
 constexpr int kLeastTile = 16; // no kernel's tiles are shorter
+int fwd_tile(int G);           // tokens per unit of the bf16 forward
+int dq_tile(int G);            // tokens per unit of the bf16 dQ
+
+cudaError_t launch_fwd_f32(const void* q, const void* k, const void* v, void* o, float* lse, const Header* hdr,
+                           const Tile* list, const Problem& p, cudaStream_t st);
+cudaError_t launch_bwd_f32(const void* q, const void* k, const void* v, const void* o, const float* lse,
+                           const void* d_o, float* delta, void* dq, void* dk, void* dv, const Header* hdr,
+                           const Tile* by_query, const Tile* by_key, const Problem& p, cudaStream_t st);
 cudaError_t launch_fwd_tc(const void* q, const void* k, const void* v, void* o, float* lse, const Header* hdr,
                           const Tile* list, const Problem& p, cudaStream_t st);
-
-int dq_tile(int G);            // tokens per unit of the tensor-core dQ
-constexpr int kKeyTile = 128;  // keys per CTA of the tensor-core dK, dV
 cudaError_t launch_bwd_tc(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* d_o,
                           float* delta, void* dq, void* dk, void* dv, const Header* hdr, const Tile* by_query,
                           const Tile* by_key, const Problem& p, cudaStream_t st);

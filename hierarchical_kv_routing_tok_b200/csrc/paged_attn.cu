@@ -693,7 +693,7 @@ constexpr size_t kCounterBytes = kMaxCtas * sizeof(int);
 
 size_t paged_attn_scratch_bytes() { return kCounterBytes + 2 * (size_t)kMaxCtas * sizeof(Part); }
 
-cudaError_t launch_paged_attn(bool bf16, bool tensor_cores, const Cache& c, int layer, int n, int Hq, float scale,
+cudaError_t launch_paged_attn(bool bf16, const Cache& c, int layer, int n, int Hq, float scale,
                               const int32_t* rows, const void* q, int64_t q_stride_n, const void* k_pool,
                               const void* v_pool, void* o, float* lse, void* scratch, uint64_t wait_ns,
                               cudaStream_t st) {
@@ -733,7 +733,7 @@ cudaError_t launch_paged_attn(bool bf16, bool tensor_cores, const Cache& c, int 
     if (g > kMaxCtas) g = kMaxCtas;
     return dim3((unsigned)(g < tiles ? g : tiles));
   };
-  if (bf16 && tensor_cores) {
+  if (bf16) {
     CUtensorMap mk, mv;
     if (!make_pool_map(&mk, a.k_pool, c) || !make_pool_map(&mv, a.v_pool, c)) return cudaErrorInvalidValue;
     auto kernel = a.G <= 8 ? paged_mma_kernel<1> : paged_mma_kernel<2>;
@@ -742,7 +742,7 @@ cudaError_t launch_paged_attn(bool bf16, bool tensor_cores, const Cache& c, int 
     if (e != cudaSuccess) return e;
     return launch_dependent(kernel, grid_of(2), dim3(kMmaThreads), smem, st, 1, mk, mv, a);
   }
-  auto kernel = bf16 ? paged_simt_kernel<__nv_bfloat16> : paged_simt_kernel<float>;
+  auto kernel = paged_simt_kernel<float>;
   e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SimtSmem));
   if (e != cudaSuccess) return e;
   static_assert(2 * (sizeof(SimtSmem) + 1024) <= 228 * 1024, "two CTAs per SM");

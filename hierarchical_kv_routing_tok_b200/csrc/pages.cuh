@@ -43,7 +43,7 @@ cudaError_t launch_copy(const Cache& c, const Scratch& s, int n, const int32_t* 
                         void* v_pool, cudaStream_t st);
 
 size_t paged_attn_scratch_bytes();
-cudaError_t launch_paged_attn(bool bf16, bool tensor_cores, const Cache& c, int layer, int n, int Hq, float scale,
+cudaError_t launch_paged_attn(bool bf16, const Cache& c, int layer, int n, int Hq, float scale,
                               const int32_t* rows, const void* q, int64_t q_stride_n, const void* k_pool,
                               const void* v_pool, void* o, float* lse, void* scratch, uint64_t wait_ns,
                               cudaStream_t st);

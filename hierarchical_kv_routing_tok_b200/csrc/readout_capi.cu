@@ -3,8 +3,6 @@
 // kernels on the caller's stream.  No allocation, no synchronisation.
 #include <math.h>
 #include <stdint.h>
-#include <stdlib.h>
-#include <string.h>
 
 #include <initializer_list>
 
@@ -29,11 +27,6 @@ int check_workspace(const void* ws) {
 }
 
 int from_cuda(cudaError_t e) { return e == cudaSuccess ? HGA_OK : HGA_ERR_CUDA; }
-
-bool force_cuda_cores() {
-  const char* v = getenv("HGA_ATTN_PATH");
-  return v && strcmp(v, "cuda_cores") == 0;
-}
 
 uint64_t wait_limit(int64_t ns) { return ns > 0 ? (uint64_t)ns : 2000000000ull; }
 int elem_bytes(int dtype) { return dtype == HGA_BF16 ? 2 : 4; }
@@ -67,7 +60,7 @@ int check_packed(const hga_packed_config_t* c) {
   if (bad_scale(c->softmax_scale) || c->wait_limit_ns < 0) return HGA_ERR_ARG;
   // rows are 32-bit tensor-map coordinates, a tile may look past the last one; a CTA per (tile, head)
   if (c->total > (int64_t)INT32_MAX - 256 || c->n_seqs > 1 << 24) return HGA_ERR_UNSUPPORTED;
-  if (c->Hq > 4096 || (c->total / hga::packed::kSimtTile + c->n_seqs) * c->Hq > INT32_MAX) return HGA_ERR_UNSUPPORTED;
+  if (c->Hq > 4096 || (c->total / hga::packed::kLeastTile + c->n_seqs) * c->Hq > INT32_MAX) return HGA_ERR_UNSUPPORTED;
   return HGA_OK;
 }
 
@@ -111,9 +104,6 @@ size_t packed_bytes(const hga_packed_config_t* c) {
   return hga::kStatusBytes + sizeof(hga::packed::Header) + 2 * list_bytes(c) +
          round256((size_t)c->Hq * c->total * sizeof(float));
 }
-
-// bf16 runs on the tensor cores.
-bool packed_tc(const hga_packed_config_t* c) { return c->dtype == HGA_BF16 && !force_cuda_cores(); }
 
 // ---------------------------------------------------------------- pages
 int check_pages(const hga_pages_config_t* c) {
@@ -200,14 +190,13 @@ int hga_packed_attn_fwd(const hga_packed_config_t* cfg, const void* q, const voi
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const hga::packed::Problem p = packed_problem(cfg, workspace);
   const PackedWorkspace w = packed_workspace(cfg, workspace);
-  const bool tc = packed_tc(cfg);
-  const hga::packed::ListSpec list{tc ? hga::packed::fwd_tile(p.G) : hga::packed::kSimtTile, 0, w.lists[0]};
+  const bool bf16 = cfg->dtype == HGA_BF16;
+  const hga::packed::ListSpec list{bf16 ? hga::packed::fwd_tile(p.G) : hga::packed::kF32Tile, 0, w.lists[0]};
   cudaError_t e = hga::packed::launch_plan(cu_seqlens, cfg->n_seqs, cfg->total, 1, &list, w.hdr, p.status,
                                            (cfg->flags & HGA_PACKED_CLEAR_STATUS) != 0, st);
   if (e != cudaSuccess || cfg->total == 0) return from_cuda(e);
-  if (tc) return from_cuda(hga::packed::launch_fwd_tc(q, k, v, o, lse, w.hdr, w.lists[0], p, st));
-  return from_cuda(
-      hga::packed::launch_fwd_simt(cfg->dtype == HGA_BF16, q, k, v, o, lse, w.hdr, w.lists[0], p, st));
+  return from_cuda((bf16 ? hga::packed::launch_fwd_tc : hga::packed::launch_fwd_f32)(q, k, v, o, lse, w.hdr, w.lists[0],
+                                                                                     p, st));
 }
 
 int hga_packed_attn_bwd(const hga_packed_config_t* cfg, const void* q, const void* k, const void* v,
@@ -221,18 +210,15 @@ int hga_packed_attn_bwd(const hga_packed_config_t* cfg, const void* q, const voi
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const hga::packed::Problem p = packed_problem(cfg, workspace);
   const PackedWorkspace w = packed_workspace(cfg, workspace);
-  const bool tc = packed_tc(cfg);
+  const bool bf16 = cfg->dtype == HGA_BF16;
   const hga::packed::ListSpec lists[2] = {
-      {tc ? hga::packed::dq_tile(p.G) : hga::packed::kSimtTile, 0, w.lists[0]},
-      {tc ? hga::packed::kKeyTile : hga::packed::kSimtTile, 1, w.lists[1]}};
+      {bf16 ? hga::packed::dq_tile(p.G) : hga::packed::kF32Tile, 0, w.lists[0]},
+      {bf16 ? hga::packed::kKeyTile : hga::packed::kF32Tile, 1, w.lists[1]}};
   cudaError_t e = hga::packed::launch_plan(cu_seqlens, cfg->n_seqs, cfg->total, 2, lists, w.hdr, p.status,
                                            (cfg->flags & HGA_PACKED_CLEAR_STATUS) != 0, st);
   if (e != cudaSuccess || cfg->total == 0) return from_cuda(e);
-  if (tc)
-    return from_cuda(hga::packed::launch_bwd_tc(q, k, v, o, lse, d_o, w.delta, dq, dk, dv, w.hdr, w.lists[0],
-                                                w.lists[1], p, st));
-  return from_cuda(hga::packed::launch_bwd_simt(cfg->dtype == HGA_BF16, q, k, v, o, lse, d_o, w.delta, dq, dk, dv,
-                                                w.hdr, w.lists[0], w.lists[1], p, st));
+  return from_cuda((bf16 ? hga::packed::launch_bwd_tc : hga::packed::launch_bwd_f32)(
+      q, k, v, o, lse, d_o, w.delta, dq, dk, dv, w.hdr, w.lists[0], w.lists[1], p, st));
 }
 
 int hga_pages_workspace_size(const hga_pages_config_t* cfg, int32_t Hq, size_t* bytes_out) {
@@ -295,7 +281,7 @@ int hga_paged_attn(const hga_pages_config_t* cfg, int32_t layer, int32_t n, int3
     return rc;
   if (n == 0) return HGA_OK;
   return from_cuda(hga::pages::launch_paged_attn(
-      cfg->dtype == HGA_BF16, !force_cuda_cores(), cache_of(cfg, table, seq_len, nullptr, workspace), layer, n, Hq,
+      cfg->dtype == HGA_BF16, cache_of(cfg, table, seq_len, nullptr, workspace), layer, n, Hq,
       eff_scale(softmax_scale), rows, q, q_stride_n ? q_stride_n : (int64_t)Hq * hga::kD, k_pool, v_pool, o, lse,
       attn_scratch_of(cfg, workspace), wait_limit(cfg->wait_limit_ns), static_cast<cudaStream_t>(stream)));
 }

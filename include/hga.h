@@ -392,7 +392,8 @@ HGA_API int hga_route_groups_cached(const hga_config_t* cfg, const float* qb, co
  * Query head h uses KV head h / (Hq / Hkv).  cu_seqlens: n_seqs + 1 int32 on the device, from 0,
  * not decreasing, at most total; if it is not, no sequence is computed (all rows count as rows of
  * no sequence) and HGA_ERR_ARG is recorded in the workspace status word.
- * bf16 runs on the tensor cores, float32 on the CUDA cores in float32 arithmetic.
+ * Products accumulate in float32.  bf16: probabilities and dS are rounded to bf16 before their second
+ * product.  float32: each operand as the sum of two tf32 numbers, which keeps float32 accuracy.
  * total <= 2^31 - 1 - 256; total = 0 or n_seqs = 0 is a valid empty problem.
  * Two calls that may overlap in time need two workspaces. */
 enum hga_packed_flags {

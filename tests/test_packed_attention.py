@@ -296,14 +296,6 @@ def test_broadcast_gradient(hga):
         assert torch.equal(x.grad, 2 * once[n])
 
 
-def test_cuda_cores_agree(hga, monkeypatch):
-    """bf16 on the CUDA cores (asked for by the environment) keeps the same bounds."""
-    monkeypatch.setenv("HGA_ATTN_PATH", "cuda_cores")
-    lens = [130, 1, 77]
-    q, k, v, d_o = make(lens, 6, 2, BF16, "fused", tail=3)
-    check_all(run(hga, q, k, v, d_o, ends(lens)), R.packed(q, k, v, lens, d_o=d_o))
-
-
 def test_refusals(hga):
     q, k, v, d_o = make([9], 4, 2, BF16)
     cu = ends([9])

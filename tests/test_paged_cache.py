@@ -460,13 +460,6 @@ def test_attend_is_reproducible(hga, dtype):
         assert torch.equal(a, c) and torch.equal(b, d)
 
 
-def test_cuda_cores_agree(hga, monkeypatch):
-    monkeypatch.setenv("HGA_ATTN_PATH", "cuda_cores")
-    cache, gen = filled(hga, [999, 3000, 5, 0], 64, 2, BF16)
-    q = torch.randn(4, 8, 128, generator=gen, device="cuda").to(BF16)
-    attend_and_check(cache, q, [0, 1, 2, 3])
-
-
 def test_extreme_scores(hga):
     for dtype in (F32, BF16):
         cache, gen = filled(hga, [700], 32, 1, dtype)
