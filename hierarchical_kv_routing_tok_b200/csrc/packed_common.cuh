@@ -21,7 +21,7 @@ struct Problem {
   uint64_t wait_ns;
 };
 
-constexpr int kF32Tile = 64;   // tokens per tile of the float32 kernels
+int f32_tile(int64_t total, int n_seqs, int units);   // tokens per tile of the float32 kernels
 constexpr int kKeyTile = 128;  // keys per CTA of the bf16 dK, dV kernel
 constexpr int kLeastTile = 16; // no kernel's tiles are shorter
 int fwd_tile(int G);           // tokens per unit of the bf16 forward

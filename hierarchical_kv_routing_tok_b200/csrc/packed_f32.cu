@@ -10,8 +10,9 @@
 // Three m16n8k8 products run at 90 TFLOP/s (271 measured for one, against 67 for the FMA pipe), and a fragment
 // serves several products, where the FMA pipe would wait for shared memory.
 //
-// One CTA per (64-row tile, head): eight warps, 16 rows each, two groups of four that take the 32-column halves of
-// every 64-column tile and meet at the end.  Column tiles arrive by 16-byte asynchronous copies, double-buffered;
+// One CTA per (row tile, head): eight warps of 16 rows each, in RW row positions and 8 / RW groups that share out the
+// columns of every 64-column tile and meet at the end.  RW = 4 (64 rows, two groups of 32 columns), or 2 (32 rows, four
+// groups of 16) while that leaves SMs without work: the longest row tile then takes half as long.  Column tiles arrive by 16-byte asynchronous copies, double-buffered;
 // rows outside the sequence arrive as zeros.  The rows are queries (forward, dq) or keys (dk, dv).  Every output
 // element has one owner: no atomics.  Bound by the tensor pipe, or, for few tiles, by the longest row tile.
 #include <math.h>
@@ -24,7 +25,7 @@ namespace packed {
 
 namespace {
 
-constexpr int kRows = 64, kCols = 64;      // rows and columns of a tile
+constexpr int kCols = 64;                  // columns of a tile
 constexpr int LD = kD + 4;                 // row stride of a tile in shared memory: no bank conflicts
 constexpr int kTileFloats = 64 * LD;
 constexpr int kThreads = 256;
@@ -49,58 +50,60 @@ __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], const float* p) {
 
 // The tensor cores cut their sums (round towards zero): a product's chain is kept to 32 inner terms and added to its
 // total on the FMA pipe, which rounds to nearest.  (One chain over everything was six times further off: 3.5e-6.)
-__device__ __forceinline__ void add(float (&c)[4][4], const float (&x)[4][4]) {
+template <int N>
+__device__ __forceinline__ void add(float (&c)[N][4], const float (&x)[N][4]) {
 #pragma unroll
-  for (int n = 0; n < 4; ++n)
+  for (int n = 0; n < N; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) c[n][e] += x[n][e];
 }
 
-// c[n][..] = A[16 rows] . B[32 columns]^T over 128 dims (n: eight columns each).
-__device__ __forceinline__ void mul_abt(float (&c)[4][4], const float* A, const float* B) {
+// c[n][..] = A[16 rows] . B[8 N columns]^T over 128 dims (n: eight columns each).
+template <int N>
+__device__ __forceinline__ void mul_abt(float (&c)[N][4], const float* A, const float* B) {
   const int lane = threadIdx.x & 31;
   const float* pa = A + ((lane & 7) + ((lane >> 3) & 1) * 8) * LD + (lane >> 4) * 4;
   const float* pb = B + ((lane & 7) + (lane >> 4) * 8) * LD + ((lane >> 3) & 1) * 4;
 #pragma unroll
-  for (int n = 0; n < 4; ++n)
+  for (int n = 0; n < N; ++n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) c[n][e] = 0.f;
 #pragma unroll 1
   for (int k0 = 0; k0 < kD / 8; k0 += 4) {
-    float x[4][4] = {};
+    float x[N][4] = {};
 #pragma unroll
     for (int ks = k0; ks < k0 + 4; ++ks) {
-      uint32_t a[4], ah[4], al[4], b[2][4], bh[2][4], bl[2][4];
+      uint32_t a[4], ah[4], al[4], b[N / 2][4], bh[N / 2][4], bl[N / 2][4];
       ldsm4(a, pa + 8 * ks);
-      ldsm4(b[0], pb + 8 * ks);
-      ldsm4(b[1], pb + 16 * LD + 8 * ks);
+#pragma unroll
+      for (int y = 0; y < N / 2; ++y) ldsm4(b[y], pb + 16 * y * LD + 8 * ks);
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         split(__uint_as_float(a[e]), ah[e], al[e]);
-        split(__uint_as_float(b[0][e]), bh[0][e], bl[0][e]);
-        split(__uint_as_float(b[1][e]), bh[1][e], bl[1][e]);
+#pragma unroll
+        for (int y = 0; y < N / 2; ++y) split(__uint_as_float(b[y][e]), bh[y][e], bl[y][e]);
       }
 #pragma unroll
-      for (int n = 0; n < 4; ++n) mma_tf32(x[n], ah, bl[n >> 1][2 * (n & 1)], bl[n >> 1][2 * (n & 1) + 1]);
+      for (int n = 0; n < N; ++n) mma_tf32(x[n], ah, bl[n >> 1][2 * (n & 1)], bl[n >> 1][2 * (n & 1) + 1]);
 #pragma unroll
-      for (int n = 0; n < 4; ++n) mma_tf32(x[n], al, bh[n >> 1][2 * (n & 1)], bh[n >> 1][2 * (n & 1) + 1]);
+      for (int n = 0; n < N; ++n) mma_tf32(x[n], al, bh[n >> 1][2 * (n & 1)], bh[n >> 1][2 * (n & 1) + 1]);
 #pragma unroll
-      for (int n = 0; n < 4; ++n) mma_tf32(x[n], ah, bh[n >> 1][2 * (n & 1)], bh[n >> 1][2 * (n & 1) + 1]);
+      for (int n = 0; n < N; ++n) mma_tf32(x[n], ah, bh[n >> 1][2 * (n & 1)], bh[n >> 1][2 * (n & 1) + 1]);
     }
     add(c, x);
   }
 }
 
-// acc[n][..] += P[16 rows][32 columns] . B[32 columns][128 dims].  P is a result fragment of mul_abt: its column
+// acc[n][..] += P[16 rows][8 N columns] . B[8 N columns][128 dims].  P is a result fragment of mul_abt: its column
 // pair (2t, 2t + 1) of eight serves as the product's inner indexes t, t + 4, with the rows of B taken to match.
 // kFinite: values of B that are not finite count as 0 and set *found (0 * inf would not be 0).
-template <bool kFinite>
-__device__ __forceinline__ void mul_pb(float (&acc)[16][4], const float (&P)[4][4], const float* B, bool* found) {
+template <bool kFinite, int N>
+__device__ __forceinline__ void mul_pb(float (&acc)[16][4], const float (&P)[N][4], const float* B, bool* found) {
   const int lane = threadIdx.x & 31;
   const float* pb = B + 2 * (lane & 3) * LD + (lane >> 2);
-  uint32_t ah[4][4], al[4][4];
+  uint32_t ah[N][4], al[N][4];
 #pragma unroll
-  for (int kb = 0; kb < 4; ++kb) {
+  for (int kb = 0; kb < N; ++kb) {
     split(P[kb][0], ah[kb][0], al[kb][0]);
     split(P[kb][2], ah[kb][1], al[kb][1]);
     split(P[kb][1], ah[kb][2], al[kb][2]);
@@ -110,7 +113,7 @@ __device__ __forceinline__ void mul_pb(float (&acc)[16][4], const float (&P)[4][
   for (int n0 = 0; n0 < 16; n0 += 4) {
     float x[4][4] = {};
 #pragma unroll
-    for (int kb = 0; kb < 4; ++kb) {
+    for (int kb = 0; kb < N; ++kb) {
       uint32_t bh[4][2], bl[4][2];
 #pragma unroll
       for (int n = 0; n < 4; ++n)
@@ -137,10 +140,11 @@ __device__ __forceinline__ void mul_pb(float (&acc)[16][4], const float (&P)[4][
   }
 }
 
-// Rows t0 .. t0 + 63 of head h of a strided tensor into a tile; zeros outside [0, len).
+// Rows t0 .. t0 + R - 1 of head h of a strided tensor into a tile; zeros outside [0, len).
+template <int R>
 __device__ __forceinline__ void load_tile_async(float* dst, const float* x, Strided s, const Tile& w, int64_t t0, int h) {
 #pragma unroll
-  for (int i = 0; i < 64 * (kD / 4) / kThreads; ++i) {
+  for (int i = 0; i < R * (kD / 4) / kThreads; ++i) {
     const int y = i * kThreads + (int)threadIdx.x, r = y / (kD / 4), c = 4 * (y % (kD / 4));
     const int64_t t = t0 + r;
     const bool in = t < w.len;
@@ -187,7 +191,22 @@ __device__ __forceinline__ void store_tile(float* out, const float* tile, int r0
   }
 }
 
+// The column groups' sums of a row tile meet in `tile`, in the order of the groups.  Called by all threads; ends with a
+// barrier.
+template <int RW>
+__device__ __forceinline__ void meet(float* tile, int grp, int row0, const float (&acc)[16][4], float f0, float f1) {
+#pragma unroll
+  for (int x = 0; x < 8 / RW; ++x) {
+    if (grp == x) {
+      if (x == 0) put_rows(tile, row0, acc, f0, f1);
+      else add_rows(tile, row0, acc, f0, f1);
+    }
+    __syncthreads();
+  }
+}
+
 // ------------------------------------------------------------------------------------ forward
+template <int RW>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_fwd_f32_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
                           float* __restrict__ o, float* __restrict__ lse, const Header* hdr, const Tile* list,
@@ -196,9 +215,10 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* Qs = f32_smem;
   float* Ks = Qs + kTileFloats;            // two stages each
   float* Vs = Ks + 2 * kTileFloats;
-  __shared__ float s_m[2][kRows], s_l[2][kRows];
+  __shared__ float s_m[8 / RW][16 * RW], s_l[8 / RW][16 * RW];
   __shared__ int s_found;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = warp >> 2, row0 = 16 * (warp & 3);
+  constexpr int kRows = 16 * RW, kGroup = 8 * RW, NC = RW;    // rows of the tile; columns, and their eights, of a group
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = warp / RW, row0 = 16 * (warp % RW);
   const int g = lane >> 2, tq = lane & 3;
   pdl_trigger();
   pdl_wait();
@@ -212,9 +232,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Tile w = list[blockIdx.x / p.Hq];
   const int n_tiles = (int)((min((int64_t)w.t0 + kRows, (int64_t)w.len) - 1) / kCols) + 1;
   if (threadIdx.x == 0) s_found = 0;
-  load_tile_async(Qs, q, p.q, w, w.t0, h);
-  load_tile_async(Ks, k, p.k, w, 0, kh);
-  load_tile_async(Vs, v, p.v, w, 0, kh);
+  load_tile_async<kRows>(Qs, q, p.q, w, w.t0, h);
+  load_tile_async<kCols>(Ks, k, p.k, w, 0, kh);
+  load_tile_async<kCols>(Vs, v, p.v, w, 0, kh);
   async_commit();
 
   const float c2 = p.scale * kLog2eF;
@@ -226,23 +246,23 @@ __global__ void __launch_bounds__(kThreads, 1)
   bool found = false;
   for (int j = 0; j < n_tiles; ++j) {
     if (j + 1 < n_tiles) {
-      load_tile_async(Ks + ((j + 1) & 1) * kTileFloats, k, p.k, w, (int64_t)(j + 1) * kCols, kh);
-      load_tile_async(Vs + ((j + 1) & 1) * kTileFloats, v, p.v, w, (int64_t)(j + 1) * kCols, kh);
+      load_tile_async<kCols>(Ks + ((j + 1) & 1) * kTileFloats, k, p.k, w, (int64_t)(j + 1) * kCols, kh);
+      load_tile_async<kCols>(Vs + ((j + 1) & 1) * kTileFloats, v, p.v, w, (int64_t)(j + 1) * kCols, kh);
     }
     async_commit();
     async_wait<1>();
     __syncthreads();
-    const int col0 = j * kCols + 32 * grp;             // this group's first key
+    const int col0 = j * kCols + kGroup * grp;             // this group's first key
     const int last = w.t0 + row0 + 15 - col0;          // last of them that the warp's last row attends
     if (last >= 0) {
-      float s[4][4];
-      mul_abt(s, Qs + row0 * LD, Ks + (j & 1) * kTileFloats + 32 * grp * LD);
+      float s[NC][4];
+      mul_abt(s, Qs + row0 * LD, Ks + (j & 1) * kTileFloats + kGroup * grp * LD);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int lim = w.t0 + row0 + g + 8 * x - col0; // last key that row g + 8x attends
         float mx = -INFINITY;
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < NC; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float& y = s[n][2 * x + e];
@@ -255,7 +275,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const float alpha = exp2f(m[x] - ref);          // 0 when m = -inf
         float rs = 0.f;
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < NC; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float& y = s[n][2 * x + e];
@@ -270,11 +290,11 @@ __global__ void __launch_bounds__(kThreads, 1)
           acc[n][2 * x + 1] *= alpha;
         }
       }
-      mul_pb<true>(acc, s, Vs + (j & 1) * kTileFloats + 32 * grp * LD, &found);
+      mul_pb<true>(acc, s, Vs + (j & 1) * kTileFloats + kGroup * grp * LD, &found);
     }
     __syncthreads();                                    // the stage is free
   }
-  // ---- the two groups' statistics and outputs meet in the K area
+  // ---- the groups' statistics and outputs meet in the K area
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
@@ -290,19 +310,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
   for (int x = 0; x < 2; ++x) {
     const int r = row0 + g + 8 * x;
-    const float mt = fmaxf(s_m[0][r], s_m[1][r]);
-    // (the first key of a sequence is attended by every row, so group 0 always has a maximum; NaN goes through)
-    const float l0 = s_l[0][r] * exp2f(s_m[0][r] - mt), l1 = s_l[1][r] == 0.f ? 0.f : s_l[1][r] * exp2f(s_m[1][r] - mt);
-    const float inv = 1.f / (l0 + l1);
-    f[x] = m[x] == -INFINITY ? 0.f : exp2f(m[x] - mt) * inv;
+    float mt = s_m[0][r];
+#pragma unroll
+    for (int y = 1; y < 8 / RW; ++y) mt = fmaxf(mt, s_m[y][r]);
+    // (every row attends the first key of its sequence, so group 0 has a maximum; a group without keys has sum 0)
+    float lt = 0.f;
+#pragma unroll
+    for (int y = 0; y < 8 / RW; ++y) lt += s_l[y][r] == 0.f ? 0.f : s_l[y][r] * exp2f(s_m[y][r] - mt);
+    f[x] = m[x] == -INFINITY ? 0.f : exp2f(m[x] - mt) / lt;
     const int64_t t = (int64_t)w.t0 + r;
     if (grp == 0 && tq == 0 && t < w.len)
-      lse[h * p.total + w.start + t] = (mt + log2f(l0 + l1)) * 0.6931471805599453f;
+      lse[h * p.total + w.start + t] = (mt + log2f(lt)) * 0.6931471805599453f;
   }
-  if (grp == 1) put_rows(Ks, row0, acc, f[0], f[1]);
-  __syncthreads();
-  if (grp == 0) add_rows(Ks, row0, acc, f[0], f[1]);
-  __syncthreads();
+  meet<RW>(Ks, grp, row0, acc, f[0], f[1]);
   if (s_found) {
     // values that counted as 0 in the products: each adds itself to the rows that attend it
     for (int y = threadIdx.x; y < kRows * kD; y += kThreads) {
@@ -323,6 +343,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------------------------ backward: dq
 // Forms delta of its rows and leaves it in `delta` [Hq, total] for the dk, dv kernel.
+template <int RW>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_dq_f32_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
                          const float* __restrict__ o, const float* __restrict__ lse, const float* __restrict__ d_o,
@@ -333,8 +354,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* Gs = Qs + kTileFloats;
   float* Ks = Gs + kTileFloats;            // two stages each
   float* Vs = Ks + 2 * kTileFloats;
-  __shared__ float s_lse[kRows], s_delta[kRows];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = warp >> 2, row0 = 16 * (warp & 3);
+  __shared__ float s_lse[16 * RW], s_delta[16 * RW];
+  constexpr int kRows = 16 * RW, kGroup = 8 * RW, NC = RW;    // rows of the tile; columns, and their eights, of a group
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = warp / RW, row0 = 16 * (warp % RW);
   const int g = lane >> 2, tq = lane & 3;
   pdl_trigger();
   pdl_wait();
@@ -346,13 +368,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const Tile w = list[blockIdx.x / p.Hq];
   const Strided so{(int64_t)p.Hq * kD, kD};
   const int n_tiles = (int)((min((int64_t)w.t0 + kRows, (int64_t)w.len) - 1) / kCols) + 1;
-  load_tile_async(Qs, q, p.q, w, w.t0, h);
-  load_tile_async(Gs, d_o, so, w, w.t0, h);
-  load_tile_async(Ks, k, p.k, w, 0, kh);
-  load_tile_async(Vs, v, p.v, w, 0, kh);
+  load_tile_async<kRows>(Qs, q, p.q, w, w.t0, h);
+  load_tile_async<kRows>(Gs, d_o, so, w, w.t0, h);
+  load_tile_async<kCols>(Ks, k, p.k, w, 0, kh);
+  load_tile_async<kCols>(Vs, v, p.v, w, 0, kh);
   async_commit();
-  // delta and lse of the tile's rows: a warp per eight rows
-  for (int r = 8 * warp; r < 8 * warp + 8; ++r) {
+  // delta and lse of the tile's rows: shared out to the warps
+  for (int r = kRows / 8 * warp; r < kRows / 8 * (warp + 1); ++r) {
     const int64_t t = (int64_t)w.t0 + r, row = w.start + t;
     float x = 0.f, y = 0.f;
     if (t < w.len) {
@@ -376,17 +398,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int e = 0; e < 4; ++e) acc[n][e] = 0.f;
   for (int j = 0; j < n_tiles; ++j) {
     if (j + 1 < n_tiles) {
-      load_tile_async(Ks + ((j + 1) & 1) * kTileFloats, k, p.k, w, (int64_t)(j + 1) * kCols, kh);
-      load_tile_async(Vs + ((j + 1) & 1) * kTileFloats, v, p.v, w, (int64_t)(j + 1) * kCols, kh);
+      load_tile_async<kCols>(Ks + ((j + 1) & 1) * kTileFloats, k, p.k, w, (int64_t)(j + 1) * kCols, kh);
+      load_tile_async<kCols>(Vs + ((j + 1) & 1) * kTileFloats, v, p.v, w, (int64_t)(j + 1) * kCols, kh);
     }
     async_commit();
     async_wait<1>();
     __syncthreads();
-    const int col0 = j * kCols + 32 * grp;
+    const int col0 = j * kCols + kGroup * grp;
     if (w.t0 + row0 + 15 - col0 >= 0) {
-      const float* kt = Ks + (j & 1) * kTileFloats + 32 * grp * LD;
-      const float* vt = Vs + (j & 1) * kTileFloats + 32 * grp * LD;
-      float s[4][4], dp[4][4];
+      const float* kt = Ks + (j & 1) * kTileFloats + kGroup * grp * LD;
+      const float* vt = Vs + (j & 1) * kTileFloats + kGroup * grp * LD;
+      float s[NC][4], dp[NC][4];
       mul_abt(s, Qs + row0 * LD, kt);
       mul_abt(dp, Gs + row0 * LD, vt);
 #pragma unroll
@@ -395,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int lim = w.t0 + r < w.len ? w.t0 + r - col0 : -1;    // last key that the row attends
         const float ls = s_lse[r], dl = s_delta[r];
 #pragma unroll
-        for (int n = 0; n < 4; ++n)
+        for (int n = 0; n < NC; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
             float& y = s[n][2 * x + e];
@@ -406,10 +428,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
   }
-  if (grp == 1) put_rows(Ks, row0, acc, 1.f, 1.f);
-  __syncthreads();
-  if (grp == 0) add_rows(Ks, row0, acc, 1.f, 1.f);
-  __syncthreads();
+  meet<RW>(Ks, grp, row0, acc, 1.f, 1.f);
   store_tile(dq, Ks, 0, kRows, w, p.Hq, h, p.scale);
 }
 
@@ -417,6 +436,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // The rows are keys, the columns the queries of the KV head's query heads, one head after another.  When there are
 // fewer (tile, KV head) units than SMs, the heads are split over a cluster of cs CTAs; their sums meet through
 // distributed shared memory, each CTA adding and storing its share of the rows in the order of the ranks.
+template <int RW>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_dkdv_f32_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
                            const float* __restrict__ lse, const float* __restrict__ d_o,
@@ -428,7 +448,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   float* Qs = Vs + kTileFloats;            // two stages each
   float* Gs = Qs + 2 * kTileFloats;
   __shared__ float s_lse[2][kCols], s_delta[2][kCols];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = warp >> 2, row0 = 16 * (warp & 3);
+  constexpr int kRows = 16 * RW, kGroup = 8 * RW, NC = RW;    // rows of the tile; columns, and their eights, of a group
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, grp = warp / RW, row0 = 16 * (warp % RW);
   const int g = lane >> 2, tq = lane & 3;
   pdl_trigger();
   pdl_wait();
@@ -449,8 +470,8 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto load_step = [&](int j) {
     const int h = h0 + j / per_head;
     const int64_t t0 = w.t0 + (int64_t)(j % per_head) * kCols;
-    load_tile_async(Qs + (j & 1) * kTileFloats, q, p.q, w, t0, h);
-    load_tile_async(Gs + (j & 1) * kTileFloats, d_o, so, w, t0, h);
+    load_tile_async<kCols>(Qs + (j & 1) * kTileFloats, q, p.q, w, t0, h);
+    load_tile_async<kCols>(Gs + (j & 1) * kTileFloats, d_o, so, w, t0, h);
     if (threadIdx.x < 2 * kCols) {
       const int c = threadIdx.x & (kCols - 1);
       const bool in = t0 + c < w.len;
@@ -462,8 +483,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                    : "memory");
     }
   };
-  load_tile_async(Ks, k, p.k, w, w.t0, kh);
-  load_tile_async(Vs, v, p.v, w, w.t0, kh);
+  load_tile_async<kRows>(Ks, k, p.k, w, w.t0, kh);
+  load_tile_async<kRows>(Vs, v, p.v, w, w.t0, kh);
   load_step(0);
   async_commit();
   const float c2 = p.scale * kLog2eF;
@@ -477,19 +498,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     async_commit();
     async_wait<1>();
     __syncthreads();
-    const int col0 = w.t0 + j % per_head * kCols + 32 * grp;      // this group's first query
-    if (col0 + 31 >= w.t0 + row0 && col0 < w.len) {
-      const float* qt = Qs + (j & 1) * kTileFloats + 32 * grp * LD;
-      const float* gt = Gs + (j & 1) * kTileFloats + 32 * grp * LD;
-      float s[4][4], dp[4][4];
+    const int col0 = w.t0 + j % per_head * kCols + kGroup * grp;      // this group's first query
+    if (col0 + kGroup - 1 >= w.t0 + row0 && col0 < w.len) {
+      const float* qt = Qs + (j & 1) * kTileFloats + kGroup * grp * LD;
+      const float* gt = Gs + (j & 1) * kTileFloats + kGroup * grp * LD;
+      float s[NC][4], dp[NC][4];
       mul_abt(s, Ks + row0 * LD, qt);
       mul_abt(dp, Vs + row0 * LD, gt);
 #pragma unroll
-      for (int n = 0; n < 4; ++n)
+      for (int n = 0; n < NC; ++n)
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           const int c = 8 * n + 2 * tq + e, t = col0 + c;
-          const float ls = s_lse[j & 1][32 * grp + c] * kLog2eF, dl = s_delta[j & 1][32 * grp + c];
+          const float ls = s_lse[j & 1][kGroup * grp + c] * kLog2eF, dl = s_delta[j & 1][kGroup * grp + c];
 #pragma unroll
           for (int x = 0; x < 2; ++x) {
             const bool seen = t >= w.t0 + row0 + g + 8 * x && t < w.len;
@@ -503,20 +524,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     __syncthreads();
   }
-  // ---- the two groups meet (dK in the first Q stage, dV in the second), then the cluster's CTAs
+  // ---- the groups meet (dK in the first Q stage, dV in the second), then the cluster's CTAs
   float* tk = Qs;
   float* tv = Qs + kTileFloats;
-  if (grp == 1) {
-    put_rows(tk, row0, gk, 1.f, 1.f);
-    put_rows(tv, row0, gv, 1.f, 1.f);
-  }
-  __syncthreads();
-  if (grp == 0) {
-    add_rows(tk, row0, gk, 1.f, 1.f);
-    add_rows(tv, row0, gv, 1.f, 1.f);
-  }
+  meet<RW>(tk, grp, row0, gk, 1.f, 1.f);
+  meet<RW>(tv, grp, row0, gv, 1.f, 1.f);
   if (cs == 1) {
-    __syncthreads();
     store_tile(dk, tk, 0, kRows, w, p.Hkv, kh, p.scale);
     store_tile(dv, tv, 0, kRows, w, p.Hkv, kh, 1.f);
     return;
@@ -559,20 +572,32 @@ constexpr size_t kTileBytesF = kTileFloats * sizeof(float);
 
 }  // namespace
 
+// Whether 64-row tiles leave SMs without work (units: heads of one tile): then tiles of 32.  Tiny float32 layer (17 tiles
+// of 64, 4 heads), forward and backward: 306 us with 64 rows, SHORT us with 32; 8192 tokens, 32 heads: LONG64 against LONG32.
+int f32_tile(int64_t total, int n_seqs, int units) {
+  int dev = 0, sms = 148;
+  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
+  return list_capacity(total, n_seqs, 64) * units < sms ? 32 : 64;
+}
+
 cudaError_t launch_fwd_f32(const void* q, const void* k, const void* v, void* o, float* lse, const Header* hdr,
                            const Tile* list, const Problem& p, cudaStream_t st) {
-  const int64_t n = list_capacity(p.total, p.n_seqs, kF32Tile) * p.Hq;
-  return launch(packed_fwd_f32_kernel, n < 1 ? 1 : n, 5 * kTileBytesF, 1, st, (const float*)q, (const float*)k,
-                (const float*)v, (float*)o, lse, hdr, list, p);
+  const int tile = f32_tile(p.total, p.n_seqs, p.Hq);
+  const int64_t n = list_capacity(p.total, p.n_seqs, tile) * p.Hq;
+  return launch(tile == 32 ? packed_fwd_f32_kernel<2> : packed_fwd_f32_kernel<4>, n < 1 ? 1 : n, 5 * kTileBytesF, 1, st,
+                (const float*)q, (const float*)k, (const float*)v, (float*)o, lse, hdr, list, p);
 }
 
 cudaError_t launch_bwd_f32(const void* q, const void* k, const void* v, const void* o, const float* lse,
                            const void* d_o, float* delta, void* dq, void* dk, void* dv, const Header* hdr,
                            const Tile* by_query, const Tile* by_key, const Problem& p, cudaStream_t st) {
-  const int64_t tiles = list_capacity(p.total, p.n_seqs, kF32Tile);
+  // (both lists by the query heads: a cluster may share out the heads of a key tile)
+  const int tile = f32_tile(p.total, p.n_seqs, p.Hq);
+  const int64_t tiles = list_capacity(p.total, p.n_seqs, tile);
   const int64_t nq = tiles * p.Hq, nk = tiles * p.Hkv;
-  cudaError_t e = launch(packed_dq_f32_kernel, nq < 1 ? 1 : nq, 6 * kTileBytesF, 1, st, (const float*)q, (const float*)k,
-                         (const float*)v, (const float*)o, lse, (const float*)d_o, delta, (float*)dq, hdr, by_query, p);
+  cudaError_t e = launch(tile == 32 ? packed_dq_f32_kernel<2> : packed_dq_f32_kernel<4>, nq < 1 ? 1 : nq, 6 * kTileBytesF,
+                         1, st, (const float*)q, (const float*)k, (const float*)v, (const float*)o, lse,
+                         (const float*)d_o, delta, (float*)dq, hdr, by_query, p);
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 0;
   e = cudaGetDevice(&dev);
@@ -582,9 +607,9 @@ cudaError_t launch_bwd_f32(const void* q, const void* k, const void* v, const vo
   if (nk < sms)
     for (int c = 2; c <= 8; ++c)
       if (p.G % c == 0) cs = c;
-  return launch(packed_dkdv_f32_kernel, (nk < 1 ? 1 : nk) * cs, 6 * kTileBytesF, (unsigned)cs, st, (const float*)q,
-                (const float*)k, (const float*)v, lse, (const float*)d_o, (const float*)delta, (float*)dk, (float*)dv,
-                hdr, by_key, p, cs);
+  return launch(tile == 32 ? packed_dkdv_f32_kernel<2> : packed_dkdv_f32_kernel<4>, (nk < 1 ? 1 : nk) * cs,
+                6 * kTileBytesF, (unsigned)cs, st, (const float*)q, (const float*)k, (const float*)v, lse,
+                (const float*)d_o, (const float*)delta, (float*)dk, (float*)dv, hdr, by_key, p, cs);
 }
 
 }  // namespace packed

@@ -191,7 +191,8 @@ int hga_packed_attn_fwd(const hga_packed_config_t* cfg, const void* q, const voi
   const hga::packed::Problem p = packed_problem(cfg, workspace);
   const PackedWorkspace w = packed_workspace(cfg, workspace);
   const bool bf16 = cfg->dtype == HGA_BF16;
-  const hga::packed::ListSpec list{bf16 ? hga::packed::fwd_tile(p.G) : hga::packed::kF32Tile, 0, w.lists[0]};
+  const int f32_tile = hga::packed::f32_tile(p.total, p.n_seqs, p.Hq);
+  const hga::packed::ListSpec list{bf16 ? hga::packed::fwd_tile(p.G) : f32_tile, 0, w.lists[0]};
   cudaError_t e = hga::packed::launch_plan(cu_seqlens, cfg->n_seqs, cfg->total, 1, &list, w.hdr, p.status,
                                            (cfg->flags & HGA_PACKED_CLEAR_STATUS) != 0, st);
   if (e != cudaSuccess || cfg->total == 0) return from_cuda(e);
@@ -211,9 +212,10 @@ int hga_packed_attn_bwd(const hga_packed_config_t* cfg, const void* q, const voi
   const hga::packed::Problem p = packed_problem(cfg, workspace);
   const PackedWorkspace w = packed_workspace(cfg, workspace);
   const bool bf16 = cfg->dtype == HGA_BF16;
+  const int f32_tile = hga::packed::f32_tile(p.total, p.n_seqs, p.Hq);
   const hga::packed::ListSpec lists[2] = {
-      {bf16 ? hga::packed::dq_tile(p.G) : hga::packed::kF32Tile, 0, w.lists[0]},
-      {bf16 ? hga::packed::kKeyTile : hga::packed::kF32Tile, 1, w.lists[1]}};
+      {bf16 ? hga::packed::dq_tile(p.G) : f32_tile, 0, w.lists[0]},
+      {bf16 ? hga::packed::kKeyTile : f32_tile, 1, w.lists[1]}};
   cudaError_t e = hga::packed::launch_plan(cu_seqlens, cfg->n_seqs, cfg->total, 2, lists, w.hdr, p.status,
                                            (cfg->flags & HGA_PACKED_CLEAR_STATUS) != 0, st);
   if (e != cudaSuccess || cfg->total == 0) return from_cuda(e);
