@@ -7,7 +7,7 @@
 // (16 per clock and SM).  A unit is two query tiles of 128 rows (packed_tc.cuh) that share their K/V tiles of
 // 128 keys.  One CTA per SM walks the units of the work list, heaviest first; barriers and rings count tiles
 // across units, so the next unit's loads and first products run under the epilogue of the current one.
-// Warps: 0 loads Q and K, 2 loads V (TMA, rings of 3 and 2), 1 issues the products, 4-7 and 8-11 are the
+// Warps: 0 loads Q and K, 2 loads V (TMA, rings of two), 1 issues the products, 4-7 and 8-11 are the
 // softmax of the two tiles (thread = row), 3 cleans the V tiles that masked rows meet: on the causal
 // diagonal p = 0 meets values that the row does not attend, and 0 * inf is not 0.  Values there that are not
 // finite become 0 before the product, and the epilogue adds them to the rows that do attend them.
@@ -25,11 +25,11 @@ using namespace tc;
 namespace {
 
 constexpr float kRescaleThreshold = 8.f;   // log2 units
-constexpr int KS = 3, VS = 2;              // ring stages
+constexpr int KS = 2, VS = 2;              // ring stages
 constexpr int kThreads = 384;
 
 struct FwdParams {
-  int Hq, Hkv, G, pk, tp;                  // tp: tokens per query tile, 128 / pk
+  int Hq, Hkv, G, pk, pk_shift, tp;        // pk = 1 << pk_shift; tp: tokens per query tile, 128 / pk
   int hu;                                  // head units: Hkv * G / pk
   int64_t total;
   float scale_log2;
@@ -48,10 +48,11 @@ struct FwdSmem {
   static constexpr uint32_t kQ = 0;
   static constexpr uint32_t kK = kQ + 2 * kTileBytes;
   static constexpr uint32_t kV = kK + KS * kTileBytes;
-  static constexpr uint32_t kBar = kV + VS * kTileBytes;
+  static constexpr uint32_t kO = kV + VS * kTileBytes;          // 4 KB per softmax warp: 32 rows x 64 dims of o
+  static constexpr uint32_t kBar = kO + 8 * 4096;
   // q_full, q_empty, k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], v_clean[VS], s_full[2], p_full[2],
-  // o_full[2], mma_done
-  static constexpr int kNumBars = 2 + 2 * KS + 3 * VS + 6 + 1;
+  // o_full[2], mma_done, p_most[2]
+  static constexpr int kNumBars = 2 + 2 * KS + 3 * VS + 6 + 3;
   static constexpr uint32_t kMisc = kBar + 8 * kNumBars;        // TMEM address, abort, flags of 4 units
   static constexpr uint32_t kBytes = kMisc + 32;
 };
@@ -99,6 +100,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto p_full = [&](int i) { return BAR(4 + 2 * KS + 3 * VS + i); };
   auto o_full = [&](int i) { return BAR(6 + 2 * KS + 3 * VS + i); };
   const uint32_t mma_done = BAR(8 + 2 * KS + 3 * VS);
+  auto p_most = [&](int i) { return BAR(9 + 2 * KS + 3 * VS + i); };    // P of the tile's first 96 keys
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
   // whether a unit's diagonal tiles hold values that are not finite: unit k in slot k mod 4 (the cleaner is at
@@ -121,6 +123,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full(i), 1);
       mbar_init(p_full(i), 4);
+      mbar_init(p_most(i), 4);
       mbar_init(o_full(i), 1);
     }
     mbar_init(mma_done, 1);
@@ -236,13 +239,19 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (j >= x.T[i]) continue;
+          ok = mbar_wait_w(p_most(i), np[i] & 1, abort_flag, p.status, p.wait_ns);
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int ks = 0; ks < 6; ++ks)
+            mma_ts_w(tmem + 256 + i * 128, tmem + i * 128 + ks * 8, vd[ks], idesc_pv, (j > 0 || ks > 0));
           ok = mbar_wait_w(p_full(i), np[i] & 1, abort_flag, p.status, p.wait_ns);
           if (!ok) break;
           ++np[i];
           tc_fence_after();
 #pragma unroll
-          for (int ks = 0; ks < 8; ++ks)
-            mma_ts_w(tmem + 256 + i * 128, tmem + i * 128 + ks * 8, vd[ks], idesc_pv, (j > 0 || ks > 0));
+          for (int ks = 6; ks < 8; ++ks)
+            mma_ts_w(tmem + 256 + i * 128, tmem + i * 128 + ks * 8, vd[ks], idesc_pv, 1);
           if (j + 1 < x.T[i]) {
             if (!have_k) {
               ok = mbar_wait_w(k_full(sn), (uint32_t)(((J + 1) / KS) & 1), abort_flag, p.status, p.wait_ns);
@@ -281,13 +290,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t tS = tmem + lane_off + i * 128;
     const uint32_t tO = tmem + lane_off + 256 + i * 128;
-    const bool o_v8 = (reinterpret_cast<uintptr_t>(p.o) & 31u) == 0;
     int ns = 0, no = 0;                                 // S tiles, outputs taken
     bool ok = true;
     for (int k = 0; ok && load_unit(p, n_units, k, &x); ++k) {
       const int T = x.T[i];
       if (T == 0) continue;
-      const int t_pos = x.t0 + i * p.tp + r / p.pk;     // (rows past the sequence compute, and store nothing)
+      const int t_pos = x.t0 + i * p.tp + (r >> p.pk_shift);     // (rows past the sequence compute, and store nothing)
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < T; ++j, ++ns) {
         ok = mbar_wait_w(s_full(i), ns & 1, abort_flag, p.status, p.wait_ns);
@@ -301,52 +309,75 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&v[64]));
         tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&v[96]));
         tmem_wait_ld();
-        if (nvalid < kBN) {
+        const bool masked = __any_sync(0xffffffffu, nvalid < kBN);
+        if (masked) {
 #pragma unroll
           for (int e = 0; e < kBN; ++e)
             if (e >= nvalid) v[e] = __float_as_uint(-INFINITY);
         }
-        float mx0 = -INFINITY, mx1 = -INFINITY;         // of the raw products (the scale is positive)
-#pragma unroll
-        for (int e = 0; e < kBN; e += 2) {
-          mx0 = fmaxf(mx0, __uint_as_float(v[e]));
-          mx1 = fmaxf(mx1, __uint_as_float(v[e + 1]));
-        }
-        const float mx = fmaxf(mx0, mx1) * p.scale_log2;
-        // move the reference only when the maximum grows by more than 2^8
-        const bool need = mx > m + kRescaleThreshold || (m == -INFINITY && mx > -INFINITY);
-        const float mnew = need ? mx : m;
-        const float alpha = need ? ex2(m - mnew) : 1.f; // m = -inf -> 0
-        if (j > 0 && __any_sync(0xffffffffu, need)) {
-#pragma unroll 1
-          for (int cc = 0; cc < 4; ++cc) {
-            uint32_t o[32];
-            tmem_ld32(tO + cc * 32, o);
-            tmem_wait_ld();
-#pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tmem_st32(tO + cc * 32, o);
-          }
-        }
-        l *= alpha;
-        m = mnew;
-        const float mref = (m == -INFINITY) ? 0.f : m;
-        // probabilities, their sum in float32, and as bf16 (the product's operand type) over S
-        float rs0 = 0.f, rs1 = 0.f;
-#pragma unroll
-        for (int cc = 0; cc < 4; ++cc) {
-          uint32_t pk[16];
+        // Probabilities of 32 keys, their sum in float32, and as bf16 (the product's operand type).
+        const uint64_t c2 = pair(p.scale_log2, p.scale_log2);
+        uint64_t rs[2] = {0ull, 0ull};
+        auto probs = [&](int cc, float ref, uint32_t(&pk)[16]) {
+          const uint64_t mr2 = pair(-ref, -ref);
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            const float p0 = ex2(fmaf(__uint_as_float(v[cc * 32 + e]), p.scale_log2, -mref));
-            const float p1 = ex2(fmaf(__uint_as_float(v[cc * 32 + e + 1]), p.scale_log2, -mref));
-            rs0 += p0;
-            rs1 += p1;
+            float p0, p1;
+            unpair(fma2(pair(__uint_as_float(v[cc * 32 + e]), __uint_as_float(v[cc * 32 + e + 1])), c2, mr2), p0, p1);
+            p0 = ex2(p0);
+            p1 = ex2(p1);
+            rs[(e >> 1) & 1] = add2(rs[(e >> 1) & 1], pair(p0, p1));
             pk[e >> 1] = pack_bf16(p0, p1);
+          }
+        };
+        // The reference moves only when the maximum grows by more than 2^8, so the first 32 keys start with the old one
+        // while the maximum is still being found, and are done again in the rare case that it moves.
+        uint32_t pk[16];
+        probs(0, m == -INFINITY ? 0.f : m, pk);
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // of the raw products (the scale is positive)
+#pragma unroll
+        for (int e = 0; e < kBN; e += 8)
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            mx[y] = max3(mx[y], __uint_as_float(v[e + 2 * y]), __uint_as_float(v[e + 2 * y + 1]));
+        const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
+        const bool need = mt > m + kRescaleThreshold || (m == -INFINITY && mt > -INFINITY);
+        if (__any_sync(0xffffffffu, need)) {
+          const float mnew = need ? mt : m;
+          const float alpha = need ? ex2(m - mnew) : 1.f;             // m = -inf -> 0
+          if (j > 0) {
+#pragma unroll 1
+            for (int cc = 0; cc < 4; ++cc) {
+              uint32_t o[32];
+              tmem_ld32(tO + cc * 32, o);
+              tmem_wait_ld();
+#pragma unroll
+              for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+              tmem_st32(tO + cc * 32, o);
+            }
+          }
+          l *= alpha;
+          m = mnew;
+          rs[0] = rs[1] = 0ull;
+          probs(0, m == -INFINITY ? 0.f : m, pk);
+        }
+        const float mref = (m == -INFINITY) ? 0.f : m;
+        tmem_st16(tS, pk);
+#pragma unroll
+        for (int cc = 1; cc < 4; ++cc) {
+          probs(cc, mref, pk);
+          if (cc == 3) {                                // the first 96 keys' product starts under the rest
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(p_most(i));
           }
           tmem_st16(tS + cc * 16, pk);
         }
-        l += rs0 + rs1;
+        float r0, r1, r2, r3;
+        unpair(rs[0], r0, r1);
+        unpair(rs[1], r2, r3);
+        l += (r0 + r1) + (r2 + r3);
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -358,9 +389,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_after();
       const float inv = 1.f / l;
       const bool store = t_pos < x.len;
-      const int h = x.h0 + r % p.pk;
+      const int h = x.h0 + (r & (p.pk - 1));
       const int64_t row = (int64_t)x.start + t_pos;
       const bool fix = not_finite[k & 3] != 0;
+      // O / l as bf16, 64 dims at a time through this warp's 4 KB (16-byte pieces at position c ^ (row mod 8): no bank
+      // conflicts), so that the stores to global memory are whole 128-byte lines
+      const uint32_t stage = sbase + L::kO + (uint32_t)(warp - 4) * 4096u;
 #pragma unroll 1
       for (int cc = 0; cc < 4; ++cc) {
         uint32_t v[32];
@@ -377,25 +411,30 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
           }
         }
-        uint32_t pk[16];
 #pragma unroll
-        for (int e = 0; e < 32; e += 2)
-          pk[e >> 1] = pack_bf16(__uint_as_float(v[e]) * inv, __uint_as_float(v[e + 1]) * inv);
-        if (store) {
-          // 64 bytes of the row: whole 32-byte sectors when o is 32-byte aligned
-          __nv_bfloat16* dst = p.o + (row * p.Hq + h) * kD + cc * 32;
-          if (o_v8) {
+        for (int y = 0; y < 4; ++y) {
+          const uint32_t a = stage + lane * 128u + (((uint32_t)(4 * (cc & 1) + y) ^ (uint32_t)(lane & 7)) << 4);
+          uint32_t w4[4];
 #pragma unroll
-            for (int y = 0; y < 2; ++y)
-              asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 16 * y),
-                           "r"(pk[8 * y]), "r"(pk[8 * y + 1]), "r"(pk[8 * y + 2]), "r"(pk[8 * y + 3]),
-                           "r"(pk[8 * y + 4]), "r"(pk[8 * y + 5]), "r"(pk[8 * y + 6]), "r"(pk[8 * y + 7])
-                           : "memory");
-          } else {
-            uint4* d4 = reinterpret_cast<uint4*>(dst);
+          for (int e = 0; e < 4; ++e)
+            w4[e] = pack_bf16(__uint_as_float(v[8 * y + 2 * e]) * inv, __uint_as_float(v[8 * y + 2 * e + 1]) * inv);
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w4[0]), "r"(w4[1]), "r"(w4[2]), "r"(w4[3]) : "memory");
+        }
+        if (cc & 1) {
+          __syncwarp();
+          const int c = lane & 7;
 #pragma unroll
-            for (int y = 0; y < 4; ++y) d4[y] = make_uint4(pk[4 * y], pk[4 * y + 1], pk[4 * y + 2], pk[4 * y + 3]);
+          for (int y = 0; y < 8; ++y) {
+            const int rr = 4 * y + (lane >> 3), rt = quarter * 32 + rr;        // row of the warp, of the tile
+            const int t = x.t0 + i * p.tp + (rt >> p.pk_shift);
+            uint32_t w4[4];
+            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w4[0]), "=r"(w4[1]), "=r"(w4[2]), "=r"(w4[3])
+                         : "r"(stage + rr * 128u + ((uint32_t)(c ^ (rr & 7)) << 4)));
+            if (t < x.len)
+              *reinterpret_cast<uint4*>(p.o + (((int64_t)x.start + t) * p.Hq + x.h0 + (rt & (p.pk - 1))) * kD + 32 * (cc - 1) + 8 * c) =
+                  make_uint4(w4[0], w4[1], w4[2], w4[3]);
           }
+          __syncwarp();
         }
       }
       if (store) p.lse[h * p.total + row] = (m + __log2f(l)) * 0.6931471805599453f;
@@ -445,7 +484,7 @@ cudaError_t launch_fwd_tc(const void* q, const void* k, const void* v, void* o, 
   if (!make_map_packed(&mq, q, p.Hq, p.total, p.q, pk, 128 / pk) || !make_map_packed(&mk, k, p.Hkv, p.total, p.k, 1, kBN) ||
       !make_map_packed(&mv, v, p.Hkv, p.total, p.v, 1, kBN))
     return cudaErrorInvalidValue;
-  FwdParams a{p.Hq, p.Hkv, p.G, pk, 128 / pk, p.Hkv * (p.G / pk), p.total, p.scale * kLog2eF,
+  FwdParams a{p.Hq, p.Hkv, p.G, pk, pk == 8 ? 3 : pk == 4 ? 2 : pk - 1, 128 / pk, p.Hkv * (p.G / pk), p.total, p.scale * kLog2eF,
               static_cast<const __nv_bfloat16*>(v), p.v, static_cast<__nv_bfloat16*>(o), lse, hdr, list, p.fill_tail,
               p.status, p.wait_ns};
   int dev = 0, sms = 0;
