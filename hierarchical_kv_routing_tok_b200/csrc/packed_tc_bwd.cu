@@ -215,7 +215,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = (int)(J % KS);                         // the current phase and the one before)
         ok = mbar_wait_w(kv_full(s), (uint32_t)((J / KS) & 1), abort_flag, p.status, p.wait_ns);
         if (ok && x.len - j * kBN < kBN) {
-          clean_tile(sbase + L::kK + s * kTileBytes, kBN, kHalfBytes, x.len - j * kBN, false);
+          zero_rows(sbase + L::kK + s * kTileBytes, kBN, kHalfBytes, x.len - j * kBN);
           __syncwarp();
           if (lane == 0) mbar_arrive(k_clean(s));
         }
@@ -608,8 +608,8 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (++i == Tq) {
         i = 0;
         const int rows = (len - t0 - (Tq - 1) * tq) * p.pk;
-        clean_tile(sbase + L::kQ + s * kQTile, BQ, kQHalf, rows, false);
-        clean_tile(sbase + L::kDO + s * kQTile, BQ, kQHalf, rows, false);
+        zero_rows(sbase + L::kQ + s * kQTile, BQ, kQHalf, rows);
+        zero_rows(sbase + L::kDO + s * kQTile, BQ, kQHalf, rows);
         __syncwarp();
         if (lane == 0) mbar_arrive(q_clean(s));
       }

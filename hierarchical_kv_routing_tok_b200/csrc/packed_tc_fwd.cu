@@ -190,7 +190,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = mbar_wait_w(v_full(s), (uint32_t)((J / VS) & 1), abort_flag, p.status, p.wait_ns);
         if (!ok) break;
         if (j < jd) continue;
-        any |= clean_tile(sbase + L::kV + s * kTileBytes, kBN, kHalfBytes, x.len - j * kBN, true);
+        const uint32_t tile = sbase + L::kV + s * kTileBytes;
+        if (x.len - j * kBN < kBN) {
+          zero_rows(tile, kBN, kHalfBytes, x.len - j * kBN);
+          __syncwarp();
+        }
+        any |= zero_not_finite(tile);
         if (lane == 0) not_finite[k & 3] = any;         // (the first query tile may end before the second)
         __syncwarp();
         if (lane == 0) mbar_arrive(v_clean(s));
