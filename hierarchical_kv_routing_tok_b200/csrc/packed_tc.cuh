@@ -32,6 +32,29 @@ __device__ __forceinline__ int64_t unit_of_cta(int k, int c, int G) {
   return (k & 1) ? (2 * round + 2) * G - 1 - c : 2 * round * G + c;
 }
 
+// 64 bytes of a row as bf16: whole 32-byte sectors when the tensor is 32-byte aligned.
+__device__ __forceinline__ void store32(__nv_bfloat16* dst, const uint32_t (&pk)[16], bool v8) {
+  if (v8) {
+#pragma unroll
+    for (int y = 0; y < 2; ++y)
+      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 16 * y), "r"(pk[8 * y]),
+                   "r"(pk[8 * y + 1]), "r"(pk[8 * y + 2]), "r"(pk[8 * y + 3]), "r"(pk[8 * y + 4]), "r"(pk[8 * y + 5]),
+                   "r"(pk[8 * y + 6]), "r"(pk[8 * y + 7])
+                   : "memory");
+  } else {
+    uint4* d4 = reinterpret_cast<uint4*>(dst);
+#pragma unroll
+    for (int y = 0; y < 4; ++y) d4[y] = make_uint4(pk[4 * y], pk[4 * y + 1], pk[4 * y + 2], pk[4 * y + 3]);
+  }
+}
+
+// tc::mbar_wait_w with one suspending try in front: what a wait costs when its phase is complete stands between a
+// tensor-core kernel's products.  (Limits below kPollLimitNs poll, so that they expire.)
+__device__ __forceinline__ bool wait_w(uint32_t bar, uint32_t parity, volatile int* abort, int* status, uint64_t limit_ns) {
+  if (limit_ns >= tc::kPollLimitNs && __all_sync(0xffffffffu, tc::mbar_try_wait(bar, parity))) return true;
+  return tc::mbar_wait_w(bar, parity, abort, status, limit_ns);
+}
+
 // ---- pairs of floats: one instruction for two multiply-adds
 __device__ __forceinline__ uint64_t pair(float x, float y) {
   uint64_t r;
@@ -75,13 +98,13 @@ __device__ __forceinline__ void zero_rows(uint32_t tile, int n_rows, uint32_t ha
 __device__ __forceinline__ uint32_t not_finite_mask(uint32_t w) {
   return ((w & 0x7f807f80u) + 0x00800080u) & 0x80008000u;
 }
-// The values of a 128-row tile that are not finite become zeros.  Called by a warp; returns (warp-uniform) whether there
-// are any.  Eight pieces in flight per lane and no branch while all is finite: about 1000 cycles for 32 KB.
-__device__ __forceinline__ bool zero_not_finite(uint32_t tile) {
+// The values of a tile of `pieces` 16-byte pieces (a multiple of 256) that are not finite become zeros.  Called by a warp;
+// returns (warp-uniform) whether there are any.  Eight pieces in flight per lane and no branch while all is finite.
+__device__ __forceinline__ bool zero_not_finite(uint32_t tile, int pieces) {
   const int lane = threadIdx.x & 31;
   uint32_t found = 0;
 #pragma unroll 1
-  for (int b = 0; b < 2048; b += 256) {                                 // 16-byte pieces of the tile
+  for (int b = 0; b < pieces; b += 256) {
     uint32_t w[8][4], any = 0;
 #pragma unroll
     for (int y = 0; y < 8; ++y)

@@ -39,22 +39,6 @@ struct BwdParams {
   uint64_t wait_ns;
 };
 
-// 64 bytes of a row as bf16: whole 32-byte sectors when the tensor is 32-byte aligned.
-__device__ __forceinline__ void store32(__nv_bfloat16* dst, const uint32_t (&pk)[16], bool v8) {
-  if (v8) {
-#pragma unroll
-    for (int y = 0; y < 2; ++y)
-      asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(dst + 16 * y), "r"(pk[8 * y]),
-                   "r"(pk[8 * y + 1]), "r"(pk[8 * y + 2]), "r"(pk[8 * y + 3]), "r"(pk[8 * y + 4]), "r"(pk[8 * y + 5]),
-                   "r"(pk[8 * y + 6]), "r"(pk[8 * y + 7])
-                   : "memory");
-  } else {
-    uint4* d4 = reinterpret_cast<uint4*>(dst);
-#pragma unroll
-    for (int y = 0; y < 4; ++y) d4[y] = make_uint4(pk[4 * y], pk[4 * y + 1], pk[4 * y + 2], pk[4 * y + 3]);
-  }
-}
-
 // ======================================================================================== dQ
 namespace dq {
 

@@ -7,12 +7,14 @@
 // (16 per clock and SM).  A unit is two query tiles of 128 rows (packed_tc.cuh) that share their K/V tiles of
 // 128 keys.  One CTA per SM walks the units of the work list, heaviest first; barriers and rings count tiles
 // across units, so the next unit's loads and first products run under the epilogue of the current one.
-// Warps: 0 loads Q and K, 2 loads V (TMA, rings of two), 1 issues the products, 4-7 and 8-11 are the
-// softmax of the two tiles (thread = row), 3 cleans the V tiles that masked rows meet: on the causal
-// diagonal p = 0 meets values that the row does not attend, and 0 * inf is not 0.  Values there that are not
+// Warps: 0 loads (TMA; a ring of two items, V(j) with K(j+1), so that the issuing warp waits once for both), 1 issues the
+// products, 4-7 and 8-11 are the softmax of the two tiles (thread = row), 3 checks the V tiles that masked rows meet: on
+// the causal diagonal p = 0 meets values that the row does not attend, and 0 * inf is not 0.  Values there that are not
 // finite become 0 before the product, and the epilogue adds them to the rows that do attend them.
 // TMEM: S_0 S_1 O_0 O_1 (128 columns each); P_i as bf16 over the first half of S_i.  Issue order S_0 S_1 |
 // PV_0 S_0' PV_1 S_1' | ...: S_i(j+1) complete implies PV_i(j) complete, so no barrier guards the rescale.
+// (Measured slower: S in two buffers of 64 keys, 2406 against 1903 us at 16K, whose products of 64 columns wait for shared
+// memory, 48 cycles in place of 32; a part of the exponentials by a polynomial on the FMA pipe, 2160 -> 2550 us.)
 #include <cuda_bf16.h>
 
 #include "packed_tc.cuh"
@@ -25,7 +27,7 @@ using namespace tc;
 namespace {
 
 constexpr float kRescaleThreshold = 8.f;   // log2 units
-constexpr int KS = 2, VS = 2;              // ring stages
+constexpr int NS = 2;                      // ring items
 constexpr int kThreads = 384;
 
 struct FwdParams {
@@ -47,12 +49,11 @@ struct FwdParams {
 struct FwdSmem {
   static constexpr uint32_t kQ = 0;
   static constexpr uint32_t kK = kQ + 2 * kTileBytes;
-  static constexpr uint32_t kV = kK + KS * kTileBytes;
-  static constexpr uint32_t kO = kV + VS * kTileBytes;          // 4 KB per softmax warp: 32 rows x 64 dims of o
+  static constexpr uint32_t kV = kK + NS * kTileBytes;
+  static constexpr uint32_t kO = kV + NS * kTileBytes;          // 4 KB per softmax warp: 32 rows x 64 dims of o
   static constexpr uint32_t kBar = kO + 8 * 4096;
-  // q_full, q_empty, k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], v_clean[VS], s_full[2], p_full[2],
-  // o_full[2], mma_done, p_most[2]
-  static constexpr int kNumBars = 2 + 2 * KS + 3 * VS + 6 + 3;
+  // q_full, q_empty, full[NS], empty[NS], v_clean[NS], s_full[2], p_full[2], o_full[2], mma_done
+  static constexpr int kNumBars = 2 + 3 * NS + 6 + 1;
   static constexpr uint32_t kMisc = kBar + 8 * kNumBars;        // TMEM address, abort, flags of 4 units
   static constexpr uint32_t kBytes = kMisc + 32;
 };
@@ -91,16 +92,13 @@ __global__ void __launch_bounds__(kThreads, 1)
   const uint32_t sbase = smem_u32(smem);
   auto BAR = [&](int i) { return sbase + L::kBar + 8u * (uint32_t)i; };
   const uint32_t q_full = BAR(0), q_empty = BAR(1);
-  auto k_full = [&](int s) { return BAR(2 + s); };
-  auto k_empty = [&](int s) { return BAR(2 + KS + s); };
-  auto v_full = [&](int s) { return BAR(2 + 2 * KS + s); };
-  auto v_empty = [&](int s) { return BAR(2 + 2 * KS + VS + s); };
-  auto v_clean = [&](int s) { return BAR(2 + 2 * KS + 2 * VS + s); };
-  auto s_full = [&](int i) { return BAR(2 + 2 * KS + 3 * VS + i); };
-  auto p_full = [&](int i) { return BAR(4 + 2 * KS + 3 * VS + i); };
-  auto o_full = [&](int i) { return BAR(6 + 2 * KS + 3 * VS + i); };
-  const uint32_t mma_done = BAR(8 + 2 * KS + 3 * VS);
-  auto p_most = [&](int i) { return BAR(9 + 2 * KS + 3 * VS + i); };    // P of the tile's first 96 keys
+  auto full = [&](int s) { return BAR(2 + s); };
+  auto empty = [&](int s) { return BAR(2 + NS + s); };
+  auto v_clean = [&](int s) { return BAR(2 + 2 * NS + s); };
+  auto s_full = [&](int i) { return BAR(2 + 3 * NS + i); };
+  auto p_full = [&](int i) { return BAR(4 + 3 * NS + i); };
+  auto o_full = [&](int i) { return BAR(6 + 3 * NS + i); };
+  const uint32_t mma_done = BAR(8 + 3 * NS);
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
   // whether a unit's diagonal tiles hold values that are not finite: unit k in slot k mod 4 (the cleaner is at
@@ -111,19 +109,14 @@ __global__ void __launch_bounds__(kThreads, 1)
   if (threadIdx.x == 0) {
     mbar_init(q_full, 1);
     mbar_init(q_empty, 1);
-    for (int s = 0; s < KS; ++s) {
-      mbar_init(k_full(s), 1);
-      mbar_init(k_empty(s), 1);
-    }
-    for (int s = 0; s < VS; ++s) {
-      mbar_init(v_full(s), 1);
-      mbar_init(v_empty(s), 1);
+    for (int s = 0; s < NS; ++s) {
+      mbar_init(full(s), 1);
+      mbar_init(empty(s), 1);
       mbar_init(v_clean(s), 1);
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full(i), 1);
       mbar_init(p_full(i), 4);
-      mbar_init(p_most(i), 4);
       mbar_init(o_full(i), 1);
     }
     mbar_init(mma_done, 1);
@@ -143,51 +136,49 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t n_units = (int64_t)p.hdr->n_tiles[0] * p.hu;
   Unit x;
 
-  if (warp == 0 || warp == 2) {
-    // ======================= TMA producers: warp 0 Q and K, warp 2 V
+  if (warp == 0) {
+    // ======================= TMA producer: per unit Q, then the items K(0) | V(0) K(1) | ... | V(T-1)
     if (lane == 0) {
-      const bool kv = warp == 2;
-      const CUtensorMap* map = kv ? &tm_v : &tm_k;
-      const int NS = kv ? VS : KS;
       int64_t J = 0;
       bool ok = true;
       int loads = 0;
       for (int k = 0; ok && load_unit(p, n_units, k, &x); ++k) {
-        if (!kv) {
-          if (k > 0 && !(ok = mbar_wait(q_empty, (k - 1) & 1, abort_flag, p.status, p.wait_ns))) break;
-          mbar_arrive_expect_tx(q_full, 2 * kTileBytes);
-          for (int i = 0; i < 2; ++i)
-            for (int h = 0; h < 2; ++h)
-              tma_load_3d(sbase + L::kQ + i * kTileBytes + h * kHalfBytes, &tm_q, 64 * h, x.h0,
-                          x.start + x.t0 + i * p.tp, q_full);
-          ++loads;
-        }
-        for (int j = 0; j < x.Tmax; ++j, ++J) {
+        if (k > 0 && !(ok = mbar_wait(q_empty, (k - 1) & 1, abort_flag, p.status, p.wait_ns))) break;
+        mbar_arrive_expect_tx(q_full, 2 * kTileBytes);
+        for (int i = 0; i < 2; ++i)
+          for (int h = 0; h < 2; ++h)
+            tma_load_3d(sbase + L::kQ + i * kTileBytes + h * kHalfBytes, &tm_q, 64 * h, x.h0, x.start + x.t0 + i * p.tp,
+                        q_full);
+        ++loads;
+        for (int j = -1; j < x.Tmax; ++j, ++J) {
           const int s = (int)(J % NS);
-          const uint32_t full = kv ? v_full(s) : k_full(s), empty = kv ? v_empty(s) : k_empty(s);
-          if (!(ok = mbar_wait(empty, (uint32_t)((J / NS) & 1) ^ 1, abort_flag, p.status, p.wait_ns))) break;
-          mbar_arrive_expect_tx(full, kTileBytes);
-          const uint32_t dst = sbase + (kv ? L::kV : L::kK) + s * kTileBytes;
-          tma_load_3d(dst, map, 0, x.kh, x.start + j * kBN, full);
-          tma_load_3d(dst + kHalfBytes, map, 64, x.kh, x.start + j * kBN, full);
+          if (!(ok = mbar_wait(empty(s), (uint32_t)((J / NS) & 1) ^ 1, abort_flag, p.status, p.wait_ns))) break;
+          const bool has_v = j >= 0, has_k = j + 1 < x.Tmax;
+          mbar_arrive_expect_tx(full(s), has_v && has_k ? 2 * kTileBytes : kTileBytes);
+          if (has_v)
+            for (int h = 0; h < 2; ++h)
+              tma_load_3d(sbase + L::kV + s * kTileBytes + h * kHalfBytes, &tm_v, 64 * h, x.kh, x.start + j * kBN, full(s));
+          if (has_k)
+            for (int h = 0; h < 2; ++h)
+              tma_load_3d(sbase + L::kK + s * kTileBytes + h * kHalfBytes, &tm_k, 64 * h, x.kh, x.start + (j + 1) * kBN, full(s));
         }
       }
       // every load of this warp has landed before the CTA may exit
       for (int64_t j = J > NS ? J - NS : 0; j < J; ++j)
-        drain_wait(kv ? v_full((int)(j % NS)) : k_full((int)(j % NS)), (uint32_t)((j / NS) & 1), p.status);
+        drain_wait(full((int)(j % NS)), (uint32_t)((j / NS) & 1), p.status);
       if (loads) drain_wait(q_full, (loads - 1) & 1, p.status);
     }
     __syncwarp();
   } else if (warp == 3) {
-    // ======================= cleaner of the V tiles at or behind the unit's first token
+    // ======================= check of the V tiles at or behind the unit's first token
     int64_t J = 0;
     bool ok = true;
     for (int k = 0; ok && load_unit(p, n_units, k, &x); ++k) {
       const int jd = x.t0 / kBN;
       bool any = false;
-      for (int j = 0; j < x.Tmax; ++j, ++J) {           // (every tile is waited for: a parity names only the
-        const int s = (int)(J % VS);                    // current phase and the one before)
-        ok = mbar_wait_w(v_full(s), (uint32_t)((J / VS) & 1), abort_flag, p.status, p.wait_ns);
+      for (int j = -1; j < x.Tmax; ++j, ++J) {          // (every item is waited for: a parity names only the current
+        const int s = (int)(J % NS);                    // phase and the one before)
+        ok = mbar_wait_w(full(s), (uint32_t)((J / NS) & 1), abort_flag, p.status, p.wait_ns);
         if (!ok) break;
         if (j < jd) continue;
         const uint32_t tile = sbase + L::kV + s * kTileBytes;
@@ -195,89 +186,64 @@ __global__ void __launch_bounds__(kThreads, 1)
           zero_rows(tile, kBN, kHalfBytes, x.len - j * kBN);
           __syncwarp();
         }
-        any |= zero_not_finite(tile);
+        any |= zero_not_finite(tile, kBN * 16);
         if (lane == 0) not_finite[k & 3] = any;         // (the first query tile may end before the second)
         __syncwarp();
         if (lane == 0) mbar_arrive(v_clean(s));
       }
     }
   } else if (warp == 1) {
-    // ======================= MMA issuer: the whole warp runs the loop, one elected lane issues
+    // ======================= MMA issuer: the whole warp runs the loop, one elected lane issues.  Per tile it waits for the
+    // item, P_0 and P_1, and commits S_0, S_1 and the item: each wait costs the tensor pipe about 100 cycles.
     constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kBN, false);
     constexpr uint32_t idesc_pv = idesc_bf16_f32(128, kD, true);
     uint64_t qd[2][8], kd[8], vd[8];
 #pragma unroll
     for (int i = 0; i < 2; ++i) kmajor_descs(qd[i], sbase + L::kQ + i * kTileBytes, kHalfBytes, 1024);
+    const uint64_t k0 = smem_desc_sw128(sbase + L::kK, 16, 1024), v0 = smem_desc_sw128(sbase + L::kV, kHalfBytes, 1024);
     int64_t J = 0;
     int np[2] = {0, 0};                    // P tiles taken of each query tile
-    int cleaned[VS] = {0, 0};              // cleaned tiles taken from each V stage
+    uint32_t clean_phase = 0;              // bit s: parity of the next checked item in slot s
     bool ok = true;
     for (int k = 0; ok && load_unit(p, n_units, k, &x); ++k) {
-      ok = mbar_wait_w(q_full, k & 1, abort_flag, p.status, p.wait_ns) &&
-           mbar_wait_w(k_full((int)(J % KS)), (uint32_t)((J / KS) & 1), abort_flag, p.status, p.wait_ns);
-      if (!ok) break;
-      tc_fence_after();
-      kmajor_descs(kd, sbase + L::kK + (int)(J % KS) * kTileBytes, kHalfBytes, 1024);
-#pragma unroll
-      for (int i = 0; i < 2; ++i) {
-        if (x.T[i] == 0) continue;
-#pragma unroll
-        for (int ks = 0; ks < 8; ++ks) mma_ss_w(tmem + i * 128, qd[i][ks], kd[ks], idesc_qk, ks > 0);
-        mma_commit_w(s_full(i));
-      }
-      mma_commit_w(k_empty((int)(J % KS)));
-      if (x.Tmax == 1) mma_commit_w(q_empty);
+      ok = wait_w(q_full, k & 1, abort_flag, p.status, p.wait_ns);
       const int jd = x.t0 / kBN;
-      for (int j = 0; j < x.Tmax; ++j, ++J) {
-        const int s = (int)(J % VS);
+      for (int j = -1; ok && j < x.Tmax; ++j, ++J) {
+        const int s = (int)(J % NS);
         if (j >= jd) {
-          ok = mbar_wait_w(v_clean(s), cleaned[s] & 1, abort_flag, p.status, p.wait_ns);
-          ++cleaned[s];
+          ok = wait_w(v_clean(s), (clean_phase >> s) & 1u, abort_flag, p.status, p.wait_ns);
+          clean_phase ^= 1u << s;
         } else {
-          ok = mbar_wait_w(v_full(s), (uint32_t)((J / VS) & 1), abort_flag, p.status, p.wait_ns);
+          ok = wait_w(full(s), (uint32_t)((J / NS) & 1), abort_flag, p.status, p.wait_ns);
         }
         if (!ok) break;
         tc_fence_after();
-        mnmajor_descs<8>(vd, sbase + L::kV + s * kTileBytes, kHalfBytes, 1024);
-        const int sn = (int)((J + 1) % KS);
-        bool have_k = false;               // the next K tile has landed
+        const uint64_t soff = (uint64_t)(s * (kTileBytes >> 4));
+        kmajor_from_base(kd, k0 + soff, kHalfBytes >> 4);
+        mnmajor_from_base<8>(vd, v0 + soff, (2 * 1024u) >> 4);
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
           if (j >= x.T[i]) continue;
-          ok = mbar_wait_w(p_most(i), np[i] & 1, abort_flag, p.status, p.wait_ns);
-          if (!ok) break;
-          tc_fence_after();
+          if (j >= 0) {
+            ok = wait_w(p_full(i), np[i] & 1, abort_flag, p.status, p.wait_ns);
+            if (!ok) break;
+            ++np[i];
+            tc_fence_after();
 #pragma unroll
-          for (int ks = 0; ks < 6; ++ks)
-            mma_ts_w(tmem + 256 + i * 128, tmem + i * 128 + ks * 8, vd[ks], idesc_pv, (j > 0 || ks > 0));
-          ok = mbar_wait_w(p_full(i), np[i] & 1, abort_flag, p.status, p.wait_ns);
-          if (!ok) break;
-          ++np[i];
-          tc_fence_after();
-#pragma unroll
-          for (int ks = 6; ks < 8; ++ks)
-            mma_ts_w(tmem + 256 + i * 128, tmem + i * 128 + ks * 8, vd[ks], idesc_pv, 1);
+            for (int ks = 0; ks < 8; ++ks)
+              mma_ts_w(tmem + 256 + i * 128, tmem + i * 128 + ks * 8, vd[ks], idesc_pv, (j > 0 || ks > 0));
+          }
           if (j + 1 < x.T[i]) {
-            if (!have_k) {
-              ok = mbar_wait_w(k_full(sn), (uint32_t)(((J + 1) / KS) & 1), abort_flag, p.status, p.wait_ns);
-              if (!ok) break;
-              tc_fence_after();
-              kmajor_descs(kd, sbase + L::kK + sn * kTileBytes, kHalfBytes, 1024);
-              have_k = true;
-            }
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks) mma_ss_w(tmem + i * 128, qd[i][ks], kd[ks], idesc_qk, ks > 0);
             mma_commit_w(s_full(i));
-          } else {
+          } else if (j >= 0) {
             mma_commit_w(o_full(i));       // the last product of this query tile
           }
         }
         if (!ok) break;
-        mma_commit_w(v_empty(s));
-        if (j + 1 < x.Tmax) {
-          mma_commit_w(k_empty(sn));
-          if (j + 2 == x.Tmax) mma_commit_w(q_empty);      // the unit's last S products are issued
-        }
+        mma_commit_w(empty(s));
+        if (j + 2 == x.Tmax) mma_commit_w(q_empty);          // the unit's last S products are issued
       }
     }
     mma_commit_w(mma_done);
@@ -303,7 +269,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t_pos = x.t0 + i * p.tp + (r >> p.pk_shift);     // (rows past the sequence compute, and store nothing)
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < T; ++j, ++ns) {
-        ok = mbar_wait_w(s_full(i), ns & 1, abort_flag, p.status, p.wait_ns);
+        ok = wait_w(s_full(i), ns & 1, abort_flag, p.status, p.wait_ns);
         if (!ok) break;
         tc_fence_after();
         const int nvalid = t_pos - j * kBN + 1;         // keys of this tile that the row attends
@@ -371,12 +337,6 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int cc = 1; cc < 4; ++cc) {
           probs(cc, mref, pk);
-          if (cc == 3) {                                // the first 96 keys' product starts under the rest
-            tmem_wait_st();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(p_most(i));
-          }
           tmem_st16(tS + cc * 16, pk);
         }
         float r0, r1, r2, r3;
@@ -388,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full(i));
       }
-      if (ok) ok = mbar_wait_w(o_full(i), no & 1, abort_flag, p.status, p.wait_ns);
+      if (ok) ok = wait_w(o_full(i), no & 1, abort_flag, p.status, p.wait_ns);
       ++no;
       if (!ok) break;
       tc_fence_after();
