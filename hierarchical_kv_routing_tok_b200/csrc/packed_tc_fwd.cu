@@ -7,8 +7,8 @@
 // (16 per clock and SM).  A unit is two query tiles of 128 rows (packed_tc.cuh) that share their K/V tiles of
 // 128 keys.  One CTA per SM walks the units of the work list, heaviest first; barriers and rings count tiles
 // across units, so the next unit's loads and first products run under the epilogue of the current one.
-// Warps: 0 loads (TMA; a ring of two items, V(j) with K(j+1), so that the issuing warp waits once for both), 1 issues the
-// products, 4-7 and 8-11 are the softmax of the two tiles (thread = row), 3 checks the V tiles that masked rows meet: on
+// Warps: 16 loads (TMA; a ring of two items, V(j) with K(j+1), so that the issuing warp waits once for both), 17 issues the
+// products, 0-7 and 8-15 are the softmax of the two tiles (thread = half a row), 18 checks the V tiles that masked rows meet: on
 // the causal diagonal p = 0 meets values that the row does not attend, and 0 * inf is not 0.  Values there that are not
 // finite become 0 before the product, and the epilogue adds them to the rows that do attend them.
 // TMEM: S_0 S_1 O_0 O_1 (128 columns each); P_i as bf16 over the first half of S_i.  Issue order S_0 S_1 |
@@ -28,7 +28,9 @@ namespace {
 
 constexpr float kRescaleThreshold = 8.f;   // log2 units
 constexpr int NS = 2;                      // ring items
-constexpr int kThreads = 384;
+constexpr int kSoftmax = 512;              // threads of the 16 softmax warps
+constexpr int kMmaWarp = 17;
+constexpr int kThreads = kSoftmax + 96;
 
 struct FwdParams {
   int Hq, Hkv, G, pk, pk_shift, tp;        // pk = 1 << pk_shift; tp: tokens per query tile, 128 / pk
@@ -50,12 +52,13 @@ struct FwdSmem {
   static constexpr uint32_t kQ = 0;
   static constexpr uint32_t kK = kQ + 2 * kTileBytes;
   static constexpr uint32_t kV = kK + NS * kTileBytes;
-  static constexpr uint32_t kO = kV + NS * kTileBytes;          // 4 KB per softmax warp: 32 rows x 64 dims of o
-  static constexpr uint32_t kBar = kO + 8 * 4096;
+  static constexpr uint32_t kO = kV + NS * kTileBytes;          // 2 KB per softmax warp: 32 rows x 32 dims of o
+  static constexpr uint32_t kBar = kO + 16 * 2048;
   // q_full, q_empty, full[NS], empty[NS], v_clean[NS], s_full[2], p_full[2], o_full[2], mma_done
   static constexpr int kNumBars = 2 + 3 * NS + 6 + 1;
   static constexpr uint32_t kMisc = kBar + 8 * kNumBars;        // TMEM address, abort, flags of 4 units
-  static constexpr uint32_t kBytes = kMisc + 32;
+  static constexpr uint32_t kNeed = kMisc + 32;                 // [tile parity][pair of warps][half]
+  static constexpr uint32_t kBytes = kNeed + 2 * 8 * 2 * 4;
 };
 static_assert(FwdSmem::kBytes + 1024 <= 227 * 1024, "shared memory");
 
@@ -116,14 +119,14 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int i = 0; i < 2; ++i) {
       mbar_init(s_full(i), 1);
-      mbar_init(p_full(i), 4);
+      mbar_init(p_full(i), 8);
       mbar_init(o_full(i), 1);
     }
     mbar_init(mma_done, 1);
     *abort_flag = 0;
     mbar_fence_init();
   }
-  if (warp == 1) {
+  if (warp == kMmaWarp) {
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
@@ -136,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int64_t n_units = (int64_t)p.hdr->n_tiles[0] * p.hu;
   Unit x;
 
-  if (warp == 0) {
+  if (warp == 16) {
     // ======================= TMA producer: per unit Q, then the items K(0) | V(0) K(1) | ... | V(T-1)
     if (lane == 0) {
       int64_t J = 0;
@@ -169,7 +172,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (loads) drain_wait(q_full, (loads - 1) & 1, p.status);
     }
     __syncwarp();
-  } else if (warp == 3) {
+  } else if (warp == 18) {
     // ======================= check of the V tiles at or behind the unit's first token
     int64_t J = 0;
     bool ok = true;
@@ -192,7 +195,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (lane == 0) mbar_arrive(v_clean(s));
       }
     }
-  } else if (warp == 1) {
+  } else if (warp == kMmaWarp) {
     // ======================= MMA issuer: the whole warp runs the loop, one elected lane issues.  Per tile it waits for the
     // item, P_0 and P_1, and commits S_0, S_1 and the item: each wait costs the tensor pipe about 100 cycles.
     constexpr uint32_t idesc_qk = idesc_bf16_f32(128, kBN, false);
@@ -231,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc_fence_after();
 #pragma unroll
             for (int ks = 0; ks < 8; ++ks)
-              mma_ts_w(tmem + 256 + i * 128, tmem + i * 128 + ks * 8, vd[ks], idesc_pv, (j > 0 || ks > 0));
+              mma_ts_w(tmem + 256 + i * 128, tmem + i * 128 + (ks >> 2) * 64 + (ks & 3) * 8, vd[ks], idesc_pv, (j > 0 || ks > 0));
           }
           if (j + 1 < x.T[i]) {
 #pragma unroll
@@ -248,48 +251,62 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     mma_commit_w(mma_done);
     drain_wait(mma_done, 0, p.status);
-  } else if (warp >= 4) {
-    // ======================= softmax and epilogue, one warpgroup per query tile
+  } else {
+    // ======================= softmax and epilogue: two warpgroups per query tile, 64 keys of each tile (and 64 dims of the
+    // output) each.  The two warps of a row (a pair) keep the same maximum m; each has the sum of its keys.
+    const int st = threadIdx.x;
     if (p.fill_tail) {
-      const int64_t worker = (int64_t)blockIdx.x * 256 + (threadIdx.x - 128), workers = (int64_t)gridDim.x * 256;
+      const int64_t worker = (int64_t)blockIdx.x * kSoftmax + st, workers = (int64_t)gridDim.x * kSoftmax;
       fill_tail_rows(p.o, p.Hq, p.hdr->end, p.total, worker, workers);
       fill_tail_lse(p.lse, p.Hq, p.hdr->end, p.total, worker, workers);
     }
-    const int i = (warp - 4) >> 2;
-    const int quarter = warp & 3;
+    const int i = st >> 8, half = (st >> 7) & 1;
+    const int quarter = warp & 3, pair_id = 4 * i + quarter;
     const int r = quarter * 32 + lane;                  // row of the query tile = TMEM lane
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
-    const uint32_t tS = tmem + lane_off + i * 128;
-    const uint32_t tO = tmem + lane_off + 256 + i * 128;
+    const uint32_t tS = tmem + lane_off + i * 128 + 64 * half;
+    const uint32_t tO = tmem + lane_off + 256 + i * 128 + 64 * half;
+    volatile int* s_need = reinterpret_cast<volatile int*>(smem + L::kNeed) + 2 * pair_id;      // + 16 * parity + half
+    // a row's maximum or sum for the other warp: in the writer's part of the output staging
+    volatile float* s_row = reinterpret_cast<volatile float*>(smem + L::kO) + (8 * i + quarter) * 512 + lane;   // + 2048 * half
+    auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + pair_id) : "memory"); };
     int ns = 0, no = 0;                                 // S tiles, outputs taken
     bool ok = true;
     for (int k = 0; ok && load_unit(p, n_units, k, &x); ++k) {
       const int T = x.T[i];
       if (T == 0) continue;
-      const int t_pos = x.t0 + i * p.tp + (r >> p.pk_shift);     // (rows past the sequence compute, and store nothing)
+      const int t_pos = x.t0 + i * p.tp + (r >> p.pk_shift);    // (rows past the sequence compute, and store nothing)
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < T; ++j, ++ns) {
         ok = wait_w(s_full(i), ns & 1, abort_flag, p.status, p.wait_ns);
-        if (!ok) break;
         tc_fence_after();
-        const int nvalid = t_pos - j * kBN + 1;         // keys of this tile that the row attends
-        // the whole 128-column row in one TMEM round trip
-        uint32_t v[128];
+        const int nvalid = t_pos - j * kBN + 1 - 64 * half;     // of this warp's keys, those that the row attends
+        uint32_t v[64];                                 // in one TMEM round trip
         tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
         tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
-        tmem_ld32(tS + 64, *reinterpret_cast<uint32_t(*)[32]>(&v[64]));
-        tmem_ld32(tS + 96, *reinterpret_cast<uint32_t(*)[32]>(&v[96]));
         tmem_wait_ld();
-        const bool masked = __any_sync(0xffffffffu, nvalid < kBN);
-        if (masked) {
+        if (__any_sync(0xffffffffu, nvalid < 64)) {
 #pragma unroll
-          for (int e = 0; e < kBN; ++e)
+          for (int e = 0; e < 64; ++e)
             if (e >= nvalid) v[e] = __float_as_uint(-INFINITY);
         }
-        // Probabilities of 32 keys, their sum in float32, and as bf16 (the product's operand type).
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // of the raw products (the scale is positive)
+#pragma unroll
+        for (int e = 0; e < 64; e += 8)
+#pragma unroll
+          for (int y = 0; y < 4; ++y)
+            mx[y] = max3(mx[y], __uint_as_float(v[e + 2 * y]), __uint_as_float(v[e + 2 * y + 1]));
+        float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
+        // The reference moves only when the maximum grows by more than 2^8: rarely.  Each warp tells the other whether its
+        // keys ask for it, and does the first 32 keys with the standing reference meanwhile.
+        auto asks = [&](float y) { return y > m + kRescaleThreshold || (m == -INFINITY && y > -INFINITY); };
+        const bool any = __any_sync(0xffffffffu, asks(mt));
+        if (lane == 0) s_need[16 * (j & 1) + half] = ok ? any : 2;      // (2: a wait expired; both warps leave here)
         const uint64_t c2 = pair(p.scale_log2, p.scale_log2);
         uint64_t rs[2] = {0ull, 0ull};
-        auto probs = [&](int cc, float ref, uint32_t(&pk)[16]) {
+        uint32_t pk[16];
+        auto probs = [&](int cc) {                      // of 32 keys: their sum in float32, and as bf16 (the operand type)
+          const float ref = m == -INFINITY ? 0.f : m;
           const uint64_t mr2 = pair(-ref, -ref);
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
@@ -301,24 +318,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             pk[e >> 1] = pack_bf16(p0, p1);
           }
         };
-        // The reference moves only when the maximum grows by more than 2^8, so the first 32 keys start with the old one
-        // while the maximum is still being found, and are done again in the rare case that it moves.
-        uint32_t pk[16];
-        probs(0, m == -INFINITY ? 0.f : m, pk);
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // of the raw products (the scale is positive)
-#pragma unroll
-        for (int e = 0; e < kBN; e += 8)
-#pragma unroll
-          for (int y = 0; y < 4; ++y)
-            mx[y] = max3(mx[y], __uint_as_float(v[e + 2 * y]), __uint_as_float(v[e + 2 * y + 1]));
-        const float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
-        const bool need = mt > m + kRescaleThreshold || (m == -INFINITY && mt > -INFINITY);
-        if (__any_sync(0xffffffffu, need)) {
-          const float mnew = need ? mt : m;
-          const float alpha = need ? ex2(m - mnew) : 1.f;             // m = -inf -> 0
+        probs(0);
+        pair_sync();
+        const int other = s_need[16 * (j & 1) + (half ^ 1)];
+        ok = ok && other != 2;
+        if (!ok) break;
+        if (any || other) {
+          s_row[2048 * half] = mt;
+          pair_sync();
+          mt = fmaxf(mt, s_row[2048 * (half ^ 1)]);
+          pair_sync();                                  // both have read
+          const bool move = asks(mt);
+          const float mnew = move ? mt : m, alpha = move ? ex2(m - mnew) : 1.f;      // m = -inf -> 0
           if (j > 0) {
 #pragma unroll 1
-            for (int cc = 0; cc < 4; ++cc) {
+            for (int cc = 0; cc < 2; ++cc) {            // (S(j) complete implies that the product before it is in O)
               uint32_t o[32];
               tmem_ld32(tO + cc * 32, o);
               tmem_wait_ld();
@@ -330,15 +344,17 @@ __global__ void __launch_bounds__(kThreads, 1)
           l *= alpha;
           m = mnew;
           rs[0] = rs[1] = 0ull;
-          probs(0, m == -INFINITY ? 0.f : m, pk);
-        }
-        const float mref = (m == -INFINITY) ? 0.f : m;
-        tmem_st16(tS, pk);
+          tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));   // (not kept in registers for this)
+          tmem_wait_ld();
 #pragma unroll
-        for (int cc = 1; cc < 4; ++cc) {
-          probs(cc, mref, pk);
-          tmem_st16(tS + cc * 16, pk);
+          for (int e = 0; e < 32; ++e)
+            if (e >= nvalid) v[e] = __float_as_uint(-INFINITY);
+          probs(0);
         }
+        // P stays within this warp's own (already read) columns
+        tmem_st16(tS, pk);
+        probs(1);
+        tmem_st16(tS + 16, pk);
         float r0, r1, r2, r3;
         unpair(rs[0], r0, r1);
         unpair(rs[1], r2, r3);
@@ -348,27 +364,33 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(p_full(i));
       }
-      if (ok) ok = wait_w(o_full(i), no & 1, abort_flag, p.status, p.wait_ns);
+      if (!ok) break;
+      ok = wait_w(o_full(i), no & 1, abort_flag, p.status, p.wait_ns);
       ++no;
+      if (lane == 0) s_need[16 * (T & 1) + half] = ok ? 0 : 2;
+      s_row[2048 * half] = l;
+      pair_sync();
+      l = half ? s_row[0] + l : l + s_row[2048];          // the row's sum, in the same order in both warps
+      ok = ok && s_need[16 * (T & 1) + (half ^ 1)] != 2;
+      pair_sync();
       if (!ok) break;
       tc_fence_after();
       const float inv = 1.f / l;
       const bool store = t_pos < x.len;
-      const int h = x.h0 + (r & (p.pk - 1));
-      const int64_t row = (int64_t)x.start + t_pos;
       const bool fix = not_finite[k & 3] != 0;
-      // O / l as bf16, 64 dims at a time through this warp's 4 KB (16-byte pieces at position c ^ (row mod 8): no bank
-      // conflicts), so that the stores to global memory are whole 128-byte lines
-      const uint32_t stage = sbase + L::kO + (uint32_t)(warp - 4) * 4096u;
+      // O / l as bf16, 32 dims at a time through this warp's 2 KB (16-byte pieces at position c ^ (row / 2 mod 4): no bank
+      // conflicts), so that the stores to global memory are whole 64-byte runs
+      const uint32_t stage = sbase + L::kO + (uint32_t)(st >> 5) * 2048u;
 #pragma unroll 1
-      for (int cc = 0; cc < 4; ++cc) {
+      for (int cc = 0; cc < 2; ++cc) {
+        const int d0 = 64 * half + 32 * cc;
         uint32_t v[32];
         tmem_ld32(tO + cc * 32, v);
         tmem_wait_ld();
         if (fix && store) {
           // values of the diagonal tiles that were set to 0 for the product: each adds itself
           for (int u = x.t0 / kBN * kBN; u <= t_pos; ++u) {
-            const __nv_bfloat16* vr = p.v + ((int64_t)x.start + u) * p.vs.t + x.kh * p.vs.h + cc * 32;
+            const __nv_bfloat16* vr = p.v + ((int64_t)x.start + u) * p.vs.t + x.kh * p.vs.h + d0;
 #pragma unroll
             for (int e = 0; e < 32; ++e) {
               const float y = __bfloat162float(vr[e]);
@@ -378,37 +400,36 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
 #pragma unroll
         for (int y = 0; y < 4; ++y) {
-          const uint32_t a = stage + lane * 128u + (((uint32_t)(4 * (cc & 1) + y) ^ (uint32_t)(lane & 7)) << 4);
           uint32_t w4[4];
 #pragma unroll
           for (int e = 0; e < 4; ++e)
             w4[e] = pack_bf16(__uint_as_float(v[8 * y + 2 * e]) * inv, __uint_as_float(v[8 * y + 2 * e + 1]) * inv);
+          const uint32_t a = stage + lane * 64u + (uint32_t)((y ^ ((lane >> 1) & 3)) << 4);
           asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w4[0]), "r"(w4[1]), "r"(w4[2]), "r"(w4[3]) : "memory");
         }
-        if (cc & 1) {
-          __syncwarp();
-          const int c = lane & 7;
+        __syncwarp();
+        const int c = lane & 3;
 #pragma unroll
-          for (int y = 0; y < 8; ++y) {
-            const int rr = 4 * y + (lane >> 3), rt = quarter * 32 + rr;        // row of the warp, of the tile
-            const int t = x.t0 + i * p.tp + (rt >> p.pk_shift);
-            uint32_t w4[4];
-            asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w4[0]), "=r"(w4[1]), "=r"(w4[2]), "=r"(w4[3])
-                         : "r"(stage + rr * 128u + ((uint32_t)(c ^ (rr & 7)) << 4)));
-            if (t < x.len)
-              *reinterpret_cast<uint4*>(p.o + (((int64_t)x.start + t) * p.Hq + x.h0 + (rt & (p.pk - 1))) * kD + 32 * (cc - 1) + 8 * c) =
-                  make_uint4(w4[0], w4[1], w4[2], w4[3]);
-          }
-          __syncwarp();
+        for (int y = 0; y < 4; ++y) {
+          const int rr = 8 * y + (lane >> 2), rt = quarter * 32 + rr;        // row of the warp, of the tile
+          const int t = x.t0 + i * p.tp + (rt >> p.pk_shift);
+          uint32_t w4[4];
+          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w4[0]), "=r"(w4[1]), "=r"(w4[2]), "=r"(w4[3])
+                       : "r"(stage + rr * 64u + (uint32_t)((c ^ ((rr >> 1) & 3)) << 4)));
+          if (t < x.len)
+            *reinterpret_cast<uint4*>(p.o + (((int64_t)x.start + t) * p.Hq + x.h0 + (rt & (p.pk - 1))) * kD + d0 + 8 * c) =
+                make_uint4(w4[0], w4[1], w4[2], w4[3]);
         }
+        __syncwarp();
       }
-      if (store) p.lse[h * p.total + row] = (m + __log2f(l)) * 0.6931471805599453f;
+      if (store && half == 0)
+        p.lse[(x.h0 + (r & (p.pk - 1))) * p.total + (int64_t)x.start + t_pos] = (m + __log2f(l)) * 0.6931471805599453f;
       tc_fence_before();
     }
   }
   tc_fence_before();
   __syncthreads();
-  if (warp == 1) {
+  if (warp == kMmaWarp) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
   }
