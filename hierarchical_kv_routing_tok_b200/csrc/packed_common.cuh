@@ -35,7 +35,7 @@ cudaError_t launch_bwd_f32(const void* q, const void* k, const void* v, const vo
 cudaError_t launch_fwd_tc(const void* q, const void* k, const void* v, void* o, float* lse, const Header* hdr,
                           const Tile* list, const Problem& p, cudaStream_t st);
 cudaError_t launch_bwd_tc(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* d_o,
-                          float* delta, void* dq, void* dk, void* dv, const Header* hdr, const Tile* by_query,
+                          float* stats, void* dq, void* dk, void* dv, const Header* hdr, const Tile* by_query,
                           const Tile* by_key, const Problem& p, cudaStream_t st);
 
 // Rows of no sequence: zeros in a [total, H, 128] output, -inf in lse [H, total].  Called by every

@@ -28,7 +28,7 @@ struct BwdParams {
   float c2, scale;                         // scale * log2(e), scale
   const __nv_bfloat16* o;
   const float* lse;                        // [Hq, total]
-  float* delta;                            // [Hq, total]
+  float* stats;                            // [2][Hq, total]: -lse log2(e), -delta; written by dQ for dK, dV
   __nv_bfloat16* dq;
   __nv_bfloat16* dk;
   __nv_bfloat16* dv;
@@ -183,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int64_t J = 0;
     bool ok = true;
     for (int k = 0; ok && load_unit(p, n_units, k, &x); ++k) {
-      if (k > 0) ok = mbar_wait_w(qdo_empty, (k - 1) & 1, abort_flag, p.status, p.wait_ns);
+      if (k > 0) ok = wait_w(qdo_empty, (k - 1) & 1, abort_flag, p.status, p.wait_ns);
       if (!ok) break;
       if (lane == 0) {
         mbar_arrive_expect_tx(qdo_full, 2 * kTileBytes);
@@ -197,7 +197,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       ++loads;
       for (int j = 0; ok && j < x.T; ++j, ++J) {             // (every tile is waited for: a parity names only
         const int s = (int)(J % KS);                         // the current phase and the one before)
-        ok = mbar_wait_w(kv_full(s), (uint32_t)((J / KS) & 1), abort_flag, p.status, p.wait_ns);
+        ok = wait_w(kv_full(s), (uint32_t)((J / KS) & 1), abort_flag, p.status, p.wait_ns);
         if (ok && x.len - j * kBN < kBN) {
           zero_rows(sbase + L::kK + s * kTileBytes, kBN, kHalfBytes, x.len - j * kBN);
           __syncwarp();
@@ -247,8 +247,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     uint32_t clean_phase = 0;               // bit s: parity of the next cleaned tile in K stage s
     bool have = load_unit(p, n_units, 0, &x);
     if (have) {
-      ok = mbar_wait_w(qdo_full, 0, abort_flag, p.status, p.wait_ns) &&
-           mbar_wait_w(kv_full(0), 0, abort_flag, p.status, p.wait_ns);
+      ok = wait_w(qdo_full, 0, abort_flag, p.status, p.wait_ns) &&
+           wait_w(kv_full(0), 0, abort_flag, p.status, p.wait_ns);
       if (ok) {
         issue_s(0);
         issue_dp(0);
@@ -265,9 +265,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int Tn = last ? xn.T : x.T;
         auto finish_tile = [&]() {          // dQ (+)= dS(J) K(J), then K(J) is free
           const int s = (int)(J % KS);
-          ok = mbar_wait_w(ds_full((int)(J & 1)), (uint32_t)((J >> 1) & 1), abort_flag, p.status, p.wait_ns);
+          ok = wait_w(ds_full((int)(J & 1)), (uint32_t)((J >> 1) & 1), abort_flag, p.status, p.wait_ns);
           if (ok && x.len - j * kBN < kBN) {
-            ok = mbar_wait_w(k_clean(s), (clean_phase >> s) & 1u, abort_flag, p.status, p.wait_ns);
+            ok = wait_w(k_clean(s), (clean_phase >> s) & 1u, abort_flag, p.status, p.wait_ns);
             clean_phase ^= 1u << s;
           }
           if (!ok) return;
@@ -282,13 +282,13 @@ __global__ void __launch_bounds__(kThreads, 1)
           mma_commit_w(dq_ready);
         }
         if (next) {
-          if (last) ok = mbar_wait_w(qdo_full, (k + 1) & 1, abort_flag, p.status, p.wait_ns);
+          if (last) ok = wait_w(qdo_full, (k + 1) & 1, abort_flag, p.status, p.wait_ns);
           if (ok)
-            ok = mbar_wait_w(kv_full((int)((J + 1) % KS)), (uint32_t)(((J + 1) / KS) & 1), abort_flag, p.status, p.wait_ns);
+            ok = wait_w(kv_full((int)((J + 1) % KS)), (uint32_t)(((J + 1) / KS) & 1), abort_flag, p.status, p.wait_ns);
           if (!ok) break;
           issue_s(J + 1);
         }
-        ok = mbar_wait_w(dp_free, (uint32_t)(J & 1), abort_flag, p.status, p.wait_ns);
+        ok = wait_w(dp_free, (uint32_t)(J & 1), abort_flag, p.status, p.wait_ns);
         if (!ok) break;
         if (next) {
           issue_dp(J + 1);
@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const int t_pos = x.t0 + r / p.pk;
       const bool in = t_pos < x.len;
       const int64_t row = (int64_t)x.start + t_pos;
-      const float lse2 = in ? p.lse[head * p.total + row] * kLog2eF : 0.f;
+      const float nlse2 = in ? -p.lse[head * p.total + row] * kLog2eF : 0.f;
       // delta = sum_d dO o O of this row.  Warpgroup w takes columns 32w .. 32w+31: O from global memory (issued
       // before the wait for the Q/dO tile), dO from the swizzled tile (row r: 8-row atom r/8, 16-byte chunk c of a
       // 64-column half at position c ^ (r mod 8)).  The four partial sums meet in TMEM column 384 + 32w (the first
@@ -335,7 +335,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
         for (int c = 0; c < 4; ++c) ov[c] = in ? orow[c] : make_uint4(0, 0, 0, 0);
       }
-      ok = mbar_wait_w(qdo_full, k & 1, abort_flag, p.status, p.wait_ns);
+      ok = wait_w(qdo_full, k & 1, abort_flag, p.status, p.wait_ns);
       if (!ok) break;
       float part;
       {
@@ -362,7 +362,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(delta_bar);
-      ok = mbar_wait_w(delta_bar, k & 1, abort_flag, p.status, p.wait_ns);
+      ok = wait_w(delta_bar, k & 1, abort_flag, p.status, p.wait_ns);
       if (!ok) break;
       tc_fence_after();
       float dl;
@@ -376,24 +376,32 @@ __global__ void __launch_bounds__(kThreads, 1)
         tmem_wait_ld();
         dl = ((__uint_as_float(pv[0]) + __uint_as_float(pv[1])) + __uint_as_float(pv[2])) + __uint_as_float(pv[3]);
       }
-      if (w == 0 && in) p.delta[head * p.total + row] = dl;
+      if (w == 0 && in) {
+        p.stats[head * p.total + row] = nlse2;
+        p.stats[(p.Hq + head) * p.total + row] = -dl;
+      }
+      const uint64_t c2 = pair(p.c2, p.c2), nl2 = pair(nlse2, nlse2), nd2 = pair(-dl, -dl);
       for (int j = 0; j < x.T; ++j, ++J) {
         // P of this warpgroup's 32 keys while dP is still in the tensor pipe; then dP, which frees its columns
-        ok = mbar_wait_w(s_full((int)(J & 1)), (uint32_t)((J >> 1) & 1), abort_flag, p.status, p.wait_ns);
+        ok = wait_w(s_full((int)(J & 1)), (uint32_t)((J >> 1) & 1), abort_flag, p.status, p.wait_ns);
         if (!ok) break;
         tc_fence_after();
         const uint32_t tS = tmem + lane_off + (uint32_t)(J & 1) * 128 + c0;
         // of this warpgroup's keys, those that the row attends (none for a row outside the sequence)
         const int nvalid = in ? t_pos - j * kBN + 1 - c0 : 0;
-        float pr[32];
+        uint64_t pr[16];
         {
           uint32_t sv[32];
           tmem_ld32(tS, sv);
           tmem_wait_ld();
 #pragma unroll
-          for (int e = 0; e < 32; ++e) pr[e] = ex2(fmaf(__uint_as_float(sv[e]), p.c2, -lse2));
+          for (int e = 0; e < 32; e += 2) {
+            float p0, p1;
+            unpair(fma2(pair(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), c2, nl2), p0, p1);
+            pr[e >> 1] = pair(ex2(p0), ex2(p1));
+          }
         }
-        ok = mbar_wait_w(dp_full, (uint32_t)(J & 1), abort_flag, p.status, p.wait_ns);
+        ok = wait_w(dp_full, (uint32_t)(J & 1), abort_flag, p.status, p.wait_ns);
         if (!ok) break;
         tc_fence_after();
         uint32_t dv[32], pk[16];
@@ -402,15 +410,21 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(dp_free);
+        if (__any_sync(0xffffffffu, nvalid < 32)) {
 #pragma unroll
-        for (int e = 0; e < 32; ++e) pr[e] *= __uint_as_float(dv[e]) - dl;
-        if (nvalid < 32) {
+          for (int e = 0; e < 32; e += 2) {
+            float d0, d1;
+            unpair(mul2(pr[e >> 1], add2(pair(__uint_as_float(dv[e]), __uint_as_float(dv[e + 1])), nd2)), d0, d1);
+            pk[e >> 1] = pack_bf16(e < nvalid ? d0 : 0.f, e + 1 < nvalid ? d1 : 0.f);
+          }
+        } else {
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (e >= nvalid) pr[e] = 0.f;
+          for (int e = 0; e < 32; e += 2) {
+            float d0, d1;
+            unpair(mul2(pr[e >> 1], add2(pair(__uint_as_float(dv[e]), __uint_as_float(dv[e + 1])), nd2)), d0, d1);
+            pk[e >> 1] = pack_bf16(d0, d1);
+          }
         }
-#pragma unroll
-        for (int e = 0; e < 32; e += 2) pk[e >> 1] = pack_bf16(pr[e], pr[e + 1]);
         // packed bf16 dS stays inside this warpgroup's own (already read) column range
         tmem_st16(tS, pk);
         tmem_wait_st();
@@ -418,7 +432,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(ds_full((int)(J & 1)));
       }
-      if (ok) ok = mbar_wait_w(dq_ready, k & 1, abort_flag, p.status, p.wait_ns);
+      if (ok) ok = wait_w(dq_ready, k & 1, abort_flag, p.status, p.wait_ns);
       if (!ok) break;
       tc_fence_after();
       uint32_t v[32], pk[16];
@@ -448,7 +462,7 @@ constexpr int BM = 128;                     // keys per CTA (the M dimension)
 constexpr int BQ = 64;                      // query rows per step: pk heads x 64 / pk tokens
 constexpr int NS = 4;                       // Q / dO / statistics stages
 constexpr uint32_t kQTile = BQ * 256, kQHalf = BQ * 128;
-constexpr uint32_t kStatBytes = 2 * BQ * 4; // lse[64], delta[64]
+constexpr uint32_t kStatBytes = 2 * BQ * 4; // -lse log2(e) [64], -delta [64]
 constexpr int kThreads = 640;
 
 struct Smem {
@@ -566,7 +580,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     for (int j = 0; j < NJ; ++j) {
       const int s = j % NS;
-      ok = ok && mbar_wait_w(q_empty(s), ((j / NS) & 1) ^ 1, abort_flag, p.status, p.wait_ns);
+      ok = ok && wait_w(q_empty(s), ((j / NS) & 1) ^ 1, abort_flag, p.status, p.wait_ns);
       if (!ok) break;
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
@@ -574,8 +588,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int t = t0 + i * tq + r / p.pk;
         const int64_t at = (int64_t)(kh * p.G + g * p.pk + r % p.pk) * p.total + start + (t < len ? t : t0);
         const uint32_t dst = sbase + L::kStat + s * kStatBytes + r * 4, n = t < len ? 4u : 0u;
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(p.lse + at), "r"(n) : "memory");
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + BQ * 4), "l"(p.delta + at), "r"(n) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(p.stats + at), "r"(n) : "memory");
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + BQ * 4), "l"(p.stats + p.Hq * p.total + at), "r"(n) : "memory");
       }
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(stat_full(s)) : "memory");
       if (++i == Tq) { i = 0; ++g; }
@@ -587,7 +601,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int i = 0;
     for (int j = 0; ok && j < NJ; ++j) {
       const int s = j % NS;
-      ok = mbar_wait_w(q_full(s), (j / NS) & 1, abort_flag, p.status, p.wait_ns);
+      ok = wait_w(q_full(s), (j / NS) & 1, abort_flag, p.status, p.wait_ns);
       if (!ok) break;
       if (++i == Tq) {
         i = 0;
@@ -636,25 +650,25 @@ __global__ void __launch_bounds__(kThreads, 1)
     int ready = 0;                          // the step that step_ready() waits for, within its pass
     auto step_ready = [&](int j) {
       const int s = j % NS;
-      bool ok = mbar_wait_w(q_full(s), (j / NS) & 1, abort_flag, p.status, p.wait_ns);
+      bool ok = wait_w(q_full(s), (j / NS) & 1, abort_flag, p.status, p.wait_ns);
       if (++ready == Tq) {
         ready = 0;
         if (ok && ragged) {
-          ok = mbar_wait_w(q_clean(s), (clean_phase >> s) & 1u, abort_flag, p.status, p.wait_ns);
+          ok = wait_w(q_clean(s), (clean_phase >> s) & 1u, abort_flag, p.status, p.wait_ns);
           clean_phase ^= 1u << s;
         }
       }
       tc_fence_after();
       return ok;
     };
-    bool ok = mbar_wait_w(kv_full, 0, abort_flag, p.status, p.wait_ns);
+    bool ok = wait_w(kv_full, 0, abort_flag, p.status, p.wait_ns);
     for (int j = 0; ok && j < 2 && j < NJ; ++j) {
       ok = step_ready(j);
       if (ok) issue_sd(j, j & 1);
     }
     for (int j = 0; ok && j < NJ; ++j) {
       const int b = j & 1;
-      ok = mbar_wait_w(pd_full(b), (j >> 1) & 1, abort_flag, p.status, p.wait_ns);
+      ok = wait_w(pd_full(b), (j >> 1) & 1, abort_flag, p.status, p.wait_ns);
       if (!ok) break;
       tc_fence_after();
       issue_grad(j, b);
@@ -679,16 +693,17 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tP = tS + 64;
     const float* stat_base = reinterpret_cast<const float*>(smem + L::kStat);
     const int diag_steps = (BM + tq - 1) / tq;                // steps that overlap the key tile
+    const uint64_t c2 = pair(p.c2, p.c2);
     bool ok = true;
     int i = b % Tq;
     for (int j = b; j < NJ; j += 2) {
       const int s = j % NS;
-      ok = mbar_wait_w(stat_full(s), (j / NS) & 1, abort_flag, p.status, p.wait_ns) &&
-           mbar_wait_w(sd_full(b), (j >> 1) & 1, abort_flag, p.status, p.wait_ns);
+      ok = wait_w(stat_full(s), (j / NS) & 1, abort_flag, p.status, p.wait_ns) &&
+           wait_w(sd_full(b), (j >> 1) & 1, abort_flag, p.status, p.wait_ns);
       if (!ok) break;
       tc_fence_after();
-      const float* lse = stat_base + s * (kStatBytes / 4) + 32 * hc;
-      const float* dlt = lse + BQ;
+      const float* nlse = stat_base + s * (kStatBytes / 4) + 32 * hc;
+      const float* ndelta = nlse + BQ;
       // one TMEM round trip per step: both loads in flight, one wait, compute, both stores
       uint32_t sv[32], dv[32], pp[16], pd[16];
       tmem_ld32(tS + 32 * hc, sv);
@@ -697,24 +712,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       // query column c of this step is token i tq + c / pk of the tile's own tokens: columns before `from` are not
       // attended by it
       const int from = i < diag_steps ? (r - i * tq) * p.pk - 32 * hc : 0;
+      auto pairs = [&](bool masked) {
 #pragma unroll
-      for (int e = 0; e < 32; e += 4) {
-        const float4 l4 = *reinterpret_cast<const float4*>(lse + e);
-        const float4 d4 = *reinterpret_cast<const float4*>(dlt + e);
-        const float lv[4] = {l4.x, l4.y, l4.z, l4.w}, dd[4] = {d4.x, d4.y, d4.z, d4.w};
-        float pr[4], dsr[4];
-#pragma unroll
-        for (int f = 0; f < 4; ++f) {
-          const float pv = ex2(fmaf(__uint_as_float(sv[e + f]), p.c2, -lv[f] * kLog2eF));
-          const bool seen = e + f >= from;
-          pr[f] = seen ? pv : 0.f;
-          dsr[f] = seen ? pv * (__uint_as_float(dv[e + f]) - dd[f]) : 0.f;
+        for (int e = 0; e < 32; e += 2) {
+          const uint64_t nl = *reinterpret_cast<const uint64_t*>(nlse + e), nd = *reinterpret_cast<const uint64_t*>(ndelta + e);
+          float p0, p1, d0, d1;
+          unpair(fma2(pair(__uint_as_float(sv[e]), __uint_as_float(sv[e + 1])), c2, nl), p0, p1);
+          p0 = ex2(p0);
+          p1 = ex2(p1);
+          unpair(mul2(pair(p0, p1), add2(pair(__uint_as_float(dv[e]), __uint_as_float(dv[e + 1])), nd)), d0, d1);
+          if (masked) {
+            p0 = e >= from ? p0 : 0.f;
+            d0 = e >= from ? d0 : 0.f;
+            p1 = e + 1 >= from ? p1 : 0.f;
+            d1 = e + 1 >= from ? d1 : 0.f;
+          }
+          pp[e >> 1] = pack_bf16(p0, p1);
+          pd[e >> 1] = pack_bf16(d0, d1);
         }
-        pp[e >> 1] = pack_bf16(pr[0], pr[1]);
-        pp[(e >> 1) + 1] = pack_bf16(pr[2], pr[3]);
-        pd[e >> 1] = pack_bf16(dsr[0], dsr[1]);
-        pd[(e >> 1) + 1] = pack_bf16(dsr[2], dsr[3]);
-      }
+      };
+      if (__any_sync(0xffffffffu, from > 0)) pairs(true);
+      else pairs(false);
       // packed bf16 stays inside this warpgroup's own (already read) column range
       tmem_st16(tS + 32 * hc, pp);
       tmem_st16(tP + 32 * hc, pd);
@@ -726,7 +744,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       while (i >= Tq) i -= Tq;
     }
     // ---- epilogue: warpgroups 0, 1 own dV columns 0-63 / 64-127, warpgroups 2, 3 the same of dK
-    if (ok) ok = mbar_wait_w(done, 0, abort_flag, p.status, p.wait_ns);
+    if (ok) ok = wait_w(done, 0, abort_flag, p.status, p.wait_ns);
     if (ok) {
       tc_fence_after();
       const bool is_dk = w4 >= 2;
@@ -761,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 int dq_tile(int G) { return 128 / packed_heads(G); }
 
 cudaError_t launch_bwd_tc(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* d_o,
-                          float* delta, void* dq, void* dk, void* dv, const Header* hdr, const Tile* by_query,
+                          float* stats, void* dq, void* dk, void* dv, const Header* hdr, const Tile* by_query,
                           const Tile* by_key, const Problem& p, cudaStream_t st) {
   const int pk = packed_heads(p.G);
   const Strided so{(int64_t)p.Hq * kD, kD};
@@ -772,7 +790,7 @@ cudaError_t launch_bwd_tc(const void* q, const void* k, const void* v, const voi
       !make_map_packed(&mdo64, d_o, p.Hq, p.total, so, pk, 64 / pk) ||
       !make_map_packed(&mk, k, p.Hkv, p.total, p.k, 1, kBN) || !make_map_packed(&mv, v, p.Hkv, p.total, p.v, 1, kBN))
     return cudaErrorInvalidValue;
-  BwdParams a{p.Hq, p.Hkv, p.G, pk, p.total, p.scale * kLog2eF, p.scale, static_cast<const __nv_bfloat16*>(o), lse, delta,
+  BwdParams a{p.Hq, p.Hkv, p.G, pk, p.total, p.scale * kLog2eF, p.scale, static_cast<const __nv_bfloat16*>(o), lse, stats,
               static_cast<__nv_bfloat16*>(dq), static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv), hdr,
               by_query, p.fill_tail, p.status, p.wait_ns};
   int dev = 0, sms = 0;

@@ -81,7 +81,7 @@ hga::packed::Problem packed_problem(const hga_packed_config_t* c, void* ws) {
   return p;
 }
 
-// Workspace: [status word | header | two work lists | delta rows].
+// Workspace: [status word | header | two work lists | two float32 per row: lse and delta as the dK, dV kernel takes them].
 size_t list_bytes(const hga_packed_config_t* c) {
   return round256((size_t)(hga::packed::list_capacity(c->total, c->n_seqs, hga::packed::kLeastTile) + 1) *
                   sizeof(hga::packed::Tile));
@@ -89,7 +89,7 @@ size_t list_bytes(const hga_packed_config_t* c) {
 struct PackedWorkspace {
   hga::packed::Header* hdr;
   hga::packed::Tile* lists[2];
-  float* delta;
+  float* stats;
 };
 PackedWorkspace packed_workspace(const hga_packed_config_t* c, void* ws) {
   char* p = static_cast<char*>(ws) + hga::kStatusBytes;
@@ -97,12 +97,12 @@ PackedWorkspace packed_workspace(const hga_packed_config_t* c, void* ws) {
   w.hdr = reinterpret_cast<hga::packed::Header*>(p);
   p += sizeof(hga::packed::Header);
   for (int i = 0; i < 2; ++i, p += list_bytes(c)) w.lists[i] = reinterpret_cast<hga::packed::Tile*>(p);
-  w.delta = reinterpret_cast<float*>(p);
+  w.stats = reinterpret_cast<float*>(p);
   return w;
 }
 size_t packed_bytes(const hga_packed_config_t* c) {
   return hga::kStatusBytes + sizeof(hga::packed::Header) + 2 * list_bytes(c) +
-         round256((size_t)c->Hq * c->total * sizeof(float));
+         round256(2 * (size_t)c->Hq * c->total * sizeof(float));
 }
 
 // ---------------------------------------------------------------- pages
@@ -220,7 +220,7 @@ int hga_packed_attn_bwd(const hga_packed_config_t* cfg, const void* q, const voi
                                            (cfg->flags & HGA_PACKED_CLEAR_STATUS) != 0, st);
   if (e != cudaSuccess || cfg->total == 0) return from_cuda(e);
   return from_cuda((bf16 ? hga::packed::launch_bwd_tc : hga::packed::launch_bwd_f32)(
-      q, k, v, o, lse, d_o, w.delta, dq, dk, dv, w.hdr, w.lists[0], w.lists[1], p, st));
+      q, k, v, o, lse, d_o, w.stats, dq, dk, dv, w.hdr, w.lists[0], w.lists[1], p, st));
 }
 
 int hga_pages_workspace_size(const hga_pages_config_t* cfg, int32_t Hq, size_t* bytes_out) {

@@ -410,7 +410,7 @@ typedef struct hga_packed_config {
   int64_t wait_limit_ns;    /* as in hga_config_t */
 } hga_packed_config_t;
 
-/* Bytes of workspace of the two calls below (status word, work lists, delta rows). */
+/* Bytes of workspace of the two calls below (status word, work lists, two float32 per query row). */
 HGA_API int hga_packed_workspace_size(const hga_packed_config_t* cfg, size_t* bytes_out);
 
 HGA_API int hga_packed_attn_fwd(const hga_packed_config_t* cfg, const void* q, const void* k, const void* v,
