@@ -2,18 +2,20 @@
 //
 //   o = sum_u softmax_u(scale q.k_u) v_u over the cached tokens u < seq_len of the query's sequence
 //
-// Bound by reading the cache once: 4 Hq/Hkv flops per element read.  The work is the list of 64-token
-// tiles of all (query, KV head) pairs in order; CTA c of N takes the tiles [cW/N, (c+1)W/N), so every
-// SM reads the same number of bytes whatever the lengths are.  A pair whose tiles fall to several CTAs
-// is joined: each CTA leaves its running maximum, sum and unnormalised output in the workspace, and
-// the CTA that finishes last (a counter) adds the parts in the order of their tiles, so the result
-// does not depend on which one that is.  Each CTA has at most two such parts, its first and its last.
+// Bound by reading the cache once: 4 Hq/Hkv flops per element read.  The work is the list of token tiles of all (query, KV
+// head) pairs in order, each pair counting kPairCost tiles more for what its start and end cost; CTA c of N takes the
+// share [cW/N, (c+1)W/N) of the list, so every SM has the same work whatever the lengths are.  A pair whose tiles fall to
+// several CTAs is joined: each CTA leaves its running maximum, sum and unnormalised output in the workspace, and the CTA
+// that finishes last (a counter) adds the parts in the order of their tiles, so the result does not depend on which one that
+// is.  Each CTA has at most two such parts, its first and its last.
 //
-// bf16: the queries of a KV head are the rows of an m16n8k16 product (up to 16 rows: more query heads
-// are further pairs).  A producer warp brings a tile's pages with TMA (one box of {64 dims, rows, 2
-// halves} per page, 128-byte swizzle) into a ring; four warps take 16 keys of each tile, with softmax
-// statistics of their own that meet at the end of the pair.  Few rows cannot fill a tcgen05 tile, and
-// the memory is the limit by far.  float32: CUDA cores.
+// A producer warp brings a tile's pages with TMA (one box per page) into a ring of three 32 KB stages, two CTAs per SM; four
+// warps take a quarter of each tile's tokens, with softmax statistics of their own that meet at the end of the pair.  The
+// queries of a KV head are the rows of a pair (up to 16: more query heads are further pairs).
+//   bf16: 64 tokens per tile, m16n8k16 products with the queries as rows.  Few rows cannot fill a tcgen05 tile, and the
+//         memory is the limit by far.
+//   float32: 32 tokens per tile, float32 FMAs: a lane holds four dims; the dot products of eight tokens and four rows
+//         are summed over the lanes together, in 31 shuffles that leave one sum on each lane.
 #include <cuda.h>
 #include <math.h>
 
@@ -27,11 +29,17 @@ using namespace tc;
 
 namespace {
 
-constexpr int kTile = 64;              // tokens per tile
 constexpr int kRows = 16;              // most query rows of a pair
 constexpr int kConsumers = 128;        // threads of the four computing warps
+constexpr int kThreads = kConsumers + 32;
+constexpr int kStages = 3;
+constexpr uint32_t kTileBytes = 16384; // of K, and of V
+constexpr int kWindow = 32;            // queries whose row and length are kept in shared memory
+constexpr int kPairCost = 2;           // tiles: measured, a pair's start and end cost about 4500 cycles, a tile 2200
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kErrArg = -1;
+
+template <typename T> constexpr int kTileOf = (int)(kTileBytes / (kD * sizeof(T)));   // tokens per tile: 64 or 32
 
 struct Part {                          // in the workspace, two per CTA
   float o[kRows * kD];
@@ -50,195 +58,252 @@ struct Args {
   int* status;
   int64_t q_stride_n;
   int n, Hq, Hkv, G, subs;             // subs: pairs per KV head (16 query rows each)
-  int page, max_seqs, max_pages, n_pages, layer;
-  int64_t page_elems;                  // elements between pages of the layer
-  const void* k_pool;                  // of the layer
-  const void* v_pool;
+  int page, max_seqs, max_pages, n_pages;
   float c2;                            // scale * log2(e)
   uint64_t wait_ns;
 };
 
+struct Range {
+  int64_t begin, end, first;           // this CTA's share of the list; where the query at `begin` starts
+  int64_t total;
+  int n_cta, query;
+};
+
+struct Smem {
+  unsigned char kv[kStages][2][kTileBytes];          // 1 KB aligned (128-byte swizzle)
+  float merge[4][8][kD];                             // the four warps' outputs, eight rows at a time
+  float m[4][kRows], l[4][kRows];
+  uint64_t full[kStages], empty[kStages];
+  Range range;
+  int win_row[kWindow], win_len[kWindow];            // of the queries from range.query on
+  int64_t sums[kThreads / 32];
+  uint32_t valid[kStages];                           // pages of the tile that were loaded, one bit each
+  int abort, flag;
+};
+static_assert(2 * (sizeof(Smem) + 1024) <= 228 * 1024, "two CTAs per SM");
+
 __device__ __forceinline__ void consumer_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-// Tokens of query i (0 for a bad row or length: recorded).
-__device__ __forceinline__ int tokens_of(const Args& a, int i) {
+// Tokens of query i, and its row (0 tokens for a bad row or length: recorded).
+__device__ __forceinline__ int tokens_of(const Args& a, int i, int* row) {
   const int r = a.rows[i];
   int L = r >= 0 && r < a.max_seqs ? a.seq_len[r] : -1;
   if (L < 0 || (int64_t)L > (int64_t)a.max_pages * a.page) {
     set_status(a.status, kErrArg);
     L = 0;
   }
+  *row = r;
   return L;
 }
-
-struct Range {
-  int64_t total, begin, end, first;    // tiles of all, of this CTA; first tile of the query at `begin`
-  int n_cta, query;
-};
-
+template <typename T>
+__device__ __forceinline__ int64_t units_of(int L) {   // of one pair
+  return L ? (L + kTileOf<T> - 1) / kTileOf<T> + kPairCost : 0;
+}
 __device__ __forceinline__ int64_t cta_of(int64_t w, int64_t total, int64_t n) { return ((w + 1) * n - 1) / total; }
 
-// Finds this CTA's range.  Every thread of the block calls it (kThreads of them).
-template <int kThreads>
-__device__ __forceinline__ void find_range(const Args& a, Range* out, int64_t* sums) {
+// Finds this CTA's share.  Called by all threads.
+template <typename T>
+__device__ __forceinline__ void find_range(const Args& a, Smem& s) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const int per = (a.n + kThreads - 1) / kThreads;
   const int i0 = min(tid * per, a.n), i1 = min(i0 + per, a.n);
   const int pairs = a.Hkv * a.subs;
   int64_t mine = 0;
-  for (int i = i0; i < i1; ++i) mine += (int64_t)((tokens_of(a, i) + kTile - 1) / kTile) * pairs;
+  int L = 0, row = 0;                                  // of the last of this thread's queries
+  for (int i = i0; i < i1; ++i) {
+    L = tokens_of(a, i, &row);
+    mine += units_of<T>(L) * pairs;
+  }
   int64_t x = mine;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const int64_t y = __shfl_up_sync(0xffffffffu, x, o);
     if (lane >= o) x += y;
   }
-  if (lane == 31) sums[warp] = x;
+  if (lane == 31) s.sums[warp] = x;
   __syncthreads();
   int64_t base = x - mine, total = 0;
+#pragma unroll
   for (int w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) base += sums[w];
-    total += sums[w];
+    if (w < warp) base += s.sums[w];
+    total += s.sums[w];
   }
   const int64_t n_cta = min((int64_t)gridDim.x, total);
+  const int64_t begin = blockIdx.x < n_cta ? blockIdx.x * total / n_cta : 0;
+  const int64_t end = blockIdx.x < n_cta ? (blockIdx.x + 1) * total / n_cta : 0;
   if (tid == 0) {
-    out->total = total;
-    out->n_cta = (int)n_cta;
-    out->begin = out->end = 0;
-    if (blockIdx.x < n_cta) {
-      out->begin = blockIdx.x * total / n_cta;
-      out->end = (blockIdx.x + 1) * total / n_cta;
+    s.range.total = total;
+    s.range.n_cta = (int)n_cta;
+    s.range.begin = begin;
+    s.range.end = end;
+    s.range.query = 0;
+    s.range.first = 0;
+  }
+  __syncthreads();
+  if (begin < end && begin >= base && begin < base + mine) {
+    int64_t at = base;
+    for (int i = i0; i < i1; ++i) {
+      int r;
+      const int64_t t = units_of<T>(per == 1 ? L : tokens_of(a, i, &r)) * pairs;
+      if (begin < at + t) {
+        s.range.query = i;
+        s.range.first = at;
+        break;
+      }
+      at += t;
     }
   }
-  if (blockIdx.x < n_cta) {
-    const int64_t begin = blockIdx.x * total / n_cta;
-    if (begin >= base && begin < base + mine) {
-      int64_t at = base;
-      for (int i = i0; i < i1; ++i) {
-        const int64_t t = (int64_t)((tokens_of(a, i) + kTile - 1) / kTile) * pairs;
-        if (begin < at + t) {
-          out->query = i;
-          out->first = at;
-          break;
-        }
-        at += t;
-      }
+  __syncthreads();
+  const int q0 = s.range.query;
+  if (per == 1) {
+    if (tid >= q0 && tid < q0 + kWindow && tid < a.n) {
+      s.win_row[tid - q0] = row;
+      s.win_len[tid - q0] = L;
     }
+  } else if (tid < kWindow && q0 + tid < a.n) {
+    s.win_len[tid] = tokens_of(a, q0 + tid, &row);
+    s.win_row[tid] = row;
   }
   __syncthreads();
 }
 
-// One segment: tiles [t0, t1) of pair `pair` (of nt tiles each) of query i, whose tiles start at
-// list position `first`.
+// Tiles [t0, t1) of pair `pair` (of nt tiles) of query i.
 struct Segment {
-  int i, row, L, nt, pair, t0, t1;
-  int64_t pair_first;                  // list position of the pair's first tile
+  int i, row, L, nt, kh, h0, n_rows;   // KV head, first query head, query heads of the pair
+  int t0, t1;
+  int64_t tile0;                       // list position of the pair's first tile
 };
-// The segment at list position w; *i, *first move on to its query.
-__device__ __forceinline__ Segment segment_at(const Args& a, const Range& r, int64_t w, int* i, int64_t* first) {
+// The walk over this CTA's segments; each warp walks by itself.
+struct Walk {
+  int64_t w, end, first;
+  int i;
+};
+template <typename T>
+__device__ __forceinline__ bool next_segment(const Args& a, const Smem& s, Walk& k, Segment* g) {
   const int pairs = a.Hkv * a.subs;
-  Segment s;
-  for (;;) {
-    s.L = tokens_of(a, *i);
-    s.nt = (s.L + kTile - 1) / kTile;
-    const int64_t t = (int64_t)s.nt * pairs;
-    if (w < *first + t) break;
-    *first += t;
-    ++*i;
+  while (k.w < k.end) {
+    int64_t u;
+    for (;;) {
+      const int x = k.i - s.range.query;
+      if (x < kWindow) {
+        g->L = s.win_len[x];
+        g->row = s.win_row[x];
+      } else {
+        g->L = tokens_of(a, k.i, &g->row);
+      }
+      u = units_of<T>(g->L);
+      if (k.w < k.first + u * pairs) break;
+      k.first += u * pairs;
+      ++k.i;
+    }
+    g->i = k.i;
+    g->nt = (int)(u - kPairCost);
+    const int64_t x = k.w - k.first, pair = x / u, y = x - pair * u;
+    const int64_t take = min(u - y, k.end - k.w);
+    g->kh = (int)(a.subs == 1 ? pair : pair / a.subs);
+    const int sub = (int)(pair - (int64_t)g->kh * a.subs);
+    g->h0 = g->kh * a.G + sub * kRows;
+    g->n_rows = min(kRows, a.G - sub * kRows);
+    g->t0 = (int)max(y - kPairCost, (int64_t)0);
+    g->t1 = (int)max(y + take - kPairCost, (int64_t)0);
+    g->tile0 = k.first + pair * u + kPairCost;
+    k.w += take;
+    if (g->t1 > g->t0) return true;
   }
-  s.i = *i;
-  s.row = a.rows[s.i];
-  const int64_t x = w - *first;
-  s.pair = (int)(x / s.nt);
-  s.t0 = (int)(x - (int64_t)s.pair * s.nt);
-  s.t1 = (int)min((int64_t)s.nt, s.t0 + (r.end - w));
-  s.pair_first = *first + (int64_t)s.pair * s.nt;
-  return s;
-}
-
-// Query head of row r of a pair, or -1.
-__device__ __forceinline__ int head_of(const Args& a, int pair, int r) {
-  const int kh = pair / a.subs, x = (pair - kh * a.subs) * kRows + r;
-  return x < a.G ? kh * a.G + x : -1;
+  return false;
 }
 
 // One row's final 4 dims and, once, its lse.
 template <typename T>
-__device__ __forceinline__ void emit(const Args& a, const Segment& s, int r, int c4, float4 v, float m, float l) {
-  const int h = head_of(a, s.pair, r);
-  if (h < 0) return;
+__device__ __forceinline__ void emit(const Args& a, const Segment& g, int r, int c4, float4 v, float m, float l) {
   const float inv = l == 0.f ? 0.f : 1.f / l;          // (0: every token was left out)
   v.x *= inv; v.y *= inv; v.z *= inv; v.w *= inv;
-  store4(static_cast<T*>(a.o) + ((int64_t)s.i * a.Hq + h) * kD + 4 * c4, v);
-  if (c4 == 0) a.lse[(int64_t)s.i * a.Hq + h] = (m + log2f(l)) * 0.6931471805599453f;
+  const int64_t row = (int64_t)g.i * a.Hq + g.h0 + r;
+  store4(static_cast<T*>(a.o) + row * kD + 4 * c4, v);
+  if (c4 == 0) a.lse[row] = (m + log2f(l)) * 0.6931471805599453f;
 }
 
-// After a CTA's part of a split pair is in the workspace: the last CTA to get here adds the parts up.
-// `flag`: an int in shared memory.  Called by the 128 consumer threads.
+// After a CTA's part of a split pair is in the workspace: the last CTA to get here adds the parts up, in order.  Called by the
+// 128 consumer threads; a warp has the rows w, w + 4, ..., whose parts are all in flight together.
 template <typename T>
-__device__ __forceinline__ void join(const Args& a, const Segment& s, const Range& r, int* flag) {
-  const int64_t c0 = cta_of(s.pair_first, r.total, r.n_cta), c1 = cta_of(s.pair_first + s.nt - 1, r.total, r.n_cta);
+__device__ __forceinline__ void join(const Args& a, const Segment& g, Smem& s) {
+  const int64_t c0 = cta_of(g.tile0, s.range.total, s.range.n_cta), c1 = cta_of(g.tile0 + g.nt - 1, s.range.total, s.range.n_cta);
   const int n = (int)(c1 - c0 + 1);
   __threadfence();
   consumer_sync();
   if (threadIdx.x == 0) {
     const int before = atomicAdd(&a.counters[c0], 1);
-    *flag = before == n - 1;
+    s.flag = before == n - 1;
     if (before == n - 1) a.counters[c0] = 0;
   }
   consumer_sync();
-  if (!*flag) return;
+  if (!s.flag) return;
   __threadfence();
-  const int lane = threadIdx.x & 31;
-  auto part = [&](int p) -> const Part* { return a.parts + (p == 0 ? 2 * c0 + 1 : 2 * (c0 + p)); };
-  for (int row = threadIdx.x >> 5; row < kRows; row += kConsumers / 32) {
-    if (head_of(a, s.pair, row) < 0) continue;
-    float m = -INFINITY;
-    for (int p = lane; p < n; p += 32) m = fmaxf(m, __ldcg(&part(p)->m[row]));
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  float m[4], l[4];
+  float4 acc[4];
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    const float ref = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-    for (int p = 0; p < n; ++p) {
-      const Part* x = part(p);
-      const float f = exp2f(__ldcg(&x->m[row]) - ref);
+  for (int y = 0; y < 4; ++y) {
+    m[y] = -INFINITY;
+    l[y] = 0.f;
+    acc[y] = make_float4(0.f, 0.f, 0.f, 0.f);
+  }
+#pragma unroll 2
+  for (int p = 0; p < n; ++p) {
+    const Part* x = a.parts + (p == 0 ? 2 * c0 + 1 : 2 * (c0 + p));
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      const int row = warp + 4 * y;
+      if (row >= g.n_rows) break;
+      const float mp = __ldcg(&x->m[row]), lp = __ldcg(&x->l[row]);
       const float4 v = __ldcg(reinterpret_cast<const float4*>(x->o + row * kD) + lane);
-      l += f * __ldcg(&x->l[row]);
-      acc.x += f * v.x; acc.y += f * v.y; acc.z += f * v.z; acc.w += f * v.w;
+      const float mn = fmaxf(m[y], mp), ref = mn == -INFINITY ? 0.f : mn;
+      const float f = exp2f(m[y] - ref), e = exp2f(mp - ref);
+      m[y] = mn;
+      l[y] = l[y] * f + lp * e;
+      acc[y].x = acc[y].x * f + v.x * e;
+      acc[y].y = acc[y].y * f + v.y * e;
+      acc[y].z = acc[y].z * f + v.z * e;
+      acc[y].w = acc[y].w * f + v.w * e;
     }
-    emit<T>(a, s, row, lane, acc, m, l);
   }
+#pragma unroll
+  for (int y = 0; y < 4; ++y)
+    if (warp + 4 * y < g.n_rows) emit<T>(a, g, warp + 4 * y, lane, acc[y], m[y], l[y]);
 }
 
-// Queries without tokens: zeros and -inf.  Spread over the CTAs.
-template <typename T>
-__device__ __forceinline__ void emit_empty(const Args& a, int threads) {
-  for (int i = blockIdx.x; i < a.n; i += gridDim.x) {
-    if (tokens_of(a, i) != 0) continue;
-    for (int x = threadIdx.x; x < a.Hq * (kD / 4); x += threads)
-      store4(static_cast<T*>(a.o) + (int64_t)i * a.Hq * kD + 4 * x, make_float4(0.f, 0.f, 0.f, 0.f));
-    for (int h = threadIdx.x; h < a.Hq; h += threads) a.lse[(int64_t)i * a.Hq + h] = -INFINITY;
+// Eight rows (8 x ..) of the four warps' outputs in s.merge, their statistics in s.m, s.l: summed, and stored as the result
+// or as this CTA's part.  kSwap: columns are permuted by row (4 c ^ 8 (row mod 4)).
+template <typename T, bool kSwap>
+__device__ __forceinline__ void sum_warps(const Args& a, const Segment& g, const Smem& s, int x, bool whole, Part* part) {
+#pragma unroll
+  for (int y = 0; y < 2; ++y) {
+    const int rr = ((int)threadIdx.x >> 5) + 4 * y, c4 = threadIdx.x & 31, row = rr + 8 * x;
+    if (row >= g.n_rows) continue;
+    float mm = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) mm = fmaxf(mm, s.m[k][row]);
+    const float ref = mm == -INFINITY ? 0.f : mm;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    float ll = 0.f;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const float f = ex2(s.m[k][row] - ref);
+      const float4 u = *reinterpret_cast<const float4*>(&s.merge[k][rr][kSwap ? (4 * c4) ^ ((rr & 3) << 3) : 4 * c4]);
+      v.x += f * u.x; v.y += f * u.y; v.z += f * u.z; v.w += f * u.w;
+      ll += f * s.l[k][row];
+    }
+    if (whole) {
+      emit<T>(a, g, row, c4, v, mm, ll);
+    } else {
+      __stcg(reinterpret_cast<float4*>(part->o + row * kD) + c4, v);
+      if (c4 == 0) {
+        __stcg(&part->m[row], mm);
+        __stcg(&part->l[row], ll);
+      }
+    }
   }
 }
-
-// ------------------------------------------------------------------------------------ bf16, tensor cores
-constexpr int kStages = 3;
-constexpr uint32_t kTileBytes = kTile * kD * 2;      // 16 KB of K, 16 KB of V
-constexpr int kMmaThreads = kConsumers + 32;
-
-struct MmaSmem {
-  unsigned char kv[kStages][2][kTileBytes];          // 1 KB aligned (128-byte swizzle)
-  float merge[4][8][kD];                             // the four warps' outputs, eight rows at a time
-  float m[4][kRows], l[4][kRows];
-  uint64_t full[kStages], empty[kStages];
-  int64_t sums[kMmaThreads / 32];
-  Range range;
-  uint32_t valid[kStages];                           // pages of the tile that were loaded, one bit each
-  int abort, flag;
-};
-static_assert(2 * (sizeof(MmaSmem) + 1024) <= 228 * 1024, "two CTAs per SM");
 
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -254,6 +319,14 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
                : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
                : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int32_t row, int32_t head, int32_t page,
+                                            uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(
+          dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(row), "r"(head), "r"(page), "r"(bar)
+      : "memory");
+}
 __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map, int32_t row, int32_t head,
                                             int32_t page, uint32_t bar) {
   asm volatile(
@@ -263,108 +336,136 @@ __device__ __forceinline__ void tma_load_5d(uint32_t dst, const CUtensorMap* map
       : "memory");
 }
 
-// RH: 1 when a pair has at most 8 query rows (the upper half of the m16 tile is empty), else 2.
-template <int RH>
-__global__ void __launch_bounds__(kMmaThreads, 2)
-    paged_mma_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Args a) {
-  extern __shared__ __align__(1024) unsigned char smem_raw[];
-  MmaSmem& s = *reinterpret_cast<MmaSmem*>(smem_raw);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  auto full = [&](int i) { return smem_u32(&s.full[i]); };
-  auto empty = [&](int i) { return smem_u32(&s.empty[i]); };
-  volatile int* abort_flag = &s.abort;
+// What both kernels begin with: barriers, this CTA's share, and whether there is any.
+template <typename T>
+__device__ __forceinline__ bool begin(const Args& a, Smem& s) {
   pdl_trigger();
-  if (tid == 0) {
+  if (threadIdx.x == 0) {
     for (int i = 0; i < kStages; ++i) {
-      mbar_init(full(i), 1);
-      mbar_init(empty(i), 4);
+      mbar_init(smem_u32(&s.full[i]), 1);
+      mbar_init(smem_u32(&s.empty[i]), 4);
     }
     s.abort = 0;
     mbar_fence_init();
   }
   pdl_wait();
-  find_range<kMmaThreads>(a, &s.range, s.sums);        // (its barriers also publish the mbarriers)
-  emit_empty<__nv_bfloat16>(a, kMmaThreads);
-  const Range rg = s.range;
-  if (rg.begin == rg.end) return;
+  find_range<T>(a, s);                                 // (its barriers also publish the mbarriers)
+  return s.range.begin < s.range.end;
+}
 
+// Queries without tokens: zeros and -inf, spread over the CTAs.  Called by the producer warp, when its loads are issued.
+template <typename T>
+__device__ __forceinline__ void write_empty(const Args& a) {
+  const int lane = threadIdx.x & 31;
+  for (int i = blockIdx.x; i < a.n; i += gridDim.x) {
+    int row;
+    if (tokens_of(a, i, &row) != 0) continue;
+    for (int h = 0; h < a.Hq; ++h) {
+      store4(static_cast<T*>(a.o) + ((int64_t)i * a.Hq + h) * kD + 4 * lane, make_float4(0.f, 0.f, 0.f, 0.f));
+      if (lane == 0) a.lse[(int64_t)i * a.Hq + h] = -INFINITY;
+    }
+  }
+}
+
+// The producer warp: the tiles of this CTA's segments, one after another.
+template <typename T>
+__device__ __forceinline__ void produce(const Args& a, Smem& s, const CUtensorMap& tm_k, const CUtensorMap& tm_v) {
+  constexpr int kTile = kTileOf<T>;
+  const int lane = threadIdx.x & 31;
+  auto full = [&](int i) { return smem_u32(&s.full[i]); };
+  volatile int* abort_flag = &s.abort;
   const int R = min(a.page, kTile);                    // tokens per box
   const int boxes = kTile / R;                         // boxes of a tile
-  int qi = rg.query;
-  int64_t first = rg.first;
-  if (warp == 4) {
-    // ======================= producer: the tiles of this CTA's segments, one after another
-    const uint64_t kv0 = smem_u32(&s.kv[0][0][0]);
-    int64_t J = 0;
-    bool ok = true;
-    for (int64_t w = rg.begin; ok && w < rg.end;) {
-      const Segment sg = segment_at(a, rg, w, &qi, &first);
-      w += sg.t1 - sg.t0;
-      const int32_t* ids = a.table + (int64_t)sg.row * a.max_pages;
-      const int kh = sg.pair / a.subs;
-      // box b of the segment: tokens (t0 * boxes + b) * R ..; lane l holds the pages of 32 boxes at a time
-      const int b_end = min(sg.t1 * boxes, (sg.L + R - 1) / R);
-      int b0 = sg.t0 * boxes;
-      auto page_of = [&](int b) { return b < b_end ? ids[(int64_t)b * R / a.page] : -1; };
-      int32_t cur = page_of(b0 + lane), nxt = page_of(b0 + 32 + lane);
-      for (int t = sg.t0; t < sg.t1; ++t, ++J) {
-        const int st = (int)(J % kStages);
-        if (t * boxes >= b0 + 32) {
-          b0 += 32;
-          cur = nxt;
-          nxt = page_of(b0 + 32 + lane);
-        }
-        const int b = t * boxes + lane;                // this lane's box of the tile
-        const int32_t id = __shfl_sync(0xffffffffu, cur, (t * boxes - b0 + lane) & 31);
-        const bool have = lane < boxes && b < b_end, good = have && id >= 0 && id < a.n_pages;
-        if (have && !good) set_status(a.status, kErrArg);
-        const uint32_t mask = __ballot_sync(0xffffffffu, good);
-        int go = 1;
-        if (lane == 0) {
-          go = mbar_wait(empty(st), (uint32_t)((J / kStages) & 1) ^ 1, abort_flag, a.status, a.wait_ns);
-          if (go) {
-            s.valid[st] = mask;
-            mbar_arrive_expect_tx(full(st), (uint32_t)__popc(mask) * R * kD * 2 * 2);
-          }
-        }
-        ok = __shfl_sync(0xffffffffu, go, 0) != 0;
-        if (!ok) break;
-        if (good) {
-          const uint32_t dst = (uint32_t)kv0 + st * 2 * kTileBytes + lane * R * (kD * 2);
-          const int row = (int)((int64_t)b * R % a.page);
-          tma_load_5d(dst, &tm_k, row, kh, id, full(st));
-          tma_load_5d(dst + kTileBytes, &tm_v, row, kh, id, full(st));
-        }
-        __syncwarp();
+  const uint32_t kv0 = smem_u32(&s.kv[0][0][0]);
+  Walk walk{s.range.begin, s.range.end, s.range.first, s.range.query};
+  Segment g;
+  int64_t J = 0;
+  bool ok = true;
+  while (ok && next_segment<T>(a, s, walk, &g)) {
+    const int32_t* ids = a.table + (int64_t)g.row * a.max_pages;
+    // box b of the sequence: tokens b R ..; lane l holds the pages of 32 boxes at a time
+    const int b_end = min(g.t1 * boxes, (g.L + R - 1) / R);
+    int b0 = g.t0 * boxes;
+    auto page_of = [&](int b) { return b < b_end ? ids[(int64_t)b * R / a.page] : -1; };
+    int32_t cur = page_of(b0 + lane), nxt = page_of(b0 + 32 + lane);
+    for (int t = g.t0; t < g.t1; ++t, ++J) {
+      const int st = (int)(J % kStages);
+      if (t * boxes >= b0 + 32) {
+        b0 += 32;
+        cur = nxt;
+        nxt = page_of(b0 + 32 + lane);
       }
+      const int b = t * boxes + lane;                  // this lane's box of the tile
+      const int32_t id = __shfl_sync(0xffffffffu, cur, (t * boxes - b0 + lane) & 31);
+      const bool have = lane < boxes && b < b_end, good = have && id >= 0 && id < a.n_pages;
+      if (have && !good) set_status(a.status, kErrArg);
+      const uint32_t mask = __ballot_sync(0xffffffffu, good);
+      int go = 1;
+      if (lane == 0) {
+        go = mbar_wait(smem_u32(&s.empty[st]), (uint32_t)((J / kStages) & 1) ^ 1, abort_flag, a.status, a.wait_ns);
+        if (go) {
+          s.valid[st] = mask;
+          mbar_arrive_expect_tx(full(st), (uint32_t)__popc(mask) * R * kD * sizeof(T) * 2);
+        }
+      }
+      ok = __shfl_sync(0xffffffffu, go, 0) != 0;
+      if (!ok) break;
+      if (good) {
+        const uint32_t dst = kv0 + st * 2 * kTileBytes + lane * R * (kD * (uint32_t)sizeof(T));
+        const int row = (int)((int64_t)b * R % a.page);
+        if (sizeof(T) == 2) {
+          tma_load_5d(dst, &tm_k, row, g.kh, id, full(st));
+          tma_load_5d(dst + kTileBytes, &tm_v, row, g.kh, id, full(st));
+        } else {
+          tma_load_4d(dst, &tm_k, row, g.kh, id, full(st));
+          tma_load_4d(dst + kTileBytes, &tm_v, row, g.kh, id, full(st));
+        }
+      }
+      __syncwarp();
     }
-    // its loads have landed before the CTA may exit
-    if (lane == 0)
-      for (int64_t j = J > kStages ? J - kStages : 0; j < J; ++j)
-        drain_wait(full((int)(j % kStages)), (uint32_t)((j / kStages) & 1), a.status);
-    return;
   }
+  write_empty<T>(a);
+  // its loads have landed before the CTA may exit
+  if (lane == 0)
+    for (int64_t j = J > kStages ? J - kStages : 0; j < J; ++j)
+      drain_wait(full((int)(j % kStages)), (uint32_t)((j / kStages) & 1), a.status);
+}
 
+// ------------------------------------------------------------------------------------ bf16, tensor cores
+// RH: 1 when a pair has at most 8 query rows (the upper half of the m16 tile is empty), else 2.
+template <int RH>
+__global__ void __launch_bounds__(kThreads, 2)
+    paged_bf16_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Args a) {
+  typedef __nv_bfloat16 T;
+  constexpr int kTile = kTileOf<T>;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  Smem& s = *reinterpret_cast<Smem*>(smem_raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  volatile int* abort_flag = &s.abort;
+  const bool work = begin<T>(a, s);
+  if (warp == 4) produce<T>(a, s, tm_k, tm_v);
+  if (warp == 4 || !work) return;
   // ======================= the four computing warps: keys 16 warp .. + 15 of each tile
-  const int g = lane >> 2, tq = lane & 3;              // fragment row and column pair
+  const int R = min(a.page, kTile);
+  const int fg = lane >> 2, tq = lane & 3;             // fragment row and column pair
   const int key0 = 16 * warp;
+  Walk walk{s.range.begin, s.range.end, s.range.first, s.range.query};
+  Segment g;
   int64_t J = 0;
   bool alive = true;                                   // no wait has expired
-  for (int64_t w = rg.begin; w < rg.end;) {
-    const Segment sg = segment_at(a, rg, w, &qi, &first);
-    w += sg.t1 - sg.t0;
-    // queries: rows g and g + 8, dims 16 ks + 2 tq + {0, 1} and + 8
+  while (next_segment<T>(a, s, walk, &g)) {
+    // queries: rows fg and fg + 8, dims 16 ks + 2 tq + {0, 1} and + 8
     uint32_t qf[8][4];
     {
-      const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(a.q) + sg.i * a.q_stride_n + 2 * tq;
-      const int h0 = head_of(a, sg.pair, g), h1 = RH == 2 ? head_of(a, sg.pair, g + 8) : -1;
+      const T* qb = static_cast<const T*>(a.q) + g.i * a.q_stride_n + (int64_t)g.h0 * kD + 2 * tq;
+      const bool in0 = fg < g.n_rows, in1 = RH == 2 && fg + 8 < g.n_rows;
 #pragma unroll
       for (int ks = 0; ks < 8; ++ks) {
-        const __nv_bfloat16 *p0 = qb + (int64_t)h0 * kD + 16 * ks, *p1 = qb + (int64_t)h1 * kD + 16 * ks;
-        qf[ks][0] = h0 >= 0 ? *reinterpret_cast<const uint32_t*>(p0) : 0u;
-        qf[ks][2] = h0 >= 0 ? *reinterpret_cast<const uint32_t*>(p0 + 8) : 0u;
-        qf[ks][1] = h1 >= 0 ? *reinterpret_cast<const uint32_t*>(p1) : 0u;
-        qf[ks][3] = h1 >= 0 ? *reinterpret_cast<const uint32_t*>(p1 + 8) : 0u;
+        const T *p0 = qb + fg * kD + 16 * ks, *p1 = p0 + 8 * kD;
+        qf[ks][0] = in0 ? *reinterpret_cast<const uint32_t*>(p0) : 0u;
+        qf[ks][2] = in0 ? *reinterpret_cast<const uint32_t*>(p0 + 8) : 0u;
+        qf[ks][1] = in1 ? *reinterpret_cast<const uint32_t*>(p1) : 0u;
+        qf[ks][3] = in1 ? *reinterpret_cast<const uint32_t*>(p1 + 8) : 0u;
       }
     }
     float o[16][4];
@@ -376,10 +477,10 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
 #pragma unroll
     for (int x = 0; x < RH; ++x) { m[x] = -INFINITY; l[x] = 0.f; }
 
-    for (int t = sg.t0; t < sg.t1; ++t, ++J) {
+    for (int t = g.t0; t < g.t1; ++t, ++J) {
       const int st = (int)(J % kStages);
-      alive = alive && mbar_wait_w(full(st), (uint32_t)((J / kStages) & 1), abort_flag, a.status, a.wait_ns);
-      const int nvalid = min(kTile, sg.L - t * kTile) - key0;      // of this warp's 16 keys
+      alive = alive && mbar_wait_w(smem_u32(&s.full[st]), (uint32_t)((J / kStages) & 1), abort_flag, a.status, a.wait_ns);
+      const int nvalid = min(kTile, g.L - t * kTile) - key0;       // of this warp's 16 keys
       if (alive && nvalid > 0 && (s.valid[st] >> (key0 / R) & 1u)) {
         // key x of this warp: row (key0 + x) % R of its box
         const uint32_t kbase = smem_u32(&s.kv[st][0][0]) + (key0 / R) * R * (kD * 2), vbase = kbase + kTileBytes;
@@ -456,207 +557,162 @@ __global__ void __launch_bounds__(kMmaThreads, 2)
         }
       }
       __syncwarp();
-      if (lane == 0) mbar_arrive(empty(st));
+      if (lane == 0) mbar_arrive(smem_u32(&s.empty[st]));
     }
 
     // ---- the four warps' statistics and outputs meet
+    const bool whole = g.t0 == 0 && g.t1 == g.nt;
+    Part* part = a.parts + 2 * (int64_t)blockIdx.x + (g.t0 == 0 ? 1 : 0);
+    consumer_sync();                                   // the last pair's sums have been read
 #pragma unroll
     for (int x = 0; x < RH; ++x) {
       l[x] += __shfl_xor_sync(0xffffffffu, l[x], 1);
       l[x] += __shfl_xor_sync(0xffffffffu, l[x], 2);
       if (tq == 0) {
-        s.m[warp][g + 8 * x] = m[x];
-        s.l[warp][g + 8 * x] = l[x];
+        s.m[warp][fg + 8 * x] = m[x];
+        s.l[warp][fg + 8 * x] = l[x];
       }
     }
-    const bool whole = sg.t0 == 0 && sg.t1 == sg.nt;
-    Part* part = a.parts + 2 * (int64_t)blockIdx.x + (sg.t0 == 0 ? 1 : 0);
-    consumer_sync();
 #pragma unroll
     for (int x = 0; x < RH; ++x) {
-      const int row = g + 8 * x;
-      const float mt = fmaxf(fmaxf(s.m[0][row], s.m[1][row]), fmaxf(s.m[2][row], s.m[3][row]));
-      const float f = mt == -INFINITY ? 0.f : ex2(m[x] - mt);
       if (x) consumer_sync();                          // the first eight rows have been read
 #pragma unroll
       for (int i = 0; i < 16; ++i)                     // (columns permuted by row: no bank conflicts)
-        *reinterpret_cast<float2*>(&s.merge[warp][g][(8 * i + 2 * tq) ^ ((g & 3) << 3)]) =
-            make_float2(o[i][2 * x] * f, o[i][2 * x + 1] * f);
+        *reinterpret_cast<float2*>(&s.merge[warp][fg][(8 * i + 2 * tq) ^ ((fg & 3) << 3)]) =
+            make_float2(o[i][2 * x], o[i][2 * x + 1]);
       consumer_sync();
-#pragma unroll
-      for (int y = 0; y < 2; ++y) {
-        const int z = tid + 128 * y, rr = z >> 5, c4 = z & 31, rw = rr + 8 * x;
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        float mm = -INFINITY, ll = 0.f;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) mm = fmaxf(mm, s.m[k][rw]);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) {
-          const float4 u = *reinterpret_cast<const float4*>(&s.merge[k][rr][(4 * c4) ^ ((rr & 3) << 3)]);
-          v.x += u.x; v.y += u.y; v.z += u.z; v.w += u.w;
-          ll += mm == -INFINITY ? 0.f : s.l[k][rw] * ex2(s.m[k][rw] - mm);
-        }
-        if (whole) {
-          emit<__nv_bfloat16>(a, sg, rw, c4, v, mm, ll);
-        } else {
-          __stcg(reinterpret_cast<float4*>(part->o + rw * kD) + c4, v);
-          if (c4 == 0) {
-            __stcg(&part->m[rw], mm);
-            __stcg(&part->l[rw], ll);
-          }
-        }
-      }
+      sum_warps<T, true>(a, g, s, x, whole, part);
     }
-    if (!whole) join<__nv_bfloat16>(a, sg, rg, &s.flag);
-    consumer_sync();                                   // s.m, s.l, s.flag are free again
+    if (!whole) join<T>(a, g, s);
   }
 }
 
-// ------------------------------------------------------------------------------------ CUDA cores
-struct SimtSmem {
-  float k[kTile][kD + 4];
-  float v[kTile][kD];
-  float q[kRows][kD];
-  float p[kRows][kTile];
-  float m[kRows], l[kRows], alpha[kRows];
-  int64_t sums[kConsumers / 32];
-  Range range;
-  int flag;
-};
-
-template <typename T>
-__global__ void __launch_bounds__(kConsumers) paged_simt_kernel(const Args a) {
-  extern __shared__ __align__(1024) unsigned char smem_raw[];
-  SimtSmem& s = *reinterpret_cast<SimtSmem*>(smem_raw);
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int N = Vec16<T>::N, LPR = kD / N;
-  pdl_trigger();
-  pdl_wait();
-  find_range<kConsumers>(a, &s.range, s.sums);
-  emit_empty<T>(a, kConsumers);
-  const Range rg = s.range;
-  int qi = rg.query;
-  int64_t first = rg.first;
-  for (int64_t w = rg.begin; w < rg.end;) {
-    const Segment sg = segment_at(a, rg, w, &qi, &first);
-    w += sg.t1 - sg.t0;
-    const int kh = sg.pair / a.subs;
-    const int n_rows = min(kRows, a.G - (sg.pair - kh * a.subs) * kRows);
-    __syncthreads();
-    for (int x = tid; x < kRows * (kD / 4); x += kConsumers) {
-      const int r = x / (kD / 4), c = x % (kD / 4), h = head_of(a, sg.pair, r);
-      float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-      if (h >= 0) v = load4(static_cast<const T*>(a.q) + sg.i * a.q_stride_n + (int64_t)h * kD + 4 * c);
-      v.x *= a.c2; v.y *= a.c2; v.z *= a.c2; v.w *= a.c2;
-      store4(&s.q[r][4 * c], v);
+// ------------------------------------------------------------------------------------ float32
+// Sums v[0 .. 31] over the lanes: lane l gets the sum of v[l].
+__device__ __forceinline__ float lane_sums(float (&v)[32]) {
+  const int lane = threadIdx.x & 31;
+#pragma unroll
+  for (int h = 16; h > 0; h >>= 1) {
+    const bool up = lane & h;
+#pragma unroll
+    for (int i = 0; i < h; ++i) {
+      const float give = up ? v[i] : v[i + h], keep = up ? v[i + h] : v[i];
+      v[i] = keep + __shfl_xor_sync(0xffffffffu, give, h);
     }
-    if (tid < kRows) { s.m[tid] = -INFINITY; s.l[tid] = 0.f; }
-    float acc[kRows];
+  }
+  return v[0];
+}
+
+// NB: blocks of four query rows (1, 2 or 4 for pairs of at most 4, 8 or 16).
+template <int NB>
+__global__ void __launch_bounds__(kThreads, 2)
+    paged_f32_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Args a) {
+  typedef float T;
+  constexpr int kTile = kTileOf<T>;
+  extern __shared__ __align__(1024) unsigned char smem_raw[];
+  Smem& s = *reinterpret_cast<Smem*>(smem_raw);
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  volatile int* abort_flag = &s.abort;
+  const bool work = begin<T>(a, s);
+  if (warp == 4) produce<T>(a, s, tm_k, tm_v);
+  if (warp == 4 || !work) return;
+  // ======================= the four computing warps: keys 8 warp .. + 7 of each tile; a lane has dims 4 lane .. + 3
+  const int R = min(a.page, kTile);
+  const int key0 = 8 * warp;
+  Walk walk{s.range.begin, s.range.end, s.range.first, s.range.query};
+  Segment g;
+  int64_t J = 0;
+  bool alive = true;                                   // no wait has expired
+  while (next_segment<T>(a, s, walk, &g)) {
+    float4 q[4 * NB], o[4 * NB];
 #pragma unroll
-    for (int r = 0; r < kRows; ++r) acc[r] = 0.f;
-    for (int t = sg.t0; t < sg.t1; ++t) {
-      const int nv = min(kTile, sg.L - t * kTile);
-      __syncthreads();
-      for (int x = tid; x < kTile * LPR; x += kConsumers) {
-        const int key = x / LPR, c = (x % LPR) * N;
-        const int64_t pos = (int64_t)t * kTile + key;
-        float kf[N], vf[N];
-#pragma unroll
-        for (int e = 0; e < N; ++e) kf[e] = vf[e] = 0.f;
-        if (key < nv) {
-          const int id = a.table[(int64_t)sg.row * a.max_pages + pos / a.page];
-          if (id >= 0 && id < a.n_pages) {
-            const int64_t off = id * a.page_elems + ((int64_t)kh * a.page + pos % a.page) * kD + c;
-            Vec16<T>::load(static_cast<const T*>(a.k_pool) + off, kf);
-            Vec16<T>::load(static_cast<const T*>(a.v_pool) + off, vf);
-          } else {
-            set_status(a.status, kErrArg);
-            kf[0] = NAN;                               // marks the token as left out
-          }
-        }
-#pragma unroll
-        for (int e = 0; e < N; e += 4) {
-          store4(&s.k[key][c + e], make_float4(kf[e], kf[e + 1], kf[e + 2], kf[e + 3]));
-          store4(&s.v[key][c + e], make_float4(vf[e], vf[e + 1], vf[e + 2], vf[e + 3]));
-        }
+    for (int r = 0; r < 4 * NB; ++r) {
+      q[r] = o[r] = make_float4(0.f, 0.f, 0.f, 0.f);
+      if (r < g.n_rows) {
+        q[r] = load4(static_cast<const T*>(a.q) + g.i * a.q_stride_n + (int64_t)(g.h0 + r) * kD + 4 * lane);
+        q[r].x *= a.c2; q[r].y *= a.c2; q[r].z *= a.c2; q[r].w *= a.c2;
       }
-      __syncthreads();
-      {
-        // scores: thread = key, half of the rows
-        const int key = tid & 63, r0 = (tid >> 6) * 8;
-        const int id = key < nv ? a.table[(int64_t)sg.row * a.max_pages + ((int64_t)t * kTile + key) / a.page] : -1;
-        const bool in = id >= 0 && id < a.n_pages;
-        float d[8] = {};
-        if (r0 < n_rows)
-          for (int c = 0; c < kD; c += 4) {
-            const float4 kv = *reinterpret_cast<const float4*>(&s.k[key][c]);
+    }
+    // lane l has the score of key l / 4, row l % 4 of a block; m, l of that row, the same in its eight lanes
+    float m[NB], l[NB];
 #pragma unroll
-            for (int r = 0; r < 8; ++r) {
-              const float4 qv = *reinterpret_cast<const float4*>(&s.q[r0 + r][c]);
-              d[r] += kv.x * qv.x + kv.y * qv.y + kv.z * qv.z + kv.w * qv.w;
+    for (int x = 0; x < NB; ++x) { m[x] = -INFINITY; l[x] = 0.f; }
+    for (int t = g.t0; t < g.t1; ++t, ++J) {
+      const int st = (int)(J % kStages);
+      alive = alive && mbar_wait_w(smem_u32(&s.full[st]), (uint32_t)((J / kStages) & 1), abort_flag, a.status, a.wait_ns);
+      const int nvalid = min(kTile, g.L - t * kTile) - key0;       // of this warp's 8 keys
+      if (alive && nvalid > 0 && (s.valid[st] >> (key0 / R) & 1u)) {
+        const float4* kt = reinterpret_cast<const float4*>(&s.kv[st][0][0]) + key0 * (kD / 4) + lane;
+        const float4* vt = reinterpret_cast<const float4*>(&s.kv[st][1][0]) + key0 * (kD / 4) + lane;
+#pragma unroll
+        for (int x = 0; x < NB; ++x) {
+          if (4 * x >= g.n_rows) break;
+          float d[32];
+#pragma unroll
+          for (int key = 0; key < 8; ++key) {
+            const float4 k = kt[key * (kD / 4)];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float4 y = q[4 * x + r];
+              d[4 * key + r] = k.x * y.x + k.y * y.y + k.z * y.z + k.w * y.w;
+            }
+          }
+          float sc = lane_sums(d);
+          if ((lane >> 2) >= nvalid) sc = -INFINITY;
+          float mx = sc;
+#pragma unroll
+          for (int h = 4; h < 32; h <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, h));
+          const float mnew = fmaxf(m[x], mx), ref = mnew == -INFINITY ? 0.f : mnew;
+          const float alpha = exp2f(m[x] - ref), p = exp2f(sc - ref);
+          m[x] = mnew;
+          l[x] = l[x] * alpha + p;                     // of this lane's key
+          if (__any_sync(0xffffffffu, alpha != 1.f)) {
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              const float al = __shfl_sync(0xffffffffu, alpha, r);
+              float4& y = o[4 * x + r];
+              y.x *= al; y.y *= al; y.z *= al; y.w *= al;
             }
           }
 #pragma unroll
-        for (int r = 0; r < 8; ++r) s.p[r0 + r][key] = in ? d[r] : -INFINITY;
-      }
-      __syncthreads();
-      for (int r = warp; r < n_rows; r += 4) {
-        const float x0 = s.p[r][lane], x1 = s.p[r][lane + 32];
-        float mx = fmaxf(x0, x1);
+          for (int key = 0; key < 8; ++key) {
+            if (key >= nvalid) break;                  // (whatever the page holds there)
+            const float4 v = vt[key * (kD / 4)];
 #pragma unroll
-        for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const float mo = s.m[r], mnew = fmaxf(mo, mx), ref = mnew == -INFINITY ? 0.f : mnew;
-        const float p0 = exp2f(x0 - ref), p1 = exp2f(x1 - ref);
-        float sum = p0 + p1;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-        s.p[r][lane] = p0;
-        s.p[r][lane + 32] = p1;
-        __syncwarp();
-        if (lane == 0) {
-          const float al = exp2f(mo - ref);
-          s.alpha[r] = al;
-          s.m[r] = mnew;
-          s.l[r] = s.l[r] * al + sum;
-        }
-      }
-      __syncthreads();
-#pragma unroll
-      for (int r = 0; r < kRows; ++r)
-        if (r < n_rows) acc[r] *= s.alpha[r];
-      for (int key = 0; key < nv; key += 4) {          // (keys past nv: p = 0, v = 0)
-        float v[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = s.v[key + e][tid];
-#pragma unroll
-        for (int r = 0; r < kRows; ++r)
-          if (r < n_rows) {
-            const float4 p = *reinterpret_cast<const float4*>(&s.p[r][key]);
-            acc[r] += p.x * v[0] + p.y * v[1] + p.z * v[2] + p.w * v[3];
+            for (int r = 0; r < 4; ++r) {
+              const float pr = __shfl_sync(0xffffffffu, p, 4 * key + r);
+              float4& y = o[4 * x + r];
+              y.x += pr * v.x; y.y += pr * v.y; y.z += pr * v.z; y.w += pr * v.w;
+            }
           }
-      }
-    }
-    // outputs through the K area, four dims per thread
-    __syncthreads();
-    const bool whole = sg.t0 == 0 && sg.t1 == sg.nt;
-    Part* part = a.parts + 2 * (int64_t)blockIdx.x + (sg.t0 == 0 ? 1 : 0);
-    float* buf = &s.v[0][0];
-#pragma unroll
-    for (int r = 0; r < kRows; ++r) buf[r * kD + tid] = acc[r];
-    __syncthreads();
-    for (int r = warp; r < n_rows; r += 4) {
-      const float4 v = *reinterpret_cast<const float4*>(&buf[r * kD + 4 * lane]);
-      if (whole) {
-        emit<T>(a, sg, r, lane, v, s.m[r], s.l[r]);
-      } else {
-        __stcg(reinterpret_cast<float4*>(part->o + r * kD) + lane, v);
-        if (lane == 0) {
-          __stcg(&part->m[r], s.m[r]);
-          __stcg(&part->l[r], s.l[r]);
         }
       }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(&s.empty[st]));
     }
-    if (!whole) join<T>(a, sg, rg, &s.flag);
+    // ---- the four warps' statistics and outputs meet
+    const bool whole = g.t0 == 0 && g.t1 == g.nt;
+    Part* part = a.parts + 2 * (int64_t)blockIdx.x + (g.t0 == 0 ? 1 : 0);
+    consumer_sync();                                   // the last pair's sums have been read
+#pragma unroll
+    for (int x = 0; x < NB; ++x) {
+#pragma unroll
+      for (int h = 4; h < 32; h <<= 1) l[x] += __shfl_xor_sync(0xffffffffu, l[x], h);
+      if (lane < 4) {
+        s.m[warp][4 * x + lane] = m[x];
+        s.l[warp][4 * x + lane] = l[x];
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < (NB + 1) / 2; ++x) {
+      if (8 * x >= g.n_rows) break;
+      if (x) consumer_sync();                          // the first eight rows have been read
+#pragma unroll
+      for (int r = 0; r < (NB == 1 ? 4 : 8); ++r) store4(&s.merge[warp][r][4 * lane], o[8 * x + r]);
+      consumer_sync();
+      sum_warps<T, false>(a, g, s, x, whole, part);
+    }
+    if (!whole) join<T>(a, g, s);
   }
 }
 
@@ -664,8 +720,8 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
                                   CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// A layer's pool as {64 dims, page tokens, 2 halves, KV heads, pages}; a box is one page's (at most 64)
-// tokens of one head, its two 64-dim halves one after the other.
+// A layer's pool; a box is one page's tokens (at most a tile's) of one head.  bf16: {64 dims, tokens, 2 halves, KV heads,
+// pages}, the two 64-dim halves one after the other, 128-byte swizzle.  float32: {128 dims, tokens, KV heads, pages}.
 bool make_pool_map(CUtensorMap* m, const void* base, const Cache& c) {
   static EncodeTiledFn enc = nullptr;    // resolved once; the driver symbol never changes
   if (!enc) {
@@ -676,14 +732,20 @@ bool make_pool_map(CUtensorMap* m, const void* base, const Cache& c) {
       return false;
     enc = reinterpret_cast<EncodeTiledFn>(ptr);
   }
-  const cuuint64_t row = kD * 2;
-  cuuint64_t dims[5] = {64, (cuuint64_t)c.page, 2, (cuuint64_t)c.Hkv, (cuuint64_t)c.n_pages};
-  cuuint64_t strides[4] = {row, 128, row * c.page, (cuuint64_t)c.page_bytes};
-  cuuint32_t box[5] = {64, (cuuint32_t)(c.page < kTile ? c.page : kTile), 2, 1, 1};
-  cuuint32_t estr[5] = {1, 1, 1, 1, 1};
-  return enc(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 5, const_cast<void*>(base), dims, strides, box, estr,
-             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+  const bool bf16 = c.elem == 2;
+  const cuuint64_t row = (cuuint64_t)kD * c.elem, page = row * c.page;
+  const cuuint32_t tile = bf16 ? kTileOf<__nv_bfloat16> : kTileOf<float>, R = c.page < (int)tile ? c.page : tile;
+  const cuuint64_t dims5[5] = {64, (cuuint64_t)c.page, 2, (cuuint64_t)c.Hkv, (cuuint64_t)c.n_pages};
+  const cuuint64_t strides5[4] = {row, 128, page, (cuuint64_t)c.page_bytes};
+  const cuuint32_t box5[5] = {64, R, 2, 1, 1};
+  const cuuint64_t dims4[4] = {kD, (cuuint64_t)c.page, (cuuint64_t)c.Hkv, (cuuint64_t)c.n_pages};
+  const cuuint64_t strides4[3] = {row, page, (cuuint64_t)c.page_bytes};
+  const cuuint32_t box4[4] = {kD, R, 1, 1};
+  const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+  return enc(m, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT32, bf16 ? 5 : 4,
+             const_cast<void*>(base), bf16 ? dims5 : dims4, bf16 ? strides5 : strides4, bf16 ? box5 : box4, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, bf16 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_NONE,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 constexpr int kMaxCtas = 2 * 256;      // CTAs the workspace has room for (two per SM)
@@ -717,36 +779,26 @@ cudaError_t launch_paged_attn(bool bf16, const Cache& c, int layer, int n, int H
   a.max_seqs = c.max_seqs;
   a.max_pages = c.max_pages;
   a.n_pages = c.n_pages;
-  a.page_elems = c.page_bytes / c.elem;
-  a.k_pool = static_cast<const char*>(k_pool) + layer * c.layer_bytes;
-  a.v_pool = static_cast<const char*>(v_pool) + layer * c.layer_bytes;
   a.c2 = scale * kLog2e;
   a.wait_ns = wait_ns;
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  // no more CTAs than tiles there can be
-  const int64_t tiles = (int64_t)n * c.Hkv * a.subs * (((int64_t)c.max_pages * c.page + kTile - 1) / kTile);
-  auto grid_of = [&](int per_sm) {
-    int64_t g = (int64_t)sms * per_sm;
-    if (g > kMaxCtas) g = kMaxCtas;
-    return dim3((unsigned)(g < tiles ? g : tiles));
-  };
-  if (bf16) {
-    CUtensorMap mk, mv;
-    if (!make_pool_map(&mk, a.k_pool, c) || !make_pool_map(&mv, a.v_pool, c)) return cudaErrorInvalidValue;
-    auto kernel = a.G <= 8 ? paged_mma_kernel<1> : paged_mma_kernel<2>;
-    const size_t smem = sizeof(MmaSmem);
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    return launch_dependent(kernel, grid_of(2), dim3(kMmaThreads), smem, st, 1, mk, mv, a);
-  }
-  auto kernel = paged_simt_kernel<float>;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(SimtSmem));
+  CUtensorMap mk, mv;
+  if (!make_pool_map(&mk, static_cast<const char*>(k_pool) + layer * c.layer_bytes, c) ||
+      !make_pool_map(&mv, static_cast<const char*>(v_pool) + layer * c.layer_bytes, c))
+    return cudaErrorInvalidValue;
+  auto kernel = bf16 ? (a.G <= 8 ? paged_bf16_kernel<1> : paged_bf16_kernel<2>) : (a.G <= 4 ? paged_f32_kernel<1> : a.G <= 8 ? paged_f32_kernel<2> : paged_f32_kernel<4>);
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
   if (e != cudaSuccess) return e;
-  static_assert(2 * (sizeof(SimtSmem) + 1024) <= 228 * 1024, "two CTAs per SM");
-  return launch_dependent(kernel, grid_of(2), dim3(kConsumers), sizeof(SimtSmem), st, 1, a);
+  // two CTAs per SM, and no more than there can be units of work
+  const int64_t tile = bf16 ? kTileOf<__nv_bfloat16> : kTileOf<float>;
+  const int64_t units = (int64_t)n * c.Hkv * a.subs * (((int64_t)c.max_pages * c.page + tile - 1) / tile + kPairCost);
+  int64_t grid = 2LL * sms;
+  if (grid > kMaxCtas) grid = kMaxCtas;
+  if (grid > units) grid = units;
+  return launch_dependent(kernel, dim3((unsigned)grid), dim3(kThreads), sizeof(Smem), st, 1, mk, mv, a);
 }
 
 }  // namespace pages
