@@ -35,7 +35,9 @@ constexpr int kThreads = kConsumers + 32;
 constexpr int kStages = 3;
 constexpr uint32_t kTileBytes = 16384; // of K, and of V
 constexpr int kWindow = 32;            // queries whose row and length are kept in shared memory
-constexpr int kPairCost = 2;           // tiles: measured, a pair's start and end cost about 4500 cycles, a tile 2200
+// What a pair's start and end cost, in tiles.  Batch of 48 ragged requests, 32/8 heads: 78.8 us with 0, 72.7 with 1, 69.8
+// with 3, 70.2 with 4; 32/4 heads: 50.8, 46.0, 43.1, 42.9; equal lengths: 70 us with any.
+constexpr int kPairCost = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kErrArg = -1;
 
@@ -224,7 +226,7 @@ __device__ __forceinline__ void emit(const Args& a, const Segment& g, int r, int
 }
 
 // After a CTA's part of a split pair is in the workspace: the last CTA to get here adds the parts up, in order.  Called by the
-// 128 consumer threads; a warp has the rows w, w + 4, ..., whose parts are all in flight together.
+// 128 consumer threads; a warp has the rows w, w + 4, ...  (One part after another took up to 33000 cycles under load.)
 template <typename T>
 __device__ __forceinline__ void join(const Args& a, const Segment& g, Smem& s) {
   const int64_t c0 = cta_of(g.tile0, s.range.total, s.range.n_cta), c1 = cta_of(g.tile0 + g.nt - 1, s.range.total, s.range.n_cta);
@@ -240,6 +242,7 @@ __device__ __forceinline__ void join(const Args& a, const Segment& g, Smem& s) {
   if (!s.flag) return;
   __threadfence();
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  auto part = [&](int p) -> const Part* { return a.parts + (p == 0 ? 2 * c0 + 1 : 2 * (c0 + p)); };
   float m[4], l[4];
   float4 acc[4];
 #pragma unroll
@@ -248,23 +251,47 @@ __device__ __forceinline__ void join(const Args& a, const Segment& g, Smem& s) {
     l[y] = 0.f;
     acc[y] = make_float4(0.f, 0.f, 0.f, 0.f);
   }
-#pragma unroll 2
-  for (int p = 0; p < n; ++p) {
-    const Part* x = a.parts + (p == 0 ? 2 * c0 + 1 : 2 * (c0 + p));
+  for (int p0 = 0; p0 < n; p0 += 32) {                 // 32 parts: a lane has the statistics of one
+    float f[4], lp[4];
 #pragma unroll
     for (int y = 0; y < 4; ++y) {
-      const int row = warp + 4 * y;
-      if (row >= g.n_rows) break;
-      const float mp = __ldcg(&x->m[row]), lp = __ldcg(&x->l[row]);
-      const float4 v = __ldcg(reinterpret_cast<const float4*>(x->o + row * kD) + lane);
-      const float mn = fmaxf(m[y], mp), ref = mn == -INFINITY ? 0.f : mn;
-      const float f = exp2f(m[y] - ref), e = exp2f(mp - ref);
+      const bool in = p0 + lane < n && warp + 4 * y < g.n_rows;
+      f[y] = in ? __ldcg(&part(p0 + lane)->m[warp + 4 * y]) : -INFINITY;
+      lp[y] = in ? __ldcg(&part(p0 + lane)->l[warp + 4 * y]) : 0.f;
+    }
+#pragma unroll
+    for (int y = 0; y < 4; ++y) {
+      float mn = f[y];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) mn = fmaxf(mn, __shfl_xor_sync(0xffffffffu, mn, o));
+      mn = fmaxf(mn, m[y]);
+      const float ref = mn == -INFINITY ? 0.f : mn, old = exp2f(m[y] - ref);
       m[y] = mn;
-      l[y] = l[y] * f + lp * e;
-      acc[y].x = acc[y].x * f + v.x * e;
-      acc[y].y = acc[y].y * f + v.y * e;
-      acc[y].z = acc[y].z * f + v.z * e;
-      acc[y].w = acc[y].w * f + v.w * e;
+      f[y] = exp2f(f[y] - ref);
+      float x = f[y] * lp[y];
+#pragma unroll
+      for (int o = 16; o > 0; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+      l[y] = l[y] * old + x;
+      acc[y].x *= old; acc[y].y *= old; acc[y].z *= old; acc[y].w *= old;
+    }
+    const int np = min(32, n - p0);
+    for (int p = 0; p < np; p += 4) {
+      float4 v[4][4];                                  // four parts of up to four rows in flight
+#pragma unroll
+      for (int z = 0; z < 4; ++z)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          v[z][y] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (p + z < np && warp + 4 * y < g.n_rows)
+            v[z][y] = __ldcg(reinterpret_cast<const float4*>(part(p0 + p + z)->o + (warp + 4 * y) * kD) + lane);
+        }
+#pragma unroll
+      for (int z = 0; z < 4; ++z)
+#pragma unroll
+        for (int y = 0; y < 4; ++y) {
+          const float e = __shfl_sync(0xffffffffu, f[y], p + z);       // (0 past the last part)
+          acc[y].x += e * v[z][y].x; acc[y].y += e * v[z][y].y; acc[y].z += e * v[z][y].z; acc[y].w += e * v[z][y].w;
+        }
     }
   }
 #pragma unroll
