@@ -414,7 +414,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const int r = row0 + g + 8 * x;
-        const int lim = w.t0 + r < w.len ? w.t0 + r - col0 : -1;    // last key that the row attends
+        // last key that the row attends; a sequence's first token attends one key, whose ds is 0 (dp - delta would be the
+        // rounding of two sums of the same terms)
+        const int lim = w.t0 + r < w.len && w.t0 + r > 0 ? w.t0 + r - col0 : -1;
         const float ls = s_lse[r], dl = s_delta[r];
 #pragma unroll
         for (int n = 0; n < NC; ++n)
@@ -516,7 +518,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool seen = t >= w.t0 + row0 + g + 8 * x && t < w.len;
             const float y = seen ? exp2f(s[n][2 * x + e] * c2 - ls) : 0.f;
             s[n][2 * x + e] = y;
-            dp[n][2 * x + e] = seen ? y * (dp[n][2 * x + e] - dl) : 0.f;
+            dp[n][2 * x + e] = seen && t > 0 ? y * (dp[n][2 * x + e] - dl) : 0.f;   // (token 0: one key, ds = 0)
           }
         }
       mul_pb<false>(gv, s, gt, nullptr);

@@ -387,8 +387,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (!ok) break;
         tc_fence_after();
         const uint32_t tS = tmem + lane_off + (uint32_t)(J & 1) * 128 + c0;
-        // of this warpgroup's keys, those that the row attends (none for a row outside the sequence)
-        const int nvalid = in ? t_pos - j * kBN + 1 - c0 : 0;
+        // of this warpgroup's keys, those that the row attends (none for a row outside the sequence, nor for a sequence's
+        // first token: it attends one key, whose dS is 0, where dP - delta would be the rounding of two sums)
+        const int nvalid = in && t_pos > 0 ? t_pos - j * kBN + 1 - c0 : 0;
         uint64_t pr[16];
         {
           uint32_t sv[32];
@@ -712,6 +713,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       // query column c of this step is token i tq + c / pk of the tile's own tokens: columns before `from` are not
       // attended by it
       const int from = i < diag_steps ? (r - i * tq) * p.pk - 32 * hc : 0;
+      const int dfrom = t0 == 0 && i == 0 ? max(from, p.pk - 32 * hc) : from;      // (token 0: one key, dS = 0)
       auto pairs = [&](bool masked) {
 #pragma unroll
         for (int e = 0; e < 32; e += 2) {
@@ -723,15 +725,15 @@ __global__ void __launch_bounds__(kThreads, 1)
           unpair(mul2(pair(p0, p1), add2(pair(__uint_as_float(dv[e]), __uint_as_float(dv[e + 1])), nd)), d0, d1);
           if (masked) {
             p0 = e >= from ? p0 : 0.f;
-            d0 = e >= from ? d0 : 0.f;
+            d0 = e >= dfrom ? d0 : 0.f;
             p1 = e + 1 >= from ? p1 : 0.f;
-            d1 = e + 1 >= from ? d1 : 0.f;
+            d1 = e + 1 >= dfrom ? d1 : 0.f;
           }
           pp[e >> 1] = pack_bf16(p0, p1);
           pd[e >> 1] = pack_bf16(d0, d1);
         }
       };
-      if (__any_sync(0xffffffffu, from > 0)) pairs(true);
+      if (__any_sync(0xffffffffu, dfrom > 0)) pairs(true);
       else pairs(false);
       // packed bf16 stays inside this warpgroup's own (already read) column range
       tmem_st16(tS + 32 * hc, pp);
