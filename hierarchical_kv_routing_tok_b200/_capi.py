@@ -111,8 +111,8 @@ def load() -> ctypes.CDLL:
         "hga_tier_plan": [C, P, P, P, P, P, P],
         "hga_tier_gather": [C, P, P, P, P, P, P, P],
         "hga_packed_workspace_size": [K, ctypes.POINTER(ctypes.c_size_t)],
-        "hga_packed_attn_fwd": [K, P, P, P, P, P, P, P, P],
-        "hga_packed_attn_bwd": [K, P, P, P, P, P, P, P, P, P, P, P, P],
+        "hga_packed_attn_fwd": [K, P, P, P, P, P, P, P, P, P],
+        "hga_packed_attn_bwd": [K, P, P, P, P, P, P, P, P, P, P, P, P, P],
         "hga_pages_workspace_size": [G, I, ctypes.POINTER(ctypes.c_size_t)],
         "hga_pages_reserve": [G, I, P, P, P, P, P, P, P, P],
         "hga_pages_write": [G, I, I, P, P, P, L, P, L, L, P, L, L, P, P, P, P, P, P],
@@ -268,12 +268,13 @@ def packed_workspace_size(cfg: PackedConfig) -> int:
     return int(out.value)
 
 
-def packed_attn_fwd(cfg, q, k, v, cu_seqlens, o, lse, workspace, stream=0) -> None:
-    _call("hga_packed_attn_fwd", ctypes.byref(cfg), q, k, v, cu_seqlens, o, lse, workspace, stream)
+def packed_attn_fwd(cfg, q, k, v, cu_seqlens, o, o_lo, lse, workspace, stream=0) -> None:
+    _call("hga_packed_attn_fwd", ctypes.byref(cfg), q, k, v, cu_seqlens, o, o_lo, lse, workspace, stream)
 
 
-def packed_attn_bwd(cfg, q, k, v, cu_seqlens, o, lse, d_o, dq, dk, dv, workspace, stream=0) -> None:
-    _call("hga_packed_attn_bwd", ctypes.byref(cfg), q, k, v, cu_seqlens, o, lse, d_o, dq, dk, dv, workspace, stream)
+def packed_attn_bwd(cfg, q, k, v, cu_seqlens, o, o_lo, lse, d_o, dq, dk, dv, workspace, stream=0) -> None:
+    _call("hga_packed_attn_bwd", ctypes.byref(cfg), q, k, v, cu_seqlens, o, o_lo, lse, d_o, dq, dk, dv, workspace,
+          stream)
 
 
 def pages_workspace_size(cfg: PagesConfig, Hq: int) -> int:

@@ -32,10 +32,10 @@ cudaError_t launch_fwd_f32(const void* q, const void* k, const void* v, void* o,
 cudaError_t launch_bwd_f32(const void* q, const void* k, const void* v, const void* o, const float* lse,
                            const void* d_o, float* delta, void* dq, void* dk, void* dv, const Header* hdr,
                            const Tile* by_query, const Tile* by_key, const Problem& p, cudaStream_t st);
-cudaError_t launch_fwd_tc(const void* q, const void* k, const void* v, void* o, float* lse, const Header* hdr,
-                          const Tile* list, const Problem& p, cudaStream_t st);
-cudaError_t launch_bwd_tc(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* d_o,
-                          float* stats, void* dq, void* dk, void* dv, const Header* hdr, const Tile* by_query,
+cudaError_t launch_fwd_tc(const void* q, const void* k, const void* v, void* o, void* o_lo, float* lse,
+                          const Header* hdr, const Tile* list, const Problem& p, cudaStream_t st);
+cudaError_t launch_bwd_tc(const void* q, const void* k, const void* v, const void* o, const void* o_lo,
+                          const float* lse, const void* d_o, float* stats, void* dq, void* dk, void* dv, const Header* hdr, const Tile* by_query,
                           const Tile* by_key, const Problem& p, cudaStream_t st);
 
 // Rows of no sequence: zeros in a [total, H, 128] output, -inf in lse [H, total].  Called by every

@@ -27,6 +27,7 @@ struct BwdParams {
   int64_t total;
   float c2, scale;                         // scale * log2(e), scale
   const __nv_bfloat16* o;
+  const __nv_bfloat16* o_lo;               // or nullptr
   const float* lse;                        // [Hq, total]
   float* stats;                            // [2][Hq, total]: -lse log2(e), -delta; written by dQ for dK, dV
   __nv_bfloat16* dq;
@@ -329,11 +330,14 @@ __global__ void __launch_bounds__(kThreads, 1)
       // 64-column half at position c ^ (r mod 8)).  The four partial sums meet in TMEM column 384 + 32w (the first
       // of this warpgroup's dQ, read out for the previous unit, not rewritten before this unit's first dS K
       // product) and every thread adds them in order.
-      uint4 ov[4];
+      uint4 ov[4], lo[4];
       {
-        const uint4* orow = reinterpret_cast<const uint4*>(p.o + (row * p.Hq + head) * kD + c0);
+        const int64_t at = (row * p.Hq + head) * kD + c0;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) ov[c] = in ? orow[c] : make_uint4(0, 0, 0, 0);
+        for (int c = 0; c < 4; ++c) {
+          ov[c] = in ? reinterpret_cast<const uint4*>(p.o + at)[c] : make_uint4(0, 0, 0, 0);
+          lo[c] = in && p.o_lo ? reinterpret_cast<const uint4*>(p.o_lo + at)[c] : make_uint4(0, 0, 0, 0);
+        }
       }
       ok = wait_w(qdo_full, k & 1, abort_flag, p.status, p.wait_ns);
       if (!ok) break;
@@ -347,10 +351,12 @@ __global__ void __launch_bounds__(kThreads, 1)
                                (uint32_t)(r & 7) * 128u + ((uint32_t)((chunk & 7) ^ (r & 7)) << 4);
           const uint4 dv4 = *reinterpret_cast<const uint4*>(smem + L::kDO + off);
           const uint32_t a[4] = {ov[c].x, ov[c].y, ov[c].z, ov[c].w}, d4[4] = {dv4.x, dv4.y, dv4.z, dv4.w};
+          const uint32_t b[4] = {lo[c].x, lo[c].y, lo[c].z, lo[c].w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
-            acc0 = fmaf(__uint_as_float(a[e] << 16), __uint_as_float(d4[e] << 16), acc0);
-            acc1 = fmaf(__uint_as_float(a[e] & 0xffff0000u), __uint_as_float(d4[e] & 0xffff0000u), acc1);
+            acc0 = fmaf(__uint_as_float(a[e] << 16) + __uint_as_float(b[e] << 16), __uint_as_float(d4[e] << 16), acc0);
+            acc1 = fmaf(__uint_as_float(a[e] & 0xffff0000u) + __uint_as_float(b[e] & 0xffff0000u),
+                        __uint_as_float(d4[e] & 0xffff0000u), acc1);
           }
         }
         part = acc0 + acc1;
@@ -780,8 +786,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 int dq_tile(int G) { return 128 / packed_heads(G); }
 
-cudaError_t launch_bwd_tc(const void* q, const void* k, const void* v, const void* o, const float* lse, const void* d_o,
-                          float* stats, void* dq, void* dk, void* dv, const Header* hdr, const Tile* by_query,
+cudaError_t launch_bwd_tc(const void* q, const void* k, const void* v, const void* o, const void* o_lo,
+                          const float* lse, const void* d_o, float* stats, void* dq, void* dk, void* dv, const Header* hdr, const Tile* by_query,
                           const Tile* by_key, const Problem& p, cudaStream_t st) {
   const int pk = packed_heads(p.G);
   const Strided so{(int64_t)p.Hq * kD, kD};
@@ -792,7 +798,8 @@ cudaError_t launch_bwd_tc(const void* q, const void* k, const void* v, const voi
       !make_map_packed(&mdo64, d_o, p.Hq, p.total, so, pk, 64 / pk) ||
       !make_map_packed(&mk, k, p.Hkv, p.total, p.k, 1, kBN) || !make_map_packed(&mv, v, p.Hkv, p.total, p.v, 1, kBN))
     return cudaErrorInvalidValue;
-  BwdParams a{p.Hq, p.Hkv, p.G, pk, p.total, p.scale * kLog2eF, p.scale, static_cast<const __nv_bfloat16*>(o), lse, stats,
+  BwdParams a{p.Hq, p.Hkv, p.G, pk, p.total, p.scale * kLog2eF, p.scale, static_cast<const __nv_bfloat16*>(o),
+              static_cast<const __nv_bfloat16*>(o_lo), lse, stats,
               static_cast<__nv_bfloat16*>(dq), static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv), hdr,
               by_query, p.fill_tail, p.status, p.wait_ns};
   int dev = 0, sms = 0;

@@ -40,6 +40,7 @@ struct FwdParams {
   const __nv_bfloat16* v;                  // for the values that are not finite
   Strided vs;
   __nv_bfloat16* o;
+  __nv_bfloat16* o_lo;                     // what rounding took from o, or nullptr
   float* lse;
   const Header* hdr;
   const Tile* list;
@@ -84,6 +85,74 @@ __device__ __forceinline__ bool load_unit(const FwdParams& p, int64_t n_units, i
   }
   x->Tmax = max(x->T[0], x->T[1]);
   return true;
+}
+
+// A softmax warp's output: its 32 rows of 64 dims (two passes of 32) of the unnormalised O at tO.
+struct OutArgs {
+  int start, len, t0, kh, h0;
+  int tok0, row0;              // first token of the query tile after t0; the warp's first row in it
+  int dim0, t_pos;             // first dim; this lane's token
+  uint32_t tO, stage;
+  float inv;
+  bool fix;
+};
+__device__ __noinline__ void write_output(const FwdParams& p, const OutArgs w) {
+  const int lane = threadIdx.x & 31;
+  const bool store = w.t_pos < w.len;
+  // O / l as bf16, 32 dims at a time through this warp's 2 KB (16-byte pieces at position c ^ (row / 2 mod 4): no bank
+  // conflicts), so that the stores to global memory are whole 64-byte runs
+#pragma unroll 1
+  for (int cc = 0; cc < 2; ++cc) {
+    const int d0 = w.dim0 + 32 * cc;
+    uint32_t v[32];
+    tmem_ld32(w.tO + cc * 32, v);
+    tmem_wait_ld();
+    if (w.fix && store) {
+      // values of the diagonal tiles that were set to 0 for the product: each adds itself
+      for (int u = w.t0 / kBN * kBN; u <= w.t_pos; ++u) {
+        const __nv_bfloat16* vr = p.v + ((int64_t)w.start + u) * p.vs.t + w.kh * p.vs.h + d0;
+#pragma unroll
+        for (int e = 0; e < 32; ++e) {
+          const float y = __bfloat162float(vr[e]);
+          if (!isfinite(y)) v[e] = __float_as_uint(__uint_as_float(v[e]) + y);
+        }
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] = __float_as_uint(__uint_as_float(v[e]) * w.inv);
+    // o, then what its rounding took
+#pragma unroll 1
+    for (int part = 0; part < (p.o_lo ? 2 : 1); ++part) {
+      __nv_bfloat16* out = part ? p.o_lo : p.o;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        uint32_t w4[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int z = 8 * y + 2 * e;
+          w4[e] = pack_bf16(__uint_as_float(v[z]), __uint_as_float(v[z + 1]));
+          v[z] = __float_as_uint(__uint_as_float(v[z]) - __uint_as_float(w4[e] << 16));
+          v[z + 1] = __float_as_uint(__uint_as_float(v[z + 1]) - __uint_as_float(w4[e] & 0xffff0000u));
+        }
+        const uint32_t a = w.stage + lane * 64u + (uint32_t)((y ^ ((lane >> 1) & 3)) << 4);
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w4[0]), "r"(w4[1]), "r"(w4[2]), "r"(w4[3]) : "memory");
+      }
+      __syncwarp();
+      const int c = lane & 3;
+#pragma unroll
+      for (int y = 0; y < 4; ++y) {
+        const int rr = 8 * y + (lane >> 2), rt = w.row0 + rr;      // row of the warp, of the tile
+        const int t = w.t0 + w.tok0 + (rt >> p.pk_shift);
+        uint32_t w4[4];
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w4[0]), "=r"(w4[1]), "=r"(w4[2]), "=r"(w4[3])
+                     : "r"(w.stage + rr * 64u + (uint32_t)((c ^ ((rr >> 1) & 3)) << 4)));
+        if (t < w.len)
+          *reinterpret_cast<uint4*>(out + (((int64_t)w.start + t) * p.Hq + w.h0 + (rt & (p.pk - 1))) * kD + d0 + 8 * c) =
+              make_uint4(w4[0], w4[1], w4[2], w4[3]);
+      }
+      __syncwarp();
+    }
+  }
 }
 
 __global__ void __launch_bounds__(kThreads, 1)
@@ -258,6 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (p.fill_tail) {
       const int64_t worker = (int64_t)blockIdx.x * kSoftmax + st, workers = (int64_t)gridDim.x * kSoftmax;
       fill_tail_rows(p.o, p.Hq, p.hdr->end, p.total, worker, workers);
+      if (p.o_lo) fill_tail_rows(p.o_lo, p.Hq, p.hdr->end, p.total, worker, workers);
       fill_tail_lse(p.lse, p.Hq, p.hdr->end, p.total, worker, workers);
     }
     const int i = st >> 8, half = (st >> 7) & 1;
@@ -266,9 +336,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t lane_off = (uint32_t)(quarter * 32) << 16;
     const uint32_t tS = tmem + lane_off + i * 128 + 64 * half;
     const uint32_t tO = tmem + lane_off + 256 + i * 128 + 64 * half;
-    volatile int* s_need = reinterpret_cast<volatile int*>(smem + L::kNeed) + 2 * pair_id;      // + 16 * parity + half
+    const uint32_t s_need = sbase + L::kNeed + 8 * pair_id;             // + 64 * parity + 4 * half
     // a row's maximum or sum for the other warp: in the writer's part of the output staging
-    volatile float* s_row = reinterpret_cast<volatile float*>(smem + L::kO) + (8 * i + quarter) * 512 + lane;   // + 2048 * half
+    const uint32_t s_row = sbase + L::kO + (8 * i + quarter) * 2048 + 4 * lane;      // + 8192 * half
+    auto put = [](uint32_t a, uint32_t y) { asm volatile("st.shared.b32 [%0], %1;" ::"r"(a), "r"(y) : "memory"); };
+    auto get = [](uint32_t a) {
+      uint32_t y;
+      asm volatile("ld.shared.b32 %0, [%1];" : "=r"(y) : "r"(a) : "memory");
+      return y;
+    };
     auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + pair_id) : "memory"); };
     int ns = 0, no = 0;                                 // S tiles, outputs taken
     bool ok = true;
@@ -281,52 +357,59 @@ __global__ void __launch_bounds__(kThreads, 1)
         ok = wait_w(s_full(i), ns & 1, abort_flag, p.status, p.wait_ns);
         tc_fence_after();
         const int nvalid = t_pos - j * kBN + 1 - 64 * half;     // of this warp's keys, those that the row attends
-        uint32_t v[64];                                 // in one TMEM round trip
-        tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));
-        tmem_ld32(tS + 32, *reinterpret_cast<uint32_t(*)[32]>(&v[32]));
+        uint32_t v[32], v2[32];
+        tmem_ld32(tS, v);
+        tmem_ld32(tS + 32, v2);
         tmem_wait_ld();
-        if (__any_sync(0xffffffffu, nvalid < 64)) {
+        const bool masked = __any_sync(0xffffffffu, nvalid < 64);
+        auto mask = [&](uint32_t(&y)[32], int n) {
 #pragma unroll
-          for (int e = 0; e < 64; ++e)
-            if (e >= nvalid) v[e] = __float_as_uint(-INFINITY);
+          for (int e = 0; e < 32; ++e)
+            if (e >= n) y[e] = __float_as_uint(-INFINITY);
+        };
+        if (masked) {
+          mask(v, nvalid);
+          mask(v2, nvalid - 32);
         }
-        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};   // of the raw products (the scale is positive)
+        float mx[2] = {-INFINITY, -INFINITY};   // of the raw products (the scale is positive)
 #pragma unroll
-        for (int e = 0; e < 64; e += 8)
+        for (int e = 0; e < 32; e += 4)
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
+          for (int y = 0; y < 2; ++y) {
             mx[y] = max3(mx[y], __uint_as_float(v[e + 2 * y]), __uint_as_float(v[e + 2 * y + 1]));
-        float mt = fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * p.scale_log2;
+            mx[y] = max3(mx[y], __uint_as_float(v2[e + 2 * y]), __uint_as_float(v2[e + 2 * y + 1]));
+          }
+        float mt = fmaxf(mx[0], mx[1]) * p.scale_log2;
         // The reference moves only when the maximum grows by more than 2^8: rarely.  Each warp tells the other whether its
         // keys ask for it, and does the first 32 keys with the standing reference meanwhile.
         auto asks = [&](float y) { return y > m + kRescaleThreshold || (m == -INFINITY && y > -INFINITY); };
         const bool any = __any_sync(0xffffffffu, asks(mt));
-        if (lane == 0) s_need[16 * (j & 1) + half] = ok ? any : 2;      // (2: a wait expired; both warps leave here)
+        if (lane == 0) put(s_need + 64 * (j & 1) + 4 * half, ok ? any : 2);      // (2: a wait expired; both warps leave here)
         const uint64_t c2 = pair(p.scale_log2, p.scale_log2);
-        uint64_t rs[2] = {0ull, 0ull};
+        uint64_t rs = 0ull;
         uint32_t pk[16];
-        auto probs = [&](int cc) {                      // of 32 keys: their sum in float32, and as bf16 (the operand type)
+        auto probs = [&](const uint32_t(&y)[32]) {      // of 32 keys: their sum in float32, and as bf16 (the operand type)
           const float ref = m == -INFINITY ? 0.f : m;
           const uint64_t mr2 = pair(-ref, -ref);
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
             float p0, p1;
-            unpair(fma2(pair(__uint_as_float(v[cc * 32 + e]), __uint_as_float(v[cc * 32 + e + 1])), c2, mr2), p0, p1);
+            unpair(fma2(pair(__uint_as_float(y[e]), __uint_as_float(y[e + 1])), c2, mr2), p0, p1);
             p0 = ex2(p0);
             p1 = ex2(p1);
-            rs[(e >> 1) & 1] = add2(rs[(e >> 1) & 1], pair(p0, p1));
+            rs = add2(rs, pair(p0, p1));
             pk[e >> 1] = pack_bf16(p0, p1);
           }
         };
-        probs(0);
+        probs(v);
         pair_sync();
-        const int other = s_need[16 * (j & 1) + (half ^ 1)];
+        const int other = (int)get(s_need + 64 * (j & 1) + 4 * (half ^ 1));
         ok = ok && other != 2;
         if (!ok) break;
         if (any || other) {
-          s_row[2048 * half] = mt;
+          put(s_row + 8192 * half, __float_as_uint(mt));
           pair_sync();
-          mt = fmaxf(mt, s_row[2048 * (half ^ 1)]);
+          mt = fmaxf(mt, __uint_as_float(get(s_row + 8192 * (half ^ 1))));
           pair_sync();                                  // both have read
           const bool move = asks(mt);
           const float mnew = move ? mt : m, alpha = move ? ex2(m - mnew) : 1.f;      // m = -inf -> 0
@@ -343,22 +426,19 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           l *= alpha;
           m = mnew;
-          rs[0] = rs[1] = 0ull;
-          tmem_ld32(tS, *reinterpret_cast<uint32_t(*)[32]>(&v[0]));   // (not kept in registers for this)
+          rs = 0ull;
+          tmem_ld32(tS, v);                             // (not kept in registers for this)
           tmem_wait_ld();
-#pragma unroll
-          for (int e = 0; e < 32; ++e)
-            if (e >= nvalid) v[e] = __float_as_uint(-INFINITY);
-          probs(0);
+          if (masked) mask(v, nvalid);
+          probs(v);
         }
         // P stays within this warp's own (already read) columns
         tmem_st16(tS, pk);
-        probs(1);
+        probs(v2);
         tmem_st16(tS + 16, pk);
-        float r0, r1, r2, r3;
-        unpair(rs[0], r0, r1);
-        unpair(rs[1], r2, r3);
-        l += (r0 + r1) + (r2 + r3);
+        float r0, r1;
+        unpair(rs, r0, r1);
+        l += r0 + r1;
         tmem_wait_st();
         tc_fence_before();
         __syncwarp();
@@ -367,62 +447,17 @@ __global__ void __launch_bounds__(kThreads, 1)
       if (!ok) break;
       ok = wait_w(o_full(i), no & 1, abort_flag, p.status, p.wait_ns);
       ++no;
-      if (lane == 0) s_need[16 * (T & 1) + half] = ok ? 0 : 2;
-      s_row[2048 * half] = l;
+      if (lane == 0) put(s_need + 64 * (T & 1) + 4 * half, ok ? 0 : 2);
+      put(s_row + 8192 * half, __float_as_uint(l));
       pair_sync();
-      l = half ? s_row[0] + l : l + s_row[2048];          // the row's sum, in the same order in both warps
-      ok = ok && s_need[16 * (T & 1) + (half ^ 1)] != 2;
+      l += __uint_as_float(get(s_row + 8192 * (half ^ 1)));       // the row's sum (of two terms: the same in both warps)
+      ok = ok && get(s_need + 64 * (T & 1) + 4 * (half ^ 1)) != 2;
       pair_sync();
       if (!ok) break;
       tc_fence_after();
-      const float inv = 1.f / l;
-      const bool store = t_pos < x.len;
-      const bool fix = not_finite[k & 3] != 0;
-      // O / l as bf16, 32 dims at a time through this warp's 2 KB (16-byte pieces at position c ^ (row / 2 mod 4): no bank
-      // conflicts), so that the stores to global memory are whole 64-byte runs
-      const uint32_t stage = sbase + L::kO + (uint32_t)(st >> 5) * 2048u;
-#pragma unroll 1
-      for (int cc = 0; cc < 2; ++cc) {
-        const int d0 = 64 * half + 32 * cc;
-        uint32_t v[32];
-        tmem_ld32(tO + cc * 32, v);
-        tmem_wait_ld();
-        if (fix && store) {
-          // values of the diagonal tiles that were set to 0 for the product: each adds itself
-          for (int u = x.t0 / kBN * kBN; u <= t_pos; ++u) {
-            const __nv_bfloat16* vr = p.v + ((int64_t)x.start + u) * p.vs.t + x.kh * p.vs.h + d0;
-#pragma unroll
-            for (int e = 0; e < 32; ++e) {
-              const float y = __bfloat162float(vr[e]);
-              if (!isfinite(y)) v[e] = __float_as_uint(__uint_as_float(v[e]) + y);
-            }
-          }
-        }
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          uint32_t w4[4];
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            w4[e] = pack_bf16(__uint_as_float(v[8 * y + 2 * e]) * inv, __uint_as_float(v[8 * y + 2 * e + 1]) * inv);
-          const uint32_t a = stage + lane * 64u + (uint32_t)((y ^ ((lane >> 1) & 3)) << 4);
-          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(w4[0]), "r"(w4[1]), "r"(w4[2]), "r"(w4[3]) : "memory");
-        }
-        __syncwarp();
-        const int c = lane & 3;
-#pragma unroll
-        for (int y = 0; y < 4; ++y) {
-          const int rr = 8 * y + (lane >> 2), rt = quarter * 32 + rr;        // row of the warp, of the tile
-          const int t = x.t0 + i * p.tp + (rt >> p.pk_shift);
-          uint32_t w4[4];
-          asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(w4[0]), "=r"(w4[1]), "=r"(w4[2]), "=r"(w4[3])
-                       : "r"(stage + rr * 64u + (uint32_t)((c ^ ((rr >> 1) & 3)) << 4)));
-          if (t < x.len)
-            *reinterpret_cast<uint4*>(p.o + (((int64_t)x.start + t) * p.Hq + x.h0 + (rt & (p.pk - 1))) * kD + d0 + 8 * c) =
-                make_uint4(w4[0], w4[1], w4[2], w4[3]);
-        }
-        __syncwarp();
-      }
-      if (store && half == 0)
+      write_output(p, OutArgs{x.start, x.len, x.t0, x.kh, x.h0, i * p.tp, quarter * 32, 64 * half, t_pos, tO,
+                              sbase + L::kO + (uint32_t)(st >> 5) * 2048u, 1.f / l, not_finite[k & 3] != 0});
+      if (t_pos < x.len && half == 0)
         p.lse[(x.h0 + (r & (p.pk - 1))) * p.total + (int64_t)x.start + t_pos] = (m + __log2f(l)) * 0.6931471805599453f;
       tc_fence_before();
     }
@@ -463,15 +498,15 @@ bool make_map_packed(CUtensorMap* m, const void* base, int H, int64_t total, Str
 
 int fwd_tile(int G) { return 256 / packed_heads(G); }
 
-cudaError_t launch_fwd_tc(const void* q, const void* k, const void* v, void* o, float* lse, const Header* hdr,
-                          const Tile* list, const Problem& p, cudaStream_t st) {
+cudaError_t launch_fwd_tc(const void* q, const void* k, const void* v, void* o, void* o_lo, float* lse,
+                          const Header* hdr, const Tile* list, const Problem& p, cudaStream_t st) {
   const int pk = packed_heads(p.G);
   CUtensorMap mq, mk, mv;
   if (!make_map_packed(&mq, q, p.Hq, p.total, p.q, pk, 128 / pk) || !make_map_packed(&mk, k, p.Hkv, p.total, p.k, 1, kBN) ||
       !make_map_packed(&mv, v, p.Hkv, p.total, p.v, 1, kBN))
     return cudaErrorInvalidValue;
   FwdParams a{p.Hq, p.Hkv, p.G, pk, pk == 8 ? 3 : pk == 4 ? 2 : pk - 1, 128 / pk, p.Hkv * (p.G / pk), p.total, p.scale * kLog2eF,
-              static_cast<const __nv_bfloat16*>(v), p.v, static_cast<__nv_bfloat16*>(o), lse, hdr, list, p.fill_tail,
+              static_cast<const __nv_bfloat16*>(v), p.v, static_cast<__nv_bfloat16*>(o), static_cast<__nv_bfloat16*>(o_lo), lse, hdr, list, p.fill_tail,
               p.status, p.wait_ns};
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);

@@ -181,10 +181,11 @@ int hga_packed_workspace_size(const hga_packed_config_t* cfg, size_t* bytes_out)
 }
 
 int hga_packed_attn_fwd(const hga_packed_config_t* cfg, const void* q, const void* k, const void* v,
-                        const int32_t* cu_seqlens, void* o, float* lse, void* workspace, void* stream) {
+                        const int32_t* cu_seqlens, void* o, void* o_lo, float* lse, void* workspace, void* stream) {
   int rc = check_packed(cfg);
   if (rc) return rc;
   if (cfg->total > 0 && (rc = check_ptrs({q, k, v, o, lse}, 16))) return rc;
+  if (!aligned(o_lo, 16)) return HGA_ERR_ALIGN;
   if ((rc = check_ptrs({cu_seqlens}, 4))) return rc;
   if ((rc = check_workspace(workspace))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -196,16 +197,17 @@ int hga_packed_attn_fwd(const hga_packed_config_t* cfg, const void* q, const voi
   cudaError_t e = hga::packed::launch_plan(cu_seqlens, cfg->n_seqs, cfg->total, 1, &list, w.hdr, p.status,
                                            (cfg->flags & HGA_PACKED_CLEAR_STATUS) != 0, st);
   if (e != cudaSuccess || cfg->total == 0) return from_cuda(e);
-  return from_cuda((bf16 ? hga::packed::launch_fwd_tc : hga::packed::launch_fwd_f32)(q, k, v, o, lse, w.hdr, w.lists[0],
-                                                                                     p, st));
+  if (bf16) return from_cuda(hga::packed::launch_fwd_tc(q, k, v, o, o_lo, lse, w.hdr, w.lists[0], p, st));
+  return from_cuda(hga::packed::launch_fwd_f32(q, k, v, o, lse, w.hdr, w.lists[0], p, st));
 }
 
 int hga_packed_attn_bwd(const hga_packed_config_t* cfg, const void* q, const void* k, const void* v,
-                        const int32_t* cu_seqlens, const void* o, const float* lse, const void* d_o, void* dq,
-                        void* dk, void* dv, void* workspace, void* stream) {
+                        const int32_t* cu_seqlens, const void* o, const void* o_lo, const float* lse, const void* d_o,
+                        void* dq, void* dk, void* dv, void* workspace, void* stream) {
   int rc = check_packed(cfg);
   if (rc) return rc;
   if (cfg->total > 0 && (rc = check_ptrs({q, k, v, o, lse, d_o, dq, dk, dv}, 16))) return rc;
+  if (!aligned(o_lo, 16)) return HGA_ERR_ALIGN;
   if ((rc = check_ptrs({cu_seqlens}, 4))) return rc;
   if ((rc = check_workspace(workspace))) return rc;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
@@ -219,8 +221,11 @@ int hga_packed_attn_bwd(const hga_packed_config_t* cfg, const void* q, const voi
   cudaError_t e = hga::packed::launch_plan(cu_seqlens, cfg->n_seqs, cfg->total, 2, lists, w.hdr, p.status,
                                            (cfg->flags & HGA_PACKED_CLEAR_STATUS) != 0, st);
   if (e != cudaSuccess || cfg->total == 0) return from_cuda(e);
-  return from_cuda((bf16 ? hga::packed::launch_bwd_tc : hga::packed::launch_bwd_f32)(
-      q, k, v, o, lse, d_o, w.stats, dq, dk, dv, w.hdr, w.lists[0], w.lists[1], p, st));
+  if (bf16)
+    return from_cuda(hga::packed::launch_bwd_tc(q, k, v, o, o_lo, lse, d_o, w.stats, dq, dk, dv, w.hdr, w.lists[0],
+                                                w.lists[1], p, st));
+  return from_cuda(hga::packed::launch_bwd_f32(q, k, v, o, lse, d_o, w.stats, dq, dk, dv, w.hdr, w.lists[0], w.lists[1],
+                                               p, st));
 }
 
 int hga_pages_workspace_size(const hga_pages_config_t* cfg, int32_t Hq, size_t* bytes_out) {

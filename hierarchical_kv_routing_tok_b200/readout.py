@@ -106,9 +106,9 @@ def _with_flags(cfg, flags: int):
     return out
 
 
-def packed_attn_fwd(cfg, q, k, v, cu_seqlens, o=None, lse=None, workspace=None):
+def packed_attn_fwd(cfg, q, k, v, cu_seqlens, o=None, lse=None, workspace=None, o_lo=None):
     """Forward.  Rows of no sequence are left as they were in a given o / lse, and hold zeros / -inf in a new
-    one.  workspace: at least ``_capi.packed_workspace_size(cfg)`` bytes, zeroed once (``read_status``
+    one.  o_lo: an output like o for a backward pass in bfloat16, what rounding took from o.  workspace: at least ``_capi.packed_workspace_size(cfg)`` bytes, zeroed once (``read_status``
     tells of a cu_seqlens that is not valid); without one the call makes its own."""
     T, Hq, dev, flags = cfg.total, cfg.Hq, q.get_device(), cfg.flags
     if o is None and lse is None:
@@ -120,16 +120,19 @@ def packed_attn_fwd(cfg, q, k, v, cu_seqlens, o=None, lse=None, workspace=None):
     else:
         _flat(o, "o", (T, Hq, _D), q.dtype, dev)
         _flat(lse, "lse", (Hq, T), torch.float32, dev)
+    if o_lo is not None:
+        _flat(o_lo, "o_lo", (T, Hq, _D), q.dtype, dev)
     workspace, flags = _workspace(cfg, workspace, q, flags)
     with _on(dev):
         C.packed_attn_fwd(_with_flags(cfg, flags), q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(),
-                          o.data_ptr(), lse.data_ptr(), workspace.data_ptr(), _raw_stream(dev))
+                          o.data_ptr(), None if o_lo is None else o_lo.data_ptr(), lse.data_ptr(),
+                          workspace.data_ptr(), _raw_stream(dev))
     return o, lse
 
 
-def packed_attn_bwd(cfg, q, k, v, cu_seqlens, o, lse, d_o, dq=None, dk=None, dv=None, workspace=None):
-    """Gradients (contiguous) for d_o, from the forward's o and lse.  Rows of no sequence: as in
-    ``packed_attn_fwd`` (zeros in new gradients)."""
+def packed_attn_bwd(cfg, q, k, v, cu_seqlens, o, lse, d_o, dq=None, dk=None, dv=None, workspace=None, o_lo=None):
+    """Gradients (contiguous) for d_o, from the forward's o, lse and, in bfloat16 for the accuracy of short
+    sequences, o_lo.  Rows of no sequence: as in ``packed_attn_fwd`` (zeros in new gradients)."""
     T, Hq, Hkv, dev, flags = cfg.total, cfg.Hq, cfg.Hkv, q.get_device(), cfg.flags
     if dq is None and dk is None and dv is None:
         flags |= C.HGA_PACKED_FILL_TAIL
@@ -144,11 +147,13 @@ def packed_attn_bwd(cfg, q, k, v, cu_seqlens, o, lse, d_o, dq=None, dk=None, dv=
     _flat(o, "o", (T, Hq, _D), q.dtype, dev)
     _flat(d_o, "d_o", (T, Hq, _D), q.dtype, dev)
     _flat(lse, "lse", (Hq, T), torch.float32, dev)
+    if o_lo is not None:
+        _flat(o_lo, "o_lo", (T, Hq, _D), q.dtype, dev)
     workspace, flags = _workspace(cfg, workspace, q, flags)
     with _on(dev):
         C.packed_attn_bwd(_with_flags(cfg, flags), q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(),
-                          o.data_ptr(), lse.data_ptr(), d_o.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(),
-                          workspace.data_ptr(), _raw_stream(dev))
+                          o.data_ptr(), None if o_lo is None else o_lo.data_ptr(), lse.data_ptr(), d_o.data_ptr(),
+                          dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(), _raw_stream(dev))
     return dq, dk, dv
 
 
@@ -159,9 +164,10 @@ class _PackedAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, cu_seqlens, softmax_scale):
         cfg = make_packed_config(q, k, v, cu_seqlens, softmax_scale, _NEW)
-        o, lse = packed_attn_fwd(cfg, q, k, v, cu_seqlens)
+        o_lo = q.new_empty((cfg.total, cfg.Hq, _D)) if cfg.dtype == C.HGA_BF16 else None
+        o, lse = packed_attn_fwd(cfg, q, k, v, cu_seqlens, o_lo=o_lo)
         ctx.cfg = cfg
-        ctx.save_for_backward(q, k, v, cu_seqlens, o, lse)
+        ctx.save_for_backward(q, k, v, cu_seqlens, o, lse, o_lo)
         ctx.mark_non_differentiable(lse)
         ctx.set_materialize_grads(False)
         return o, lse
@@ -171,11 +177,11 @@ class _PackedAttention(torch.autograd.Function):
     def backward(ctx, d_o, _dlse):
         if d_o is None:
             return None, None, None, None, None
-        q, k, v, cu_seqlens, o, lse = ctx.saved_tensors
+        q, k, v, cu_seqlens, o, lse, o_lo = ctx.saved_tensors
         d_o = d_o.contiguous()
         if d_o.data_ptr() & 15:
             d_o = d_o.clone()
-        dq, dk, dv = packed_attn_bwd(ctx.cfg, q, k, v, cu_seqlens, o, lse, d_o)
+        dq, dk, dv = packed_attn_bwd(ctx.cfg, q, k, v, cu_seqlens, o, lse, d_o, o_lo=o_lo)
         return dq, dk, dv, None, None
 
 

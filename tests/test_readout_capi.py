@@ -63,17 +63,18 @@ def code(call):
 def test_packed_config(kw, want):
     assert code(lambda: C.packed_workspace_size(packed(**kw))) == want
     c = packed(**kw)
-    assert code(lambda: C.packed_attn_fwd(c, *[OK] * 7)) == want
-    assert code(lambda: C.packed_attn_bwd(c, *[OK] * 11)) == want
+    assert code(lambda: C.packed_attn_fwd(c, *[OK] * 8)) == want
+    assert code(lambda: C.packed_attn_bwd(c, *[OK] * 12)) == want
 
 
 def test_packed_pointers():
     c = packed()
-    for call, n in ((C.packed_attn_fwd, 6), (C.packed_attn_bwd, 10)):
+    for call, n in ((C.packed_attn_fwd, 7), (C.packed_attn_bwd, 11)):
         for i in range(n):
             args = [OK] * n
             args[i] = None
-            assert code(lambda: call(c, *args, OK)) == C.HGA_ERR_ARG
+            if i != 5:                                 # o_lo may be left out
+                assert code(lambda: call(c, *args, OK)) == C.HGA_ERR_ARG
             args[i] = ODD if i != 3 else OK + 2
             assert code(lambda: call(c, *args, OK)) == C.HGA_ERR_ALIGN
         assert code(lambda: call(c, *[OK] * n, None)) == C.HGA_ERR_WORKSPACE
