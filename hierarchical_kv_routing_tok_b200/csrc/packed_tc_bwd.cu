@@ -330,15 +330,10 @@ __global__ void __launch_bounds__(kThreads, 1)
       // 64-column half at position c ^ (r mod 8)).  The four partial sums meet in TMEM column 384 + 32w (the first
       // of this warpgroup's dQ, read out for the previous unit, not rewritten before this unit's first dS K
       // product) and every thread adds them in order.
-      uint4 ov[4], lo[4];
-      {
-        const int64_t at = (row * p.Hq + head) * kD + c0;
+      uint4 ov[4];
+      const int64_t at = (row * p.Hq + head) * kD + c0;
 #pragma unroll
-        for (int c = 0; c < 4; ++c) {
-          ov[c] = in ? reinterpret_cast<const uint4*>(p.o + at)[c] : make_uint4(0, 0, 0, 0);
-          lo[c] = in && p.o_lo ? reinterpret_cast<const uint4*>(p.o_lo + at)[c] : make_uint4(0, 0, 0, 0);
-        }
-      }
+      for (int c = 0; c < 4; ++c) ov[c] = in ? reinterpret_cast<const uint4*>(p.o + at)[c] : make_uint4(0, 0, 0, 0);
       ok = wait_w(qdo_full, k & 1, abort_flag, p.status, p.wait_ns);
       if (!ok) break;
       float part;
@@ -351,7 +346,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                                (uint32_t)(r & 7) * 128u + ((uint32_t)((chunk & 7) ^ (r & 7)) << 4);
           const uint4 dv4 = *reinterpret_cast<const uint4*>(smem + L::kDO + off);
           const uint32_t a[4] = {ov[c].x, ov[c].y, ov[c].z, ov[c].w}, d4[4] = {dv4.x, dv4.y, dv4.z, dv4.w};
-          const uint32_t b[4] = {lo[c].x, lo[c].y, lo[c].z, lo[c].w};
+          const uint4 lo = in && p.o_lo ? reinterpret_cast<const uint4*>(p.o_lo + at)[c] : make_uint4(0, 0, 0, 0);
+          const uint32_t b[4] = {lo.x, lo.y, lo.z, lo.w};
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             acc0 = fmaf(__uint_as_float(a[e] << 16) + __uint_as_float(b[e] << 16), __uint_as_float(d4[e] << 16), acc0);
@@ -491,10 +487,12 @@ static_assert(Smem::kBytes + 1024 <= 227 * 1024, "shared memory");
 // accumulate into the same TMEM dK, dV.  Warps: 0 loads Q and dO, 2 their lse and delta, 3 zeroes the rows past the
 // sequence in a head's last step, 1 products, 4..19 element-wise (thread = key row; warpgroups split the steps by
 // parity and the 64 query columns in two).
+// With cs = 2 a cluster of two CTAs takes the steps of a unit in turn; each then has half of the key rows to store, and
+// adds what the other, through its shared memory, has summed for them (two terms: the order does not matter).
 __global__ void __launch_bounds__(kThreads, 1)
     packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                           const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-                          const BwdParams p) {
+                          const BwdParams p, const int cs) {
   using L = Smem;
   extern __shared__ __align__(1024) uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
@@ -519,14 +517,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     fill_tail_rows(p.dk, p.Hkv, p.hdr->end, p.total, worker, workers);
     fill_tail_rows(p.dv, p.Hkv, p.hdr->end, p.total, worker, workers);
   }
-  if ((int)(blockIdx.x / p.Hkv) >= p.hdr->n_tiles[1]) return;
-  const int4 wk = __ldg(reinterpret_cast<const int4*>(p.list) + blockIdx.x / p.Hkv);
+  const int rank = (int)(blockIdx.x % cs), unit = (int)(blockIdx.x / cs);
+  if (unit / p.Hkv >= p.hdr->n_tiles[1]) return;        // (the whole cluster)
+  const int4 wk = __ldg(reinterpret_cast<const int4*>(p.list) + unit / p.Hkv);
   const int start = wk.x, len = wk.y, t0 = wk.z;
-  const int kh = blockIdx.x % p.Hkv;
+  const int kh = unit % p.Hkv;
   const int tq = BQ / p.pk;                 // tokens per step
   const int per = p.G / p.pk;               // passes over the queries, pk heads each
   const int Tq = (len - t0 + tq - 1) / tq;  // steps per pass
-  const int NJ = per * Tq;
+  const int NA = per * Tq;                  // steps of the unit; this CTA's are rank, rank + cs, ...
+  const int NJ = (NA - rank + cs - 1) / cs;
+  // this CTA's step j: pass and step within the pass
+  auto pass_of = [&](int j) { return (j * cs + rank) / Tq; };
+  auto step_of = [&](int j) { return (j * cs + rank) % Tq; };
   const bool ragged = (len - t0) % tq != 0; // a pass's last step holds rows past the sequence
 
   if (threadIdx.x == 0) {
@@ -554,6 +557,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  bool ew_ok = false;                       // an element-wise warp whose accumulators are complete
 
   if (warp == 0) {
     // ======================= TMA producer
@@ -563,9 +567,9 @@ __global__ void __launch_bounds__(kThreads, 1)
         tma_load_3d(sbase + L::kK + h * kHalfBytes, &tm_k, 64 * h, kh, start + t0, kv_full);
         tma_load_3d(sbase + L::kV + h * kHalfBytes, &tm_v, 64 * h, kh, start + t0, kv_full);
       }
-      int g = 0, i = 0, issued = 0;
+      int issued = 0;
       for (int j = 0; j < NJ; ++j) {
-        const int s = j % NS;
+        const int s = j % NS, g = pass_of(j), i = step_of(j);
         if (!mbar_wait(q_empty(s), ((j / NS) & 1) ^ 1, abort_flag, p.status, p.wait_ns)) break;
         mbar_arrive_expect_tx(q_full(s), 2 * kQTile);
         const int h0 = kh * p.G + g * p.pk, tok = start + t0 + i * tq;
@@ -574,7 +578,6 @@ __global__ void __launch_bounds__(kThreads, 1)
           tma_load_3d(sbase + L::kDO + s * kQTile + h * kQHalf, &tm_do, 64 * h, h0, tok, q_full(s));
         }
         ++issued;
-        if (++i == Tq) { i = 0; ++g; }
       }
       drain_wait(kv_full, 0, p.status);
       for (int j = issued > NS ? issued - NS : 0; j < issued; ++j) drain_wait(q_full(j % NS), (j / NS) & 1, p.status);
@@ -583,10 +586,9 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 2) {
     // ======================= lse and delta of each step's rows: 4-byte asynchronous copies (a row's place depends on
     // its head and token), zeros past the sequence
-    int g = 0, i = 0;
     bool ok = true;
     for (int j = 0; j < NJ; ++j) {
-      const int s = j % NS;
+      const int s = j % NS, g = pass_of(j), i = step_of(j);
       ok = ok && wait_w(q_empty(s), ((j / NS) & 1) ^ 1, abort_flag, p.status, p.wait_ns);
       if (!ok) break;
 #pragma unroll
@@ -599,19 +601,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst + BQ * 4), "l"(p.stats + p.Hq * p.total + at), "r"(n) : "memory");
       }
       asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(stat_full(s)) : "memory");
-      if (++i == Tq) { i = 0; ++g; }
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == 3) {
     // ======================= zeroes the rows past the sequence in each pass's last step
     bool ok = ragged;
-    int i = 0;
     for (int j = 0; ok && j < NJ; ++j) {
       const int s = j % NS;
       ok = wait_w(q_full(s), (j / NS) & 1, abort_flag, p.status, p.wait_ns);
       if (!ok) break;
-      if (++i == Tq) {
-        i = 0;
+      if (step_of(j) == Tq - 1) {
         const int rows = (len - t0 - (Tq - 1) * tq) * p.pk;
         zero_rows(sbase + L::kQ + s * kQTile, BQ, kQHalf, rows);
         zero_rows(sbase + L::kDO + s * kQTile, BQ, kQHalf, rows);
@@ -654,16 +653,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
     };
     uint32_t clean_phase = 0;               // bit s: parity of the next cleaned step in stage s
-    int ready = 0;                          // the step that step_ready() waits for, within its pass
     auto step_ready = [&](int j) {
       const int s = j % NS;
       bool ok = wait_w(q_full(s), (j / NS) & 1, abort_flag, p.status, p.wait_ns);
-      if (++ready == Tq) {
-        ready = 0;
-        if (ok && ragged) {
-          ok = wait_w(q_clean(s), (clean_phase >> s) & 1u, abort_flag, p.status, p.wait_ns);
-          clean_phase ^= 1u << s;
-        }
+      if (ok && ragged && step_of(j) == Tq - 1) {
+        ok = wait_w(q_clean(s), (clean_phase >> s) & 1u, abort_flag, p.status, p.wait_ns);
+        clean_phase ^= 1u << s;
       }
       tc_fence_after();
       return ok;
@@ -702,7 +697,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int diag_steps = (BM + tq - 1) / tq;                // steps that overlap the key tile
     const uint64_t c2 = pair(p.c2, p.c2);
     bool ok = true;
-    int i = b % Tq;
+    int i = step_of(b);
     for (int j = b; j < NJ; j += 2) {
       const int s = j % NS;
       ok = wait_w(stat_full(s), (j / NS) & 1, abort_flag, p.status, p.wait_ns) &&
@@ -748,33 +743,74 @@ __global__ void __launch_bounds__(kThreads, 1)
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(pd_full(b));
-      i += 2;
+      i += 2 * cs;
       while (i >= Tq) i -= Tq;
     }
-    // ---- epilogue: warpgroups 0, 1 own dV columns 0-63 / 64-127, warpgroups 2, 3 the same of dK
+    // (a CTA without steps, the second of a cluster that has one step, has nothing in its accumulators)
     if (ok) ok = wait_w(done, 0, abort_flag, p.status, p.wait_ns);
-    if (ok) {
+    ew_ok = ok;
+  }
+  // ---- epilogue: warpgroups 0, 1 own dV columns 0-63 / 64-127, warpgroups 2, 3 the same of dK
+  const int w4 = (warp - 4) >> 2;
+  const int er = (warp & 3) * 32 + lane;    // key row of an element-wise thread
+  const uint32_t tacc = tmem + ((uint32_t)((warp & 3) * 32) << 16) + (w4 >= 2 ? 384 : 256) + 64 * (w4 & 1);
+  const bool mine = cs == 1 || (er >> 6) == rank;        // (whole warps)
+  auto piece = [&](int c) {                 // of the exchange: 16-byte piece c of a warpgroup's 64 columns
+    return sbase + L::kQ + (uint32_t)(((w4 * 16 + c) * 64 + (er & 63)) * 16);
+  };
+  if (cs == 2) {
+    if (warp >= 4 && !mine && ew_ok) {
       tc_fence_after();
-      const bool is_dk = w4 >= 2;
-      const float mul = is_dk ? p.scale : 1.f;
-      __nv_bfloat16* base = is_dk ? p.dk : p.dv;
-      const bool v8 = (reinterpret_cast<uintptr_t>(base) & 31u) == 0;
-      const uint32_t tacc = tmem + lane_off + (is_dk ? 384 : 256) + 64 * (w4 & 1);
 #pragma unroll
       for (int y = 0; y < 2; ++y) {
-        uint32_t v[32], pk[16];
+        uint32_t v[32];
         tmem_ld32(tacc + 32 * y, v);
         tmem_wait_ld();
 #pragma unroll
-        for (int e = 0; e < 32; e += 2)
-          pk[e >> 1] = pack_bf16(__uint_as_float(v[e]) * mul, __uint_as_float(v[e + 1]) * mul);
-        if (t0 + r < len)
-          store32(base + (((int64_t)start + t0 + r) * p.Hkv + kh) * kD + 64 * (w4 & 1) + 32 * y, pk, v8);
+        for (int c = 0; c < 8; ++c)
+          asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(piece(8 * y + c)), "r"(NJ ? v[4 * c] : 0u),
+                       "r"(NJ ? v[4 * c + 1] : 0u), "r"(NJ ? v[4 * c + 2] : 0u), "r"(NJ ? v[4 * c + 3] : 0u)
+                       : "memory");
       }
+    }
+    __syncwarp();
+    cluster_sync();                         // (every thread of both CTAs, on the error path too)
+  }
+  if (warp >= 4 && mine && ew_ok) {
+    tc_fence_after();
+    const bool is_dk = w4 >= 2;
+    const float mul = is_dk ? p.scale : 1.f;
+    __nv_bfloat16* base = is_dk ? p.dk : p.dv;
+    const bool v8 = (reinterpret_cast<uintptr_t>(base) & 31u) == 0;
+#pragma unroll
+    for (int y = 0; y < 2; ++y) {
+      uint32_t v[32], pk[16];
+      tmem_ld32(tacc + 32 * y, v);
+      tmem_wait_ld();
+      if (cs == 2) {
+#pragma unroll
+        for (int c = 0; c < 8; ++c) {
+          uint32_t at;
+          float u[4];
+          asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(piece(8 * y + c)), "r"(rank ^ 1));
+          asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                       : "=f"(u[0]), "=f"(u[1]), "=f"(u[2]), "=f"(u[3]) : "r"(at) : "memory");
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            v[4 * c + e] = __float_as_uint((NJ ? __uint_as_float(v[4 * c + e]) : 0.f) + u[e]);
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 32; e += 2)
+        pk[e >> 1] = pack_bf16(__uint_as_float(v[e]) * mul, __uint_as_float(v[e + 1]) * mul);
+      if (t0 + er < len)
+        store32(base + (((int64_t)start + t0 + er) * p.Hkv + kh) * kD + 64 * (w4 & 1) + 32 * y, pk, v8);
     }
   }
   tc_fence_before();
-  __syncthreads();
+  __syncwarp();
+  if (cs == 2) cluster_sync();              // no CTA leaves while the other reads its sums
+  else __syncthreads();
   if (warp == 1) {
     tc_fence_after();
     tmem_dealloc(tmem, 512);
@@ -818,8 +854,11 @@ cudaError_t launch_bwd_tc(const void* q, const void* k, const void* v, const voi
   e = cudaFuncSetAttribute(dkdv::packed_dkdv_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = list_capacity(p.total, p.n_seqs, kKeyTile) * p.Hkv;
-  return launch_dependent(dkdv::packed_dkdv_tc_kernel, dim3((unsigned)(tiles < 1 ? 1 : tiles)), dim3(dkdv::kThreads), smem,
-                          st, 1, mq64, mdo64, mk, mv, a);
+  // Two CTAs per unit while there are fewer units than SMs.  Whole backward pass, 32/8 heads: 1024 tokens (64 units) 103 us
+  // with one, 73 with two; 2048 (128) 240 and 170; 4096 (256) 456 and 474; 8/8 heads, 4096 (256) 128 and 156.
+  const int cs = tiles < sms ? 2 : 1;
+  return launch_dependent(dkdv::packed_dkdv_tc_kernel, dim3((unsigned)((tiles < 1 ? 1 : tiles) * cs)), dim3(dkdv::kThreads),
+                          smem, st, (unsigned)cs, mq64, mdo64, mk, mv, a, cs);
 }
 
 }  // namespace packed
