@@ -113,7 +113,7 @@ def load() -> ctypes.CDLL:
         "hga_packed_workspace_size": [K, ctypes.POINTER(ctypes.c_size_t)],
         "hga_packed_attn_fwd": [K, P, P, P, P, P, P, P, P, P],
         "hga_packed_attn_bwd": [K, P, P, P, P, P, P, P, P, P, P, P, P, P],
-        "hga_pages_workspace_size": [G, I, ctypes.POINTER(ctypes.c_size_t)],
+        "hga_pages_workspace_size": [G, ctypes.POINTER(ctypes.c_size_t)],
         "hga_pages_reserve": [G, I, P, P, P, P, P, P, P, P],
         "hga_pages_write": [G, I, I, P, P, P, L, P, L, L, P, L, L, P, P, P, P, P, P],
         "hga_paged_attn": [G, I, I, I, ctypes.c_float, P, P, L, P, P, P, P, P, P, P, P],
@@ -277,9 +277,9 @@ def packed_attn_bwd(cfg, q, k, v, cu_seqlens, o, o_lo, lse, d_o, dq, dk, dv, wor
           stream)
 
 
-def pages_workspace_size(cfg: PagesConfig, Hq: int) -> int:
+def pages_workspace_size(cfg: PagesConfig) -> int:
     out = ctypes.c_size_t(0)
-    _call("hga_pages_workspace_size", ctypes.byref(cfg), int(Hq), ctypes.byref(out))
+    _call("hga_pages_workspace_size", ctypes.byref(cfg), ctypes.byref(out))
     return int(out.value)
 
 

@@ -510,7 +510,6 @@ __global__ void __launch_bounds__(kThreads, 1)
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
-  if (threadIdx.x == 0) pdl_trigger();
   pdl_wait();                               // the work list, lse and delta come from the kernels before
   if (p.fill_tail) {
     const int64_t worker = (int64_t)blockIdx.x * kThreads + threadIdx.x, workers = (int64_t)gridDim.x * kThreads;
@@ -557,6 +556,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
+  if (threadIdx.x == 0) pdl_trigger();      // (behind the allocation: no kernel behind this one can hold TMEM that it waits for)
   bool ew_ok = false;                       // an element-wise warp whose accumulators are complete
 
   if (warp == 0) {

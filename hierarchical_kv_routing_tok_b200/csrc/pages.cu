@@ -117,7 +117,7 @@ __global__ void __launch_bounds__(kPlanThreads) reserve_kernel(const Cache c, co
     int total;
     const int inc = block_scan(x, s.sums, &total);
     if (i < n) s.off[i] = need + inc - x;
-    need = min(need + total, 1 << 30);
+    need = (int)min((int64_t)need + total, (int64_t)1 << 30);      // (more than any pool has; a step adds up to 2^30 + 1024)
   }
   __syncthreads();
   int err = s.bad ? kErrArg : need > c.n_pages ? kErrPages : 0;

@@ -228,10 +228,10 @@ int hga_packed_attn_bwd(const hga_packed_config_t* cfg, const void* q, const voi
                                                p, st));
 }
 
-int hga_pages_workspace_size(const hga_pages_config_t* cfg, int32_t Hq, size_t* bytes_out) {
+int hga_pages_workspace_size(const hga_pages_config_t* cfg, size_t* bytes_out) {
   int rc = check_pages(cfg);
   if (rc) return rc;
-  if (!bytes_out || Hq < 1) return HGA_ERR_ARG;
+  if (!bytes_out) return HGA_ERR_ARG;
   *bytes_out = hga::kStatusBytes + 256 + 3 * page_list_bytes(cfg) + hga::pages::paged_attn_scratch_bytes();
   return HGA_OK;
 }

@@ -63,6 +63,15 @@ def _strides(t: torch.Tensor, name: str, T: int, H: int, dtype, dev: int) -> tup
     return st, sh
 
 
+def _scale(softmax_scale: float | None) -> float:
+    """For the library, to which 0 means 1 / sqrt(128)."""
+    if softmax_scale is None:
+        return 0.0
+    if not softmax_scale > 0:
+        raise ValueError(f"softmax_scale must be positive, got {softmax_scale}")
+    return float(softmax_scale)
+
+
 def make_packed_config(q, k, v, cu_seqlens, softmax_scale: float | None = None, flags: int = 0,
                        wait_limit_ns: int = 0) -> C.PackedConfig:
     """Configuration of packed attention from q [total, Hq, 128], k, v [total, Hkv, 128] and cu_seqlens
@@ -83,7 +92,7 @@ def make_packed_config(q, k, v, cu_seqlens, softmax_scale: float | None = None, 
         raise ValueError("cu_seqlens must be [n_seqs + 1]")
     _flat(cu_seqlens, "cu_seqlens", cu_seqlens.shape, torch.int32, dev)
     return C.PackedConfig(Hq, Hkv, _D, cu_seqlens.shape[0] - 1, T, qt, qh, kt, kh, vt, vh, _DT[dtype], flags,
-                          float(softmax_scale or 0.0), 0, wait_limit_ns)
+                          _scale(softmax_scale), 0, wait_limit_ns)
 
 
 def _workspace(cfg, workspace, q, flags: int):
@@ -108,8 +117,9 @@ def _with_flags(cfg, flags: int):
 
 def packed_attn_fwd(cfg, q, k, v, cu_seqlens, o=None, lse=None, workspace=None, o_lo=None):
     """Forward.  Rows of no sequence are left as they were in a given o / lse, and hold zeros / -inf in a new
-    one.  o_lo: an output like o for a backward pass in bfloat16, what rounding took from o.  workspace: at least ``_capi.packed_workspace_size(cfg)`` bytes, zeroed once (``read_status``
-    tells of a cu_seqlens that is not valid); without one the call makes its own."""
+    one.  o_lo: an output like o for a backward pass in bfloat16, what rounding took from o.  workspace: at least
+    ``_capi.packed_workspace_size(cfg)`` bytes, zeroed once (``read_status`` tells of a cu_seqlens that is not
+    valid); without one the call makes its own."""
     T, Hq, dev, flags = cfg.total, cfg.Hq, q.get_device(), cfg.flags
     if o is None and lse is None:
         flags |= C.HGA_PACKED_FILL_TAIL
@@ -185,6 +195,21 @@ class _PackedAttention(torch.autograd.Function):
         return dq, dk, dv, None, None
 
 
+def _check_accumulators(node, dev: int) -> None:
+    """The gradient accumulator of a leaf belongs to the stream of the call that made it, for as long as an
+    autograd graph holds it: noted at the first call, and compared in a capture."""
+    stream = _raw_stream(dev)
+    for acc, _ in node.next_functions:
+        if acc is not None and acc.name() == _ACCUMULATE \
+                and acc.metadata.setdefault("hga_stream", stream) != stream and acc.metadata["hga_stream"] == 0 \
+                and torch.cuda.is_current_stream_capturing():
+            raise RuntimeError("packed_attention: an autograd graph of q, k or v made on the default stream is still alive; "
+                               "its backward pass cannot be captured. Drop its outputs, or make them on the capture's stream")
+
+
+_ACCUMULATE = "torch::autograd::AccumulateGrad"
+
+
 def packed_attention(q, k, v, cu_seqlens, softmax_scale: float | None = None):
     """Causal attention over packed sequences: rows cu_seqlens[s] .. cu_seqlens[s+1] - 1 of q [total, Hq,
     128], k, v [total, Hkv, 128] are sequence s (int32, on the device, from 0, not decreasing, at most
@@ -192,9 +217,15 @@ def packed_attention(q, k, v, cu_seqlens, softmax_scale: float | None = None):
     Rows of no sequence give zeros and -inf, and zero gradients.
 
     q, k and v may be strided (slices of a fused projection, transposed head-major tensors); float32 or
-    bfloat16."""
+    bfloat16.
+
+    Forward and backward can be captured into a CUDA graph.  Where q, k or v is a leaf, no autograd graph of it
+    that an earlier call on the default stream made may be alive then: autograd would make that stream wait
+    for the captured one, which the capture does not allow.  Such a call is refused (RuntimeError)."""
     if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
-        return _PackedAttention.apply(q, k, v, cu_seqlens, softmax_scale)
+        out = _PackedAttention.apply(q, k, v, cu_seqlens, softmax_scale)
+        _check_accumulators(out[0].grad_fn, q.get_device())
+        return out
     return packed_attn_fwd(make_packed_config(q, k, v, cu_seqlens, softmax_scale, _NEW), q, k, v, cu_seqlens)
 
 
@@ -205,11 +236,11 @@ class PagedKVCache:
     page_table int32 [max_seqs, max_pages], seq_len int32 [max_seqs], ref_count int32 [n_pages] (the last
     two zero in an empty cache).  ``PagedKVCache.new`` allocates them.
 
-    Every call is asynchronous on the current stream.  A call with a bad entry, or with too few free pages,
+    Every call is asynchronous on the current stream; calls on one cache must not overlap in time (they share its
+    workspace).  A call with a bad entry, or with too few free pages,
     changes nothing and says so in ``status()``: HGA_ERR_ARG or HGA_ERR_PAGES of ``_capi``."""
 
-    def __init__(self, k_pool, v_pool, page_table, seq_len, ref_count, max_q_heads: int = 512,
-                 wait_limit_ns: int = 0):
+    def __init__(self, k_pool, v_pool, page_table, seq_len, ref_count, wait_limit_ns: int = 0):
         if k_pool.dtype not in _DT:
             raise ValueError(f"unsupported dtype {k_pool.dtype}")
         if k_pool.dim() != 5 or page_table.dim() != 2:
@@ -236,10 +267,9 @@ class PagedKVCache:
                                  layer_stride, page_stride, wait_limit_ns)
         self.k_pool, self.v_pool = k_pool, v_pool
         self.page_table, self.seq_len, self.ref_count = page_table, seq_len, ref_count
-        self.device, self.dtype, self.max_q_heads = k_pool.device, k_pool.dtype, max_q_heads
+        self.device, self.dtype = k_pool.device, k_pool.dtype
         self._dev = dev
-        self.workspace = torch.zeros(C.pages_workspace_size(self.cfg, max_q_heads), dtype=torch.uint8,
-                                     device=k_pool.device)
+        self.workspace = torch.zeros(C.pages_workspace_size(self.cfg), dtype=torch.uint8, device=k_pool.device)
         self._ints = (page_table.data_ptr(), seq_len.data_ptr(), ref_count.data_ptr())
         self._pools = (k_pool.data_ptr(), v_pool.data_ptr())
         self._ws = self.workspace.data_ptr()
@@ -295,8 +325,8 @@ class PagedKVCache:
         cached tokens of sequence row rows[i].  Returns (o [n, Hq, 128], lse [n, Hq] float32); an empty row
         gives zeros and -inf."""
         n = self._entries(rows, "rows")
-        if q.dim() != 3 or q.shape[1] > self.max_q_heads:
-            raise ValueError(f"q must be [n, heads, 128] with at most {self.max_q_heads} heads")
+        if q.dim() != 3:
+            raise ValueError("q must be [n, heads, 128]")
         Hq = q.shape[1]
         sn, sh = _strides(q, "q", n, Hq, self.dtype, self._dev)
         if sh != _D or sn < Hq * _D:
@@ -309,7 +339,7 @@ class PagedKVCache:
             lse = q.new_empty((n, Hq), dtype=torch.float32)
         else:
             _flat(lse, "lse", (n, Hq), torch.float32, self._dev)
-        self._call(C.paged_attn, self._layer(layer), n, Hq, float(softmax_scale or 0.0), rows.data_ptr(),
+        self._call(C.paged_attn, self._layer(layer), n, Hq, _scale(softmax_scale), rows.data_ptr(),
                    q.data_ptr(), sn, *self._ints[:2], *self._pools, o.data_ptr(), lse.data_ptr())
         return o, lse
 

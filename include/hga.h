@@ -393,8 +393,10 @@ HGA_API int hga_route_groups_cached(const hga_config_t* cfg, const float* qb, co
  * not decreasing, at most total; if it is not, no sequence is computed (all rows count as rows of
  * no sequence) and HGA_ERR_ARG is recorded in the workspace status word.
  * Products accumulate in float32.  bf16: probabilities and dS are rounded to bf16 before their second
- * product.  float32: each operand as the sum of two tf32 numbers, which keeps float32 accuracy.
- * total <= 2^31 - 1 - 256; total = 0 or n_seqs = 0 is a valid empty problem.
+ * product.  float32: each operand as the sum of two tf32 numbers, which keeps float32 accuracy (the
+ * scores of a q or k row that is not finite are NaN).
+ * total <= 2^31 - 1 - 256 and (total / 16 + n_seqs) * Hq < 2^31; total = 0 or n_seqs = 0 is a valid
+ * empty problem.
  * Two calls that may overlap in time need two workspaces. */
 enum hga_packed_flags {
   HGA_PACKED_FILL_TAIL = 1,   /* rows of no sequence: o, dq, dk, dv zeros, lse -inf */
@@ -453,8 +455,8 @@ typedef struct hga_pages_config {
   int64_t wait_limit_ns;    /* as in hga_config_t */
 } hga_pages_config_t;
 
-/* Bytes of workspace of the calls below, for attention with up to Hq query heads.  Zero-filled once. */
-HGA_API int hga_pages_workspace_size(const hga_pages_config_t* cfg, int32_t Hq, size_t* bytes_out);
+/* Bytes of workspace of the calls below.  Zero-filled once. */
+HGA_API int hga_pages_workspace_size(const hga_pages_config_t* cfg, size_t* bytes_out);
 
 /* Room for add[i] >= 0 new tokens behind sequence row rows[i]: takes the pages, adds to seq_len, and
  * sets pos[i] to the position of the first new token.  When nothing is changed, pos[i] = -1.

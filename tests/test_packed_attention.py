@@ -296,6 +296,118 @@ def test_broadcast_gradient(hga):
         assert torch.equal(x.grad, 2 * once[n])
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_autograd_in_a_graph(hga, dtype):
+    """Forward and backward through autograd, captured while an eager graph of the same leaves is alive: refused where it
+    was made on the default stream, and right where on the capture's."""
+    lens = [200, 1, 99]
+    q, k, v, d_o = make(lens, 4, 2, dtype)
+    cu = ends(lens)
+    leaves = [x.requires_grad_() for x in (q, k, v)]
+    side = torch.cuda.Stream()
+    alive = hga.packed_attention(*leaves, cu)          # an eager graph that stays
+    want = torch.autograd.grad(hga.packed_attention(*leaves, cu)[0], leaves, d_o)
+    side.wait_stream(torch.cuda.current_stream())
+    with pytest.raises(RuntimeError, match="still alive"):
+        with torch.cuda.graph(torch.cuda.CUDAGraph(), stream=side):
+            hga.packed_attention(*leaves, cu)
+    for a, b in zip(torch.autograd.grad(alive[0], leaves, d_o), want):
+        assert torch.equal(a, b)
+    del alive
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        alive = hga.packed_attention(*leaves, cu)
+        torch.autograd.grad(hga.packed_attention(*leaves, cu)[0], leaves, d_o)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        got = torch.autograd.grad(hga.packed_attention(*leaves, cu)[0], leaves, d_o)
+    for _ in range(2):
+        graph.replay()
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    with torch.cuda.stream(side):
+        late = torch.autograd.grad(alive[0], leaves, d_o)
+    torch.cuda.synchronize()
+    for a, b in zip(late, want):
+        assert torch.equal(a, b)
+
+
+def test_two_at_once(hga):
+    """Two problems on two streams, each with its own workspace, over and over."""
+    probs = []
+    for seed, lens in ((0, [700, 3, 128]), (1, [1, 400, 77, 512])):
+        q, k, v, d_o = make(lens, 8, 2, BF16, seed=seed)
+        probs.append((q, k, v, d_o, ends(lens)))
+    want = [run(hga, *p) for p in probs]
+    streams = [torch.cuda.Stream() for _ in probs]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(8):
+        for i, (s, p) in enumerate(zip(streams, probs)):
+            with torch.cuda.stream(s):
+                got[i].append(run(hga, *p))
+    torch.cuda.synchronize()
+    for i in range(2):
+        for g in got[i]:
+            for n in want[i]:
+                assert torch.equal(g[n], want[i][n]), n
+
+
+def test_more_than_2_31_elements(hga):
+    """Offsets beyond 32 bits: the last sequences of 530,000 packed rows of 32 heads."""
+    lens = [1000] * 529 + [513, 487]
+    T = sum(lens)
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    q, d_o = (torch.randn(T, 32, 128, generator=gen, device="cuda", dtype=BF16) for _ in range(2))
+    k, v = (torch.randn(T, 1, 128, generator=gen, device="cuda", dtype=BF16) for _ in range(2))
+    assert q.numel() > 2 ** 31
+    got = run(hga, q, k, v, d_o, ends(lens))
+    for a, b in ((T - 487, T), (T - 1000, T - 487), (0, 1000)):
+        ref = R.packed(q[a:b], k[a:b], v[a:b], [b - a], d_o=d_o[a:b])
+        for name in ("o", "dq", "dk", "dv"):
+            R.check(got[name][a:b], ref, name)
+
+
+@pytest.mark.parametrize("Hq,Hkv,lens", [(8, 2, [300, 65]), (4, 4, [2000] * 12)], ids=["paired", "single"])
+def test_expired_wait_is_recorded(hga, Hq, Hkv, lens):
+    """A wait limit shorter than a tile's load: the kernels give up, say so and return, and the next call is exact."""
+    q, k, v, d_o = make(lens, Hq, Hkv, BF16)
+    cu = ends(lens)
+    cfg = hga.make_packed_config(q, k, v, cu)
+    ws = torch.zeros(hga._capi.packed_workspace_size(cfg), dtype=torch.uint8, device="cuda")
+    want = run(hga, q, k, v, d_o, cu)
+    short = hga.make_packed_config(q, k, v, cu, wait_limit_ns=1)
+    hga.packed_attn_fwd(short, q, k, v, cu, workspace=ws)
+    assert hga.read_status(ws) == hga._capi.HGA_ERR_TIMEOUT
+    o, lse = hga.packed_attn_fwd(cfg, q, k, v, cu, workspace=ws)
+    assert hga.read_status(ws) == 0
+    hga.packed_attn_bwd(short, q, k, v, cu, o, lse, d_o, workspace=ws)
+    assert hga.read_status(ws) == hga._capi.HGA_ERR_TIMEOUT
+    got = run(hga, q, k, v, d_o, cu)
+    for n in want:
+        assert torch.equal(got[n], want[n]), n
+
+
+def test_rounding_kept_for_the_backward(hga):
+    """o + o_lo is the output to twice the digits, and brings the gradients of short sequences nearer."""
+    lens = [5, 3, 2, 7, 1, 4] * 40
+    q, k, v, d_o = make(lens, 8, 2, BF16)
+    cu = ends(lens)
+    cfg = hga.make_packed_config(q, k, v, cu)
+    lo = torch.empty_like(q)
+    o, lse = hga.packed_attn_fwd(cfg, q, k, v, cu, o_lo=lo)
+    ref = R.packed(q, k, v, lens, d_o=d_o)
+    assert (lo.abs().float() <= o.abs().float() * 2 ** -8 + 1e-30).all()
+    off = []
+    for x in (None, lo):
+        dq, dk, dv = hga.packed_attn_bwd(cfg, q, k, v, cu, o, lse, d_o, o_lo=x)
+        for n, g in (("dq", dq), ("dk", dk), ("dv", dv)):
+            R.check(g, ref, n)
+        off.append([((g.double() - ref[n]).norm() / ref[n].norm()).item() for n, g in (("dq", dq), ("dk", dk))])
+    assert off[1][0] < off[0][0] and off[1][1] < off[0][1]
+
+
 def test_refusals(hga):
     q, k, v, d_o = make([9], 4, 2, BF16)
     cu = ends([9])

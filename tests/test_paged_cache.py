@@ -449,6 +449,78 @@ def test_generation_matches_the_prompt(hga):
     R.check(cache.attend(0, a, i32([3]))[0][0], {"o": f["o"][:, 0], "e_o": f["e_o"][:, 0]}, "o")
 
 
+def test_more_than_2_31_elements(hga):
+    """A pool of more than 2^31 elements: pages at its end are written, attended, forked and moved."""
+    page, Hkv, P = 64, 8, 33000
+    cache = hga.PagedKVCache.new(1, P, page, Hkv, 3, 4 * page)
+    assert cache.k_pool.numel() > 2 ** 31
+    cache.ref_count[:P - 6] = 1                        # only the last six pages are free
+    gen = torch.Generator(device="cuda").manual_seed(0)
+    n = 150
+    k, v = (torch.randn(n, Hkv, 128, generator=gen, device="cuda", dtype=BF16) for _ in range(2))
+    row = i32([1])
+    cache.write(0, k, v, i32([0, n]), row, cache.reserve(row, i32([n])))
+    assert cache.status() == 0
+    assert cache.page_table[1, :3].tolist() == [P - 6, P - 5, P - 4]
+    q = torch.randn(2, 32, 128, generator=gen, device="cuda", dtype=BF16)
+    attend_and_check(cache, q, [1, 1])
+    cache.fork(row, i32([2]))
+    assert cache.page_table[2, :3].tolist() == [P - 6, P - 5, P - 3]
+    a, _ = cache.attend(0, q, i32([1, 2]))
+    attend_and_check(cache, q, [2, 1])
+    cache.ref_count[100:200] = 0
+    assert cache.compact().item() == P - 6 - 100 + 4
+    assert cache.page_table[2, :3].max().item() < 200
+    b, _ = cache.attend(0, q, i32([1, 2]))
+    assert cache.status() == 0 and torch.equal(a, b)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_expired_wait_is_recorded(hga, dtype):
+    cache, gen = filled(hga, [999, 3000, 5, 0, 1200], 64, 2, dtype)
+    q = torch.randn(5, 8, 128, generator=gen, device="cuda").to(dtype)
+    rows = i32([0, 1, 2, 3, 4])
+    want, _ = cache.attend(0, q, rows)
+    cache.cfg.wait_limit_ns = 1
+    cache.attend(0, q, rows)
+    assert cache.status() == hga._capi.HGA_ERR_TIMEOUT
+    cache.cfg.wait_limit_ns = 0
+    for _ in range(3):
+        got, _ = cache.attend(0, q, rows)
+        assert torch.equal(got, want)
+    assert cache.status() == 0
+
+
+def test_reserve_of_more_than_2_31_pages(hga):
+    """The pages asked for add up beyond 32 bits: refused, nothing changed."""
+    n, P = 2100, 1 << 20
+    cache = hga.PagedKVCache.new(1, P, 16, 1, n, 16 * (P + 64))
+    rows = torch.arange(n, dtype=torch.int32, device="cuda")
+    pos = cache.reserve(rows, torch.full_like(rows, 16 * (P + 64)))
+    assert cache.status() == hga._capi.HGA_ERR_PAGES
+    assert (pos == -1).all() and not cache.seq_len.any() and not cache.ref_count.any()
+    assert cache.reserve(rows, torch.full_like(rows, 17)).eq(0).all()
+    assert cache.status() == 0 and cache.ref_count.sum().item() == 2 * n
+
+
+def test_two_caches_at_once(hga):
+    """Attention over two caches on two streams, over and over."""
+    both = [filled(hga, lens, 32, 2, BF16, seed=i) for i, lens in enumerate(([2000, 17, 640], [5, 3000]))]
+    qs = [torch.randn(len(c.seq_len), 8, 128, generator=g, device="cuda").to(BF16) for c, g in both]
+    rows = [i32(list(range(len(c.seq_len)))) for c, _ in both]
+    want = [c.attend(0, q, r)[0] for (c, _), q, r in zip(both, qs, rows)]
+    streams = [torch.cuda.Stream() for _ in both]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(30):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                got[i].append(both[i][0].attend(0, qs[i], rows[i])[0])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert all(torch.equal(g, want[i]) for g in got[i])
+
+
 @pytest.mark.parametrize("dtype", [F32, BF16])
 def test_attend_is_reproducible(hga, dtype):
     lens = [999, 3000, 5, 0, 1200]

@@ -97,7 +97,7 @@ def test_packed_workspace_grows():
 ])
 def test_pages_config(kw, want):
     c = pages(**kw)
-    assert code(lambda: C.pages_workspace_size(c, 32)) == want
+    assert code(lambda: C.pages_workspace_size(c)) == want
     assert code(lambda: C.pages_reserve(c, 1, *[OK] * 7)) == want
     assert code(lambda: C.pages_free(c, 1, *[OK] * 5)) == want
     assert code(lambda: C.pages_compact(c, *[OK] * 7)) == want
@@ -106,8 +106,7 @@ def test_pages_config(kw, want):
 
 def test_pages_calls():
     c = pages()
-    assert C.pages_workspace_size(c, 32) > 0
-    assert code(lambda: C.pages_workspace_size(c, 0)) == C.HGA_ERR_ARG
+    assert C.pages_workspace_size(c) > 0
     attn = lambda layer=0, n=1, Hq=32, scale=0.0, stride=0, ptrs=(OK,) * 9: C.paged_attn(
         c, layer, n, Hq, scale, ptrs[0], ptrs[1], stride, *ptrs[2:])
     for kw, want in ((dict(layer=2), C.HGA_ERR_ARG), (dict(layer=-1), C.HGA_ERR_ARG), (dict(n=-1), C.HGA_ERR_ARG),
@@ -139,6 +138,6 @@ def test_pages_calls():
 
 def test_layers_side_by_side_are_accepted():
     data = 8 * 64 * 128
-    assert C.pages_workspace_size(pages(page_stride=4 * data, layer_stride=2 * data), 32) > 0
-    assert C.pages_workspace_size(pages(page_stride=4 * data, layer_stride=400 * data), 32) > 0
-    assert code(lambda: C.pages_workspace_size(pages(page_stride=2 * data, layer_stride=2 * data), 32)) == C.HGA_ERR_ARG
+    assert C.pages_workspace_size(pages(page_stride=4 * data, layer_stride=2 * data)) > 0
+    assert C.pages_workspace_size(pages(page_stride=4 * data, layer_stride=400 * data)) > 0
+    assert code(lambda: C.pages_workspace_size(pages(page_stride=2 * data, layer_stride=2 * data))) == C.HGA_ERR_ARG
