@@ -27,16 +27,18 @@ constexpr int kLeastTile = 16; // no kernel's tiles are shorter
 int fwd_tile(int G);           // tokens per unit of the bf16 forward
 int dq_tile(int G);            // tokens per unit of the bf16 dQ
 
-cudaError_t launch_fwd_f32(const void* q, const void* k, const void* v, void* o, float* lse, const Header* hdr,
-                           const Tile* list, const Problem& p, cudaStream_t st);
+int head_units(int Hkv, int G); // units of a tile of the bf16 forward and dQ
+
+cudaError_t launch_fwd_f32(const void* q, const void* k, const void* v, void* o, float* lse, const Work& work,
+                           const Problem& p, cudaStream_t st);
 cudaError_t launch_bwd_f32(const void* q, const void* k, const void* v, const void* o, const float* lse,
-                           const void* d_o, float* delta, void* dq, void* dk, void* dv, const Header* hdr,
-                           const Tile* by_query, const Tile* by_key, const Problem& p, cudaStream_t st);
+                           const void* d_o, float* delta, void* dq, void* dk, void* dv, const Work& by_query,
+                           const Work& by_key, const Problem& p, cudaStream_t st);
 cudaError_t launch_fwd_tc(const void* q, const void* k, const void* v, void* o, void* o_lo, float* lse,
-                          const Header* hdr, const Tile* list, const Problem& p, cudaStream_t st);
+                          const Work& work, const Problem& p, cudaStream_t st);
 cudaError_t launch_bwd_tc(const void* q, const void* k, const void* v, const void* o, const void* o_lo,
-                          const float* lse, const void* d_o, float* stats, void* dq, void* dk, void* dv, const Header* hdr, const Tile* by_query,
-                          const Tile* by_key, const Problem& p, cudaStream_t st);
+                          const float* lse, const void* d_o, float* stats, void* dq, void* dk, void* dv,
+                          const Work& by_query, const Work& by_key, const Problem& p, cudaStream_t st);
 
 // Rows of no sequence: zeros in a [total, H, 128] output, -inf in lse [H, total].  Called by every
 // thread of a grid of kernels that share the work by (worker, workers).

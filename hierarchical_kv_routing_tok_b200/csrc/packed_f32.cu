@@ -232,11 +232,10 @@ __device__ __forceinline__ void meet(float* tile, int grp, int row0, const float
 }
 
 // ------------------------------------------------------------------------------------ forward
-template <int RW>
+template <int RW, bool kOwn>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_fwd_f32_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
-                          float* __restrict__ o, float* __restrict__ lse, const Header* hdr, const Tile* list,
-                          const Problem p) {
+                          float* __restrict__ o, float* __restrict__ lse, const Work work, const Problem p) {
   extern __shared__ __align__(16) float f32_smem[];
   float* Qs = f32_smem;
   float* Ks = Qs + kTileFloats;            // two stages each
@@ -250,14 +249,21 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int g = lane >> 2, tq = lane & 3;
   pdl_trigger();
   pdl_wait();
+  __shared__ Own own;
+  if (kOwn) {
+    if (warp == 0) own_tile(work, blockIdx.x / p.Hq, &own);
+    __syncthreads();
+  }
   if (p.fill_tail) {
     const int64_t worker = (int64_t)blockIdx.x * kThreads + threadIdx.x, workers = (int64_t)gridDim.x * kThreads;
-    fill_tail_rows(o, p.Hq, hdr->end, p.total, worker, workers);
-    fill_tail_lse(lse, p.Hq, hdr->end, p.total, worker, workers);
+    const int64_t end = end_of<kOwn>(work, own);
+    fill_tail_rows(o, p.Hq, end, p.total, worker, workers);
+    fill_tail_lse(lse, p.Hq, end, p.total, worker, workers);
   }
   const int h = blockIdx.x % p.Hq, kh = h / p.G;
-  if ((int)(blockIdx.x / p.Hq) >= hdr->n_tiles[0]) return;
-  const Tile w = list[blockIdx.x / p.Hq];
+  if (blockIdx.x >= units_of<kOwn>(work, own, p.Hq)) return;
+  const int4 w4 = tile_of<kOwn>(work, own, blockIdx.x / p.Hq);
+  const Tile w{w4.x, w4.y, w4.z, 0};
   const int n_tiles = (int)((min((int64_t)w.t0 + kRows, (int64_t)w.len) - 1) / kCols) + 1;
   if (threadIdx.x == 0) s_found = 0;
   load_tile_async<kRows>(Qs, q, p.q, w, w.t0, h);
@@ -375,12 +381,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 
 // ------------------------------------------------------------------------------------ backward: dq
 // Forms delta of its rows and leaves it in `delta` [Hq, total] for the dk, dv kernel.
-template <int RW>
+template <int RW, bool kOwn>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_dq_f32_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
                          const float* __restrict__ o, const float* __restrict__ lse, const float* __restrict__ d_o,
-                         float* __restrict__ delta, float* __restrict__ dq, const Header* hdr, const Tile* list,
-                         const Problem p) {
+                         float* __restrict__ delta, float* __restrict__ dq, const Work work, const Problem p) {
   extern __shared__ __align__(16) float f32_smem[];
   float* Qs = f32_smem;
   float* Gs = Qs + kTileFloats;
@@ -394,12 +399,18 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int g = lane >> 2, tq = lane & 3;
   pdl_trigger();
   pdl_wait();
+  __shared__ Own own;
+  if (kOwn) {
+    if (warp == 0) own_tile(work, blockIdx.x / p.Hq, &own);
+    __syncthreads();
+  }
   if (p.fill_tail)
-    fill_tail_rows(dq, p.Hq, hdr->end, p.total, (int64_t)blockIdx.x * kThreads + threadIdx.x,
+    fill_tail_rows(dq, p.Hq, end_of<kOwn>(work, own), p.total, (int64_t)blockIdx.x * kThreads + threadIdx.x,
                    (int64_t)gridDim.x * kThreads);
   const int h = blockIdx.x % p.Hq, kh = h / p.G;
-  if ((int)(blockIdx.x / p.Hq) >= hdr->n_tiles[0]) return;
-  const Tile w = list[blockIdx.x / p.Hq];
+  if (blockIdx.x >= units_of<kOwn>(work, own, p.Hq)) return;
+  const int4 w4 = tile_of<kOwn>(work, own, blockIdx.x / p.Hq);
+  const Tile w{w4.x, w4.y, w4.z, 0};
   const Strided so{(int64_t)p.Hq * kD, kD};
   const int n_tiles = (int)((min((int64_t)w.t0 + kRows, (int64_t)w.len) - 1) / kCols) + 1;
   load_tile_async<kRows>(Qs, q, p.q, w, w.t0, h);
@@ -477,12 +488,12 @@ __global__ void __launch_bounds__(kThreads, 1)
 // The rows are keys, the columns the queries of the KV head's query heads, one head after another.  When there are
 // fewer (tile, KV head) units than SMs, the heads are split over a cluster of cs CTAs; their sums meet through
 // distributed shared memory, each CTA adding and storing its share of the rows in the order of the ranks.
-template <int RW>
+template <int RW, bool kOwn>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_dkdv_f32_kernel(const float* __restrict__ q, const float* __restrict__ k, const float* __restrict__ v,
                            const float* __restrict__ lse, const float* __restrict__ d_o,
                            const float* __restrict__ delta, float* __restrict__ dk, float* __restrict__ dv,
-                           const Header* hdr, const Tile* list, const Problem p, int cs) {
+                           const Work work, const Problem p, int cs) {
   extern __shared__ __align__(16) float f32_smem[];
   float* Ks = f32_smem;
   float* Vs = Ks + kTileFloats;
@@ -496,15 +507,22 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int g = lane >> 2, tq = lane & 3;
   pdl_trigger();
   pdl_wait();
+  const int rank = blockIdx.x % cs, unit = blockIdx.x / cs;
+  __shared__ Own own;
+  if (kOwn) {
+    if (warp == 0) own_tile(work, unit / p.Hkv, &own);
+    __syncthreads();
+  }
   if (p.fill_tail) {
     const int64_t worker = (int64_t)blockIdx.x * kThreads + threadIdx.x, workers = (int64_t)gridDim.x * kThreads;
-    fill_tail_rows(dk, p.Hkv, hdr->end, p.total, worker, workers);
-    fill_tail_rows(dv, p.Hkv, hdr->end, p.total, worker, workers);
+    const int64_t end = end_of<kOwn>(work, own);
+    fill_tail_rows(dk, p.Hkv, end, p.total, worker, workers);
+    fill_tail_rows(dv, p.Hkv, end, p.total, worker, workers);
   }
-  const int rank = blockIdx.x % cs, unit = blockIdx.x / cs;
   const int kh = unit % p.Hkv;
-  if (unit / p.Hkv >= hdr->n_tiles[1]) return;           // the whole cluster
-  const Tile w = list[unit / p.Hkv];
+  if (unit >= units_of<kOwn>(work, own, p.Hkv)) return;        // the whole cluster
+  const int4 w4 = tile_of<kOwn>(work, own, unit / p.Hkv);
+  const Tile w{w4.x, w4.y, w4.z, 0};
   const Strided so{(int64_t)p.Hq * kD, kD};
   const int hpc = p.G / cs, h0 = kh * p.G + rank * hpc;
   const int per_head = (w.len - w.t0 + kCols - 1) / kCols;      // query tiles from the key tile on
@@ -629,24 +647,24 @@ int f32_tile(int64_t total, int n_seqs, int units) {
   return list_capacity(total, n_seqs, 64) * units < sms ? 32 : 64;
 }
 
-cudaError_t launch_fwd_f32(const void* q, const void* k, const void* v, void* o, float* lse, const Header* hdr,
-                           const Tile* list, const Problem& p, cudaStream_t st) {
+cudaError_t launch_fwd_f32(const void* q, const void* k, const void* v, void* o, float* lse, const Work& work,
+                           const Problem& p, cudaStream_t st) {
   const int tile = f32_tile(p.total, p.n_seqs, p.Hq);
   const int64_t n = list_capacity(p.total, p.n_seqs, tile) * p.Hq;
-  return launch(tile == 32 ? packed_fwd_f32_kernel<2> : packed_fwd_f32_kernel<4>, n < 1 ? 1 : n, 5 * kTileBytesF, 1, st,
-                (const float*)q, (const float*)k, (const float*)v, (float*)o, lse, hdr, list, p);
+  return launch(tile == 64 ? packed_fwd_f32_kernel<4, false> : work.cu ? packed_fwd_f32_kernel<2, true> : packed_fwd_f32_kernel<2, false>, n < 1 ? 1 : n, 5 * kTileBytesF, 1, st,
+                (const float*)q, (const float*)k, (const float*)v, (float*)o, lse, work, p);
 }
 
 cudaError_t launch_bwd_f32(const void* q, const void* k, const void* v, const void* o, const float* lse,
-                           const void* d_o, float* delta, void* dq, void* dk, void* dv, const Header* hdr,
-                           const Tile* by_query, const Tile* by_key, const Problem& p, cudaStream_t st) {
+                           const void* d_o, float* delta, void* dq, void* dk, void* dv, const Work& by_query,
+                           const Work& by_key, const Problem& p, cudaStream_t st) {
   // (both lists by the query heads: a cluster may share out the heads of a key tile)
   const int tile = f32_tile(p.total, p.n_seqs, p.Hq);
   const int64_t tiles = list_capacity(p.total, p.n_seqs, tile);
   const int64_t nq = tiles * p.Hq, nk = tiles * p.Hkv;
-  cudaError_t e = launch(tile == 32 ? packed_dq_f32_kernel<2> : packed_dq_f32_kernel<4>, nq < 1 ? 1 : nq, 6 * kTileBytesF,
+  cudaError_t e = launch(tile == 64 ? packed_dq_f32_kernel<4, false> : by_query.cu ? packed_dq_f32_kernel<2, true> : packed_dq_f32_kernel<2, false>, nq < 1 ? 1 : nq, 6 * kTileBytesF,
                          1, st, (const float*)q, (const float*)k, (const float*)v, (const float*)o, lse,
-                         (const float*)d_o, delta, (float*)dq, hdr, by_query, p);
+                         (const float*)d_o, delta, (float*)dq, by_query, p);
   if (e != cudaSuccess) return e;
   int dev = 0, sms = 0;
   e = cudaGetDevice(&dev);
@@ -656,9 +674,9 @@ cudaError_t launch_bwd_f32(const void* q, const void* k, const void* v, const vo
   if (nk < sms)
     for (int c = 2; c <= 8; ++c)
       if (p.G % c == 0) cs = c;
-  return launch(tile == 32 ? packed_dkdv_f32_kernel<2> : packed_dkdv_f32_kernel<4>, (nk < 1 ? 1 : nk) * cs,
+  return launch(tile == 64 ? packed_dkdv_f32_kernel<4, false> : by_key.cu ? packed_dkdv_f32_kernel<2, true> : packed_dkdv_f32_kernel<2, false>, (nk < 1 ? 1 : nk) * cs,
                 6 * kTileBytesF, (unsigned)cs, st, (const float*)q, (const float*)k, (const float*)v, lse,
-                (const float*)d_o, (const float*)delta, (float*)dk, (float*)dv, hdr, by_key, p, cs);
+                (const float*)d_o, (const float*)delta, (float*)dk, (float*)dv, by_key, p, cs);
 }
 
 }  // namespace packed

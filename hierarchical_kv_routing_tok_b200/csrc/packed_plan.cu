@@ -4,7 +4,8 @@
 // tile + s + 1 (those ranges hold at least ceil(len / tile) slots each and need no prefix sum), found
 // by bisection.  The tiles are placed by a counting sort on their work, so that the kernels behind,
 // which deal the list out to the SMs in order, start the long tiles first and end with the short ones.
-// The order of tiles of equal work is left to the atomics: no result depends on it.
+// The order of tiles of equal work is left to the atomics: no result depends on it.  Few tiles of few sequences need no
+// list (own_tile).
 // Latency-bound (a few dependent shared-memory passes).
 #include "packed_plan.cuh"
 

@@ -31,6 +31,61 @@ struct ListSpec {
   Tile* list;
 };
 
+// The tiles of one list as a kernel gets them: from the plan kernel's list or, for few tiles, from cu_seqlens itself.
+struct Work {
+  const Header* hdr;
+  const Tile* list;
+  int which;            // of the header's two lists
+  const int32_t* cu;    // not nullptr: no plan kernel ran; each CTA finds the tile of its slot (own_tile)
+  int n_seqs, tile, clear_status;
+  int64_t total;
+  int* status;
+};
+
+// Sequences whose bounds fit the lanes of a warp.
+constexpr int kOwnSeqs = 31;
+
+// A CTA's only tile, in its shared memory.
+struct alignas(16) Own {
+  Tile tile;
+  int has, end;         // whether there is one; first row of no sequence
+};
+
+// The tile of slot i of the list (as in the plan kernel; slots without a tile stay), which is all that a kernel with a
+// CTA per unit needs: the order of the list matters only when some CTAs wait for others.  Called by one warp.
+__device__ __forceinline__ void own_tile(const Work& w, int slot, Own* own) {
+  const int lane = threadIdx.x & 31;
+  const int32_t c = w.cu[min(lane, w.n_seqs)], up = __shfl_up_sync(0xffffffffu, c, 1);
+  const bool bad = __any_sync(0xffffffffu, lane == 0 ? c != 0 : c < up || (lane == 31 && c > w.total));
+  if (blockIdx.x == 0 && lane == 0) {
+    if (w.clear_status) *w.status = 0;
+    if (bad) set_status(w.status, -1);
+  }
+  const int32_t end = __shfl_sync(0xffffffffu, c, 31);
+  const uint32_t before = __ballot_sync(0xffffffffu, lane < w.n_seqs && c / w.tile + lane <= slot);
+  const int s = before ? 31 - __clz(before) : 0;
+  const int32_t start = __shfl_sync(0xffffffffu, c, s), next = __shfl_sync(0xffffffffu, c, s + 1);
+  const int64_t t0 = (int64_t)(slot - (start / w.tile + s)) * w.tile;
+  if (lane == 0) {
+    own->tile = Tile{start, next - start, (int32_t)t0, 0};
+    own->has = !bad && before && t0 < next - start;
+    own->end = bad ? 0 : end;
+  }
+}
+
+// The same for kernels of both kinds.
+template <bool kOwn>
+__device__ __forceinline__ int4 tile_of(const Work& w, const Own& own, int64_t i) {
+  return kOwn ? *reinterpret_cast<const int4*>(&own.tile) : __ldg(reinterpret_cast<const int4*>(w.list) + i);
+}
+// Work units, of `per` a tile: unit blockIdx.x is this CTA's first (own: and only) one.
+template <bool kOwn>
+__device__ __forceinline__ int64_t units_of(const Work& w, const Own& own, int per) {
+  return kOwn ? (own.has ? gridDim.x : 0) : (int64_t)w.hdr->n_tiles[w.which] * per;
+}
+template <bool kOwn>
+__device__ __forceinline__ int64_t end_of(const Work& w, const Own& own) { return kOwn ? own.end : w.hdr->end; }
+
 cudaError_t launch_plan(const int32_t* cu, int n_seqs, int64_t total, int n_lists, const ListSpec* lists, Header* hdr,
                         int* status, bool clear_status, cudaStream_t st);
 

@@ -33,8 +33,7 @@ struct BwdParams {
   __nv_bfloat16* dq;
   __nv_bfloat16* dk;
   __nv_bfloat16* dv;
-  const Header* hdr;
-  const Tile* list;
+  Work work;
   int fill_tail;
   int* status;
   uint64_t wait_ns;
@@ -58,18 +57,20 @@ struct Smem {
   // mma_done, qdo_empty, delta_bar, qdo_issued, k_clean[KS]
   static constexpr int kNumBars = 1 + 2 * KS + VS + 11 + KS;
   static constexpr uint32_t kMisc = kBar + 8 * kNumBars;
-  static constexpr uint32_t kBytes = kMisc + 16;
+  static constexpr uint32_t kOwn = (kMisc + 16 + 15) & ~15u;
+  static constexpr uint32_t kBytes = kOwn + sizeof(Own);
 };
 static_assert(Smem::kBytes + 1024 <= 227 * 1024, "shared memory");
 
 struct Unit {
   int start, len, t0, h0, kh, T;
 };
-__device__ __forceinline__ bool load_unit(const BwdParams& p, int64_t n_units, int k, Unit* x) {
+template <bool kOwn>
+__device__ __forceinline__ bool load_unit(const BwdParams& p, const Own& own, int64_t n_units, int k, Unit* x) {
   const int64_t u = unit_of_cta(k, blockIdx.x, gridDim.x);
   if (u >= n_units) return false;
   const int per = p.G / p.pk, hus = p.Hkv * per;
-  const int4 w = __ldg(reinterpret_cast<const int4*>(p.list) + u / hus);
+  const int4 w = tile_of<kOwn>(p.work, own, u / hus);
   const int hu = (int)(u % hus);
   x->start = w.x;
   x->len = w.y;
@@ -87,6 +88,7 @@ __device__ __forceinline__ bool load_unit(const BwdParams& p, int64_t n_units, i
 // Q/dO are loaded as soon as the last S and dP products of the current unit have read them.
 // Warps: 0 K, 3 V, 2 Q/dO and the cleaning of the unit's last K tile, 1 products, 4..19 element-wise (thread =
 // row, four warpgroups of 32 key columns).
+template <bool kOwn>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_dq_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                         const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -142,13 +144,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
+  const int per_tile = p.Hkv * (p.G / p.pk);
+  Own& own = *reinterpret_cast<Own*>(smem + L::kOwn);
+  if (kOwn && warp == 2) {
+    pdl_wait();
+    own_tile(p.work, blockIdx.x / per_tile, &own);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   if (threadIdx.x == 0) pdl_trigger();
   pdl_wait();                               // the work list comes from the kernel before
-  const int64_t n_units = (int64_t)p.hdr->n_tiles[0] * p.Hkv * (p.G / p.pk);
+  const int64_t n_units = units_of<kOwn>(p.work, own, per_tile);
   Unit x;
 
   if (warp == 0 || warp == 3) {
@@ -159,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       const CUtensorMap* map = is_v ? &tm_v : &tm_k;
       int64_t J = 0;
       bool ok = true;
-      for (int k = 0; ok && load_unit(p, n_units, k, &x); ++k) {
+      for (int k = 0; ok && load_unit<kOwn>(p, own, n_units, k, &x); ++k) {
         if (!(ok = mbar_wait(qdo_issued, k & 1, abort_flag, p.status, p.wait_ns))) break;
         for (int j = 0; j < x.T; ++j, ++J) {
           const int ks = (int)(J % KS), vs = (int)(J % VS);
@@ -183,7 +191,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int loads = 0;
     int64_t J = 0;
     bool ok = true;
-    for (int k = 0; ok && load_unit(p, n_units, k, &x); ++k) {
+    for (int k = 0; ok && load_unit<kOwn>(p, own, n_units, k, &x); ++k) {
       if (k > 0) ok = wait_w(qdo_empty, (k - 1) & 1, abort_flag, p.status, p.wait_ns);
       if (!ok) break;
       if (lane == 0) {
@@ -246,7 +254,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     bool ok = true;
     int64_t J = 0;
     uint32_t clean_phase = 0;               // bit s: parity of the next cleaned tile in K stage s
-    bool have = load_unit(p, n_units, 0, &x);
+    bool have = load_unit<kOwn>(p, own, n_units, 0, &x);
     if (have) {
       ok = wait_w(qdo_full, 0, abort_flag, p.status, p.wait_ns) &&
            wait_w(kv_full(0), 0, abort_flag, p.status, p.wait_ns);
@@ -258,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     for (int k = 0; ok && have; ++k) {
       Unit xn = x;
-      const bool has_next = load_unit(p, n_units, k + 1, &xn);
+      const bool has_next = load_unit<kOwn>(p, own, n_units, k + 1, &xn);
       for (int j = 0; j < x.T; ++j, ++J) {
         const bool last = j + 1 == x.T;
         const bool next = !last || has_next;
@@ -309,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else {
     // ======================= element-wise: dS = P o (dP - delta), P = exp2(S c2 - lse log2 e)
     if (p.fill_tail)
-      fill_tail_rows(p.dq, p.Hq, p.hdr->end, p.total, (int64_t)blockIdx.x * 512 + (threadIdx.x - 128),
+      fill_tail_rows(p.dq, p.Hq, end_of<kOwn>(p.work, own), p.total, (int64_t)blockIdx.x * 512 + (threadIdx.x - 128),
                      (int64_t)gridDim.x * 512);
     const int w = (warp - 4) >> 2;
     const int quarter = warp & 3;
@@ -319,7 +327,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool v8 = (reinterpret_cast<uintptr_t>(p.dq) & 31u) == 0;
     bool ok = true;
     int64_t J = 0;
-    for (int k = 0; ok && load_unit(p, n_units, k, &x); ++k) {
+    for (int k = 0; ok && load_unit<kOwn>(p, own, n_units, k, &x); ++k) {
       const int head = x.h0 + r % p.pk;
       const int t_pos = x.t0 + r / p.pk;
       const bool in = t_pos < x.len;
@@ -478,7 +486,8 @@ struct Smem {
   // kv_full, q_full[NS], q_empty[NS], q_clean[NS], sd_full[2], pd_full[2], done, mma_done, stat_full[NS]
   static constexpr int kNumBars = 1 + 4 * NS + 4 + 2;
   static constexpr uint32_t kMisc = kBar + 8 * kNumBars;
-  static constexpr uint32_t kBytes = kMisc + 16;
+  static constexpr uint32_t kOwn = (kMisc + 16 + 15) & ~15u;
+  static constexpr uint32_t kBytes = kOwn + sizeof(Own);
 };
 static_assert(Smem::kBytes + 1024 <= 227 * 1024, "shared memory");
 
@@ -489,6 +498,7 @@ static_assert(Smem::kBytes + 1024 <= 227 * 1024, "shared memory");
 // parity and the 64 query columns in two).
 // With cs = 2 a cluster of two CTAs takes the steps of a unit in turn; each then has half of the key rows to store, and
 // adds what the other, through its shared memory, has summed for them (two terms: the order does not matter).
+template <bool kOwn>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_dkdv_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_do,
                           const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
@@ -511,14 +521,20 @@ __global__ void __launch_bounds__(kThreads, 1)
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
   pdl_wait();                               // the work list, lse and delta come from the kernels before
+  const int rank = (int)(blockIdx.x % cs), unit = (int)(blockIdx.x / cs);
+  Own& own = *reinterpret_cast<Own*>(smem + L::kOwn);
+  if (kOwn) {
+    if (warp == 2) own_tile(p.work, unit / p.Hkv, &own);
+    __syncthreads();
+  }
   if (p.fill_tail) {
     const int64_t worker = (int64_t)blockIdx.x * kThreads + threadIdx.x, workers = (int64_t)gridDim.x * kThreads;
-    fill_tail_rows(p.dk, p.Hkv, p.hdr->end, p.total, worker, workers);
-    fill_tail_rows(p.dv, p.Hkv, p.hdr->end, p.total, worker, workers);
+    const int64_t end = end_of<kOwn>(p.work, own);
+    fill_tail_rows(p.dk, p.Hkv, end, p.total, worker, workers);
+    fill_tail_rows(p.dv, p.Hkv, end, p.total, worker, workers);
   }
-  const int rank = (int)(blockIdx.x % cs), unit = (int)(blockIdx.x / cs);
-  if (unit / p.Hkv >= p.hdr->n_tiles[1]) return;        // (the whole cluster)
-  const int4 wk = __ldg(reinterpret_cast<const int4*>(p.list) + unit / p.Hkv);
+  if (unit >= units_of<kOwn>(p.work, own, p.Hkv)) return;     // (the whole cluster)
+  const int4 wk = tile_of<kOwn>(p.work, own, unit / p.Hkv);
   const int start = wk.x, len = wk.y, t0 = wk.z;
   const int kh = unit % p.Hkv;
   const int tq = BQ / p.pk;                 // tokens per step
@@ -823,8 +839,8 @@ __global__ void __launch_bounds__(kThreads, 1)
 int dq_tile(int G) { return 128 / packed_heads(G); }
 
 cudaError_t launch_bwd_tc(const void* q, const void* k, const void* v, const void* o, const void* o_lo,
-                          const float* lse, const void* d_o, float* stats, void* dq, void* dk, void* dv, const Header* hdr, const Tile* by_query,
-                          const Tile* by_key, const Problem& p, cudaStream_t st) {
+                          const float* lse, const void* d_o, float* stats, void* dq, void* dk, void* dv,
+                          const Work& by_query, const Work& by_key, const Problem& p, cudaStream_t st) {
   const int pk = packed_heads(p.G);
   const Strided so{(int64_t)p.Hq * kD, kD};
   CUtensorMap mq, mdo, mk, mv, mq64, mdo64;
@@ -836,28 +852,30 @@ cudaError_t launch_bwd_tc(const void* q, const void* k, const void* v, const voi
     return cudaErrorInvalidValue;
   BwdParams a{p.Hq, p.Hkv, p.G, pk, p.total, p.scale * kLog2eF, p.scale, static_cast<const __nv_bfloat16*>(o),
               static_cast<const __nv_bfloat16*>(o_lo), lse, stats,
-              static_cast<__nv_bfloat16*>(dq), static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv), hdr,
+              static_cast<__nv_bfloat16*>(dq), static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv),
               by_query, p.fill_tail, p.status, p.wait_ns};
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   size_t smem = dq::Smem::kBytes + 1024;
-  e = cudaFuncSetAttribute(dq::packed_dq_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  auto dq_kernel = by_query.cu ? dq::packed_dq_tc_kernel<true> : dq::packed_dq_tc_kernel<false>;
+  e = cudaFuncSetAttribute(dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int64_t units = list_capacity(p.total, p.n_seqs, dq_tile(p.G)) * p.Hkv * (p.G / pk);
-  e = launch_dependent(dq::packed_dq_tc_kernel, dim3((unsigned)(units < 1 ? 1 : units < sms ? units : sms)),
+  e = launch_dependent(dq_kernel, dim3((unsigned)(units < 1 ? 1 : units < sms ? units : sms)),
                        dim3(dq::kThreads), smem, st, 1, mq, mdo, mk, mv, a);
   if (e != cudaSuccess) return e;
-  a.list = by_key;
+  a.work = by_key;
   smem = dkdv::Smem::kBytes + 1024;
-  e = cudaFuncSetAttribute(dkdv::packed_dkdv_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  auto dkdv_kernel = by_key.cu ? dkdv::packed_dkdv_tc_kernel<true> : dkdv::packed_dkdv_tc_kernel<false>;
+  e = cudaFuncSetAttribute(dkdv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = list_capacity(p.total, p.n_seqs, kKeyTile) * p.Hkv;
   // Two CTAs per unit while there are fewer units than SMs.  Whole backward pass, 32/8 heads: 1024 tokens (64 units) 103 us
   // with one, 73 with two; 2048 (128) 240 and 170; 4096 (256) 456 and 474; 8/8 heads, 4096 (256) 128 and 156.
   const int cs = tiles < sms ? 2 : 1;
-  return launch_dependent(dkdv::packed_dkdv_tc_kernel, dim3((unsigned)((tiles < 1 ? 1 : tiles) * cs)), dim3(dkdv::kThreads),
+  return launch_dependent(dkdv_kernel, dim3((unsigned)((tiles < 1 ? 1 : tiles) * cs)), dim3(dkdv::kThreads),
                           smem, st, (unsigned)cs, mq64, mdo64, mk, mv, a, cs);
 }
 

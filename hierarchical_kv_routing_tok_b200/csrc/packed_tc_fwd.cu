@@ -42,8 +42,7 @@ struct FwdParams {
   __nv_bfloat16* o;
   __nv_bfloat16* o_lo;                     // what rounding took from o, or nullptr
   float* lse;
-  const Header* hdr;
-  const Tile* list;
+  Work work;
   int fill_tail;
   int* status;
   uint64_t wait_ns;
@@ -59,7 +58,8 @@ struct FwdSmem {
   static constexpr int kNumBars = 2 + 3 * NS + 6 + 1;
   static constexpr uint32_t kMisc = kBar + 8 * kNumBars;        // TMEM address, abort, flags of 4 units
   static constexpr uint32_t kNeed = kMisc + 32;                 // [tile parity][pair of warps][half]
-  static constexpr uint32_t kBytes = kNeed + 2 * 8 * 2 * 4;
+  static constexpr uint32_t kOwn = (kNeed + 2 * 8 * 2 * 4 + 15) & ~15u;
+  static constexpr uint32_t kBytes = kOwn + sizeof(Own);
 };
 static_assert(FwdSmem::kBytes + 1024 <= 227 * 1024, "shared memory");
 
@@ -68,10 +68,11 @@ struct Unit {
   int T[2], Tmax;                          // key tiles of the two query tiles
 };
 
-__device__ __forceinline__ bool load_unit(const FwdParams& p, int64_t n_units, int k, Unit* x) {
+template <bool kOwn>
+__device__ __forceinline__ bool load_unit(const FwdParams& p, const Own& own, int64_t n_units, int k, Unit* x) {
   const int64_t u = unit_of_cta(k, blockIdx.x, gridDim.x);
   if (u >= n_units) return false;
-  const int4 w = __ldg(reinterpret_cast<const int4*>(p.list) + u / p.hu);
+  const int4 w = tile_of<kOwn>(p.work, own, u / p.hu);
   const int hu = (int)(u % p.hu), per = p.G / p.pk;
   x->start = w.x;
   x->len = w.y;
@@ -155,6 +156,7 @@ __device__ __noinline__ void write_output(const FwdParams& p, const OutArgs w) {
   }
 }
 
+template <bool kOwn>
 __global__ void __launch_bounds__(kThreads, 1)
     packed_fwd_tc_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                          const __grid_constant__ CUtensorMap tm_v, const FwdParams p) {
@@ -199,13 +201,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     tmem_alloc(smem_u32(tmem_slot), 512);
     tmem_relinquish();
   }
+  Own& own = *reinterpret_cast<Own*>(smem + L::kOwn);
+  if (kOwn && warp == 16) {
+    pdl_wait();
+    own_tile(p.work, blockIdx.x / p.hu, &own);
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = *tmem_slot;
   if (threadIdx.x == 0) pdl_trigger();
   pdl_wait();                              // the work list comes from the kernel before
-  const int64_t n_units = (int64_t)p.hdr->n_tiles[0] * p.hu;
+  const int64_t n_units = units_of<kOwn>(p.work, own, p.hu);
   Unit x;
 
   if (warp == 16) {
@@ -214,7 +221,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       int64_t J = 0;
       bool ok = true;
       int loads = 0;
-      for (int k = 0; ok && load_unit(p, n_units, k, &x); ++k) {
+      for (int k = 0; ok && load_unit<kOwn>(p, own, n_units, k, &x); ++k) {
         if (k > 0 && !(ok = mbar_wait(q_empty, (k - 1) & 1, abort_flag, p.status, p.wait_ns))) break;
         mbar_arrive_expect_tx(q_full, 2 * kTileBytes);
         for (int i = 0; i < 2; ++i)
@@ -245,7 +252,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // ======================= check of the V tiles at or behind the unit's first token
     int64_t J = 0;
     bool ok = true;
-    for (int k = 0; ok && load_unit(p, n_units, k, &x); ++k) {
+    for (int k = 0; ok && load_unit<kOwn>(p, own, n_units, k, &x); ++k) {
       const int jd = x.t0 / kBN;
       bool any = false;
       for (int j = -1; j < x.Tmax; ++j, ++J) {          // (every item is waited for: a parity names only the current
@@ -277,7 +284,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     int np[2] = {0, 0};                    // P tiles taken of each query tile
     uint32_t clean_phase = 0;              // bit s: parity of the next checked item in slot s
     bool ok = true;
-    for (int k = 0; ok && load_unit(p, n_units, k, &x); ++k) {
+    for (int k = 0; ok && load_unit<kOwn>(p, own, n_units, k, &x); ++k) {
       ok = wait_w(q_full, k & 1, abort_flag, p.status, p.wait_ns);
       const int jd = x.t0 / kBN;
       for (int j = -1; ok && j < x.Tmax; ++j, ++J) {
@@ -326,9 +333,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     const int st = threadIdx.x;
     if (p.fill_tail) {
       const int64_t worker = (int64_t)blockIdx.x * kSoftmax + st, workers = (int64_t)gridDim.x * kSoftmax;
-      fill_tail_rows(p.o, p.Hq, p.hdr->end, p.total, worker, workers);
-      if (p.o_lo) fill_tail_rows(p.o_lo, p.Hq, p.hdr->end, p.total, worker, workers);
-      fill_tail_lse(p.lse, p.Hq, p.hdr->end, p.total, worker, workers);
+      const int64_t end = end_of<kOwn>(p.work, own);
+      fill_tail_rows(p.o, p.Hq, end, p.total, worker, workers);
+      if (p.o_lo) fill_tail_rows(p.o_lo, p.Hq, end, p.total, worker, workers);
+      fill_tail_lse(p.lse, p.Hq, end, p.total, worker, workers);
     }
     const int i = st >> 8, half = (st >> 7) & 1;
     const int quarter = warp & 3, pair_id = 4 * i + quarter;
@@ -348,7 +356,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     auto pair_sync = [&] { asm volatile("bar.sync %0, 64;" ::"r"(1 + pair_id) : "memory"); };
     int ns = 0, no = 0;                                 // S tiles, outputs taken
     bool ok = true;
-    for (int k = 0; ok && load_unit(p, n_units, k, &x); ++k) {
+    for (int k = 0; ok && load_unit<kOwn>(p, own, n_units, k, &x); ++k) {
       const int T = x.T[i];
       if (T == 0) continue;
       const int t_pos = x.t0 + i * p.tp + (r >> p.pk_shift);    // (rows past the sequence compute, and store nothing)
@@ -497,26 +505,28 @@ bool make_map_packed(CUtensorMap* m, const void* base, int H, int64_t total, Str
 }
 
 int fwd_tile(int G) { return 256 / packed_heads(G); }
+int head_units(int Hkv, int G) { return Hkv * (G / packed_heads(G)); }
 
 cudaError_t launch_fwd_tc(const void* q, const void* k, const void* v, void* o, void* o_lo, float* lse,
-                          const Header* hdr, const Tile* list, const Problem& p, cudaStream_t st) {
+                          const Work& work, const Problem& p, cudaStream_t st) {
   const int pk = packed_heads(p.G);
   CUtensorMap mq, mk, mv;
   if (!make_map_packed(&mq, q, p.Hq, p.total, p.q, pk, 128 / pk) || !make_map_packed(&mk, k, p.Hkv, p.total, p.k, 1, kBN) ||
       !make_map_packed(&mv, v, p.Hkv, p.total, p.v, 1, kBN))
     return cudaErrorInvalidValue;
   FwdParams a{p.Hq, p.Hkv, p.G, pk, pk == 8 ? 3 : pk == 4 ? 2 : pk - 1, 128 / pk, p.Hkv * (p.G / pk), p.total, p.scale * kLog2eF,
-              static_cast<const __nv_bfloat16*>(v), p.v, static_cast<__nv_bfloat16*>(o), static_cast<__nv_bfloat16*>(o_lo), lse, hdr, list, p.fill_tail,
+              static_cast<const __nv_bfloat16*>(v), p.v, static_cast<__nv_bfloat16*>(o), static_cast<__nv_bfloat16*>(o_lo), lse, work, p.fill_tail,
               p.status, p.wait_ns};
   int dev = 0, sms = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
   const size_t smem = FwdSmem::kBytes + 1024;
-  e = cudaFuncSetAttribute(packed_fwd_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  auto kernel = work.cu ? packed_fwd_tc_kernel<true> : packed_fwd_tc_kernel<false>;
+  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int64_t units = list_capacity(p.total, p.n_seqs, fwd_tile(p.G)) * a.hu;
-  return launch_dependent(packed_fwd_tc_kernel, dim3((unsigned)(units < 1 ? 1 : units < sms ? units : sms)),
+  return launch_dependent(kernel, dim3((unsigned)(units < 1 ? 1 : units < sms ? units : sms)),
                           dim3(kThreads), smem, st, 1, mq, mk, mv, a);
 }
 

@@ -333,6 +333,33 @@ def test_autograd_in_a_graph(hga, dtype):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n_seqs,tail", [(1, 0), (30, 3), (31, 0), (31, 70), (32, 0), (32, 9), (33, 5)])
+def test_number_of_sequences(hga, dtype, n_seqs, tail):
+    """Few tiles of up to 31 sequences are found by the kernels themselves, others by a list: one result."""
+    lens = [(37 * i * i + 11 * i) % 23 if i % 3 else 0 for i in range(n_seqs - 1)] + [130]
+    q, k, v, d_o = make(lens, 2, 1, dtype, tail=tail)
+    check_all(run(hga, q, k, v, d_o, ends(lens)), R.packed(q, k, v, lens, d_o=d_o))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n_seqs", [3, 40])
+def test_bad_bounds_fill_everything(hga, dtype, n_seqs):
+    lens = [9] * n_seqs
+    q, k, v, d_o = make(lens, 2, 1, dtype)
+    for bad in (lambda c: c[0].fill_(1), lambda c: c[2].fill_(5), lambda c: c[-1].fill_(q.shape[0] + 1),
+                lambda c: c.fill_(-1)):
+        cu = ends(lens)
+        bad(cu)
+        o, lse = hga.packed_attention(q, k, v, cu)
+        assert not o.any() and (lse == -float("inf")).all()
+        cfg = hga.make_packed_config(q, k, v, cu)
+        ws = torch.zeros(hga._capi.packed_workspace_size(cfg), dtype=torch.uint8, device="cuda")
+        dq, dk, dv = hga.packed_attn_bwd(cfg, q, k, v, cu, o, lse, d_o, workspace=ws)
+        assert not dq.any() and not dk.any() and not dv.any()
+        assert hga.read_status(ws) == hga._capi.HGA_ERR_ARG
+
+
 def test_two_at_once(hga):
     """Two problems on two streams, each with its own workspace, over and over."""
     probs = []
