@@ -393,7 +393,7 @@ HGA_API int hga_route_groups_cached(const hga_config_t* cfg, const float* qb, co
  * not decreasing, at most total; if it is not, no sequence is computed (all rows count as rows of
  * no sequence) and HGA_ERR_ARG is recorded in the workspace status word.
  * Products accumulate in float32.  bf16: probabilities and dS are rounded to bf16 before their second
- * product.  float32: each operand as the sum of two tf32 numbers, which keeps float32 accuracy (the
+ * product (of dS in dQ, what that takes is added back where it counts most).  float32: each operand as the sum of two tf32 numbers, which keeps float32 accuracy (the
  * scores of a q or k row that is not finite are NaN).
  * total <= 2^31 - 1 - 256 and (total / 16 + n_seqs) * Hq < 2^31; total = 0 or n_seqs = 0 is a valid
  * empty problem.
