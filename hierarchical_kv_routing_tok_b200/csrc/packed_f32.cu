@@ -651,7 +651,10 @@ cudaError_t launch_fwd_f32(const void* q, const void* k, const void* v, void* o,
                            const Problem& p, cudaStream_t st) {
   const int tile = f32_tile(p.total, p.n_seqs, p.Hq);
   const int64_t n = list_capacity(p.total, p.n_seqs, tile) * p.Hq;
-  return launch(tile == 64 ? packed_fwd_f32_kernel<4, false> : work.cu ? packed_fwd_f32_kernel<2, true> : packed_fwd_f32_kernel<2, false>, n < 1 ? 1 : n, 5 * kTileBytesF, 1, st,
+  auto kernel = tile == 64 ? packed_fwd_f32_kernel<4, false>
+                : work.cu  ? packed_fwd_f32_kernel<2, true>
+                           : packed_fwd_f32_kernel<2, false>;
+  return launch(kernel, n < 1 ? 1 : n, 5 * kTileBytesF, 1, st,
                 (const float*)q, (const float*)k, (const float*)v, (float*)o, lse, work, p);
 }
 
@@ -662,7 +665,13 @@ cudaError_t launch_bwd_f32(const void* q, const void* k, const void* v, const vo
   const int tile = f32_tile(p.total, p.n_seqs, p.Hq);
   const int64_t tiles = list_capacity(p.total, p.n_seqs, tile);
   const int64_t nq = tiles * p.Hq, nk = tiles * p.Hkv;
-  cudaError_t e = launch(tile == 64 ? packed_dq_f32_kernel<4, false> : by_query.cu ? packed_dq_f32_kernel<2, true> : packed_dq_f32_kernel<2, false>, nq < 1 ? 1 : nq, 6 * kTileBytesF,
+  auto dq_kernel = tile == 64    ? packed_dq_f32_kernel<4, false>
+                   : by_query.cu ? packed_dq_f32_kernel<2, true>
+                                 : packed_dq_f32_kernel<2, false>;
+  auto dkdv_kernel = tile == 64  ? packed_dkdv_f32_kernel<4, false>
+                     : by_key.cu ? packed_dkdv_f32_kernel<2, true>
+                                 : packed_dkdv_f32_kernel<2, false>;
+  cudaError_t e = launch(dq_kernel, nq < 1 ? 1 : nq, 6 * kTileBytesF,
                          1, st, (const float*)q, (const float*)k, (const float*)v, (const float*)o, lse,
                          (const float*)d_o, delta, (float*)dq, by_query, p);
   if (e != cudaSuccess) return e;
@@ -674,7 +683,7 @@ cudaError_t launch_bwd_f32(const void* q, const void* k, const void* v, const vo
   if (nk < sms)
     for (int c = 2; c <= 8; ++c)
       if (p.G % c == 0) cs = c;
-  return launch(tile == 64 ? packed_dkdv_f32_kernel<4, false> : by_key.cu ? packed_dkdv_f32_kernel<2, true> : packed_dkdv_f32_kernel<2, false>, (nk < 1 ? 1 : nk) * cs,
+  return launch(dkdv_kernel, (nk < 1 ? 1 : nk) * cs,
                 6 * kTileBytesF, (unsigned)cs, st, (const float*)q, (const float*)k, (const float*)v, lse,
                 (const float*)d_o, (const float*)delta, (float*)dk, (float*)dv, by_key, p, cs);
 }
