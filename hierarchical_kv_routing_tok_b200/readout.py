@@ -9,8 +9,6 @@ needs no host synchronisation and can be captured into a CUDA graph.  Every comp
 """
 from __future__ import annotations
 
-import contextlib
-
 import torch
 
 from . import _capi as C
@@ -25,12 +23,18 @@ _D = 128
 _raw_stream = torch._C._cuda_getCurrentRawStream
 
 
-def _on(dev: int):
-    """Launches go to the current stream of the tensors' device, which must be the current device."""
-    return _NO_CONTEXT if torch._C._cuda_getDevice() == dev else torch.cuda.device(dev)
+def _launch(fn, dev: int, *args) -> None:
+    """fn(*args, stream) on the current stream of device dev, which must be the current device meanwhile."""
+    if torch._C._cuda_getDevice() == dev:
+        fn(*args, _raw_stream(dev))
+    else:
+        with torch.cuda.device(dev):
+            fn(*args, _raw_stream(dev))
 
 
-_NO_CONTEXT = contextlib.nullcontext()
+def _like(t: torch.Tensor, shape) -> torch.Tensor:
+    """A new contiguous tensor of t's type and device (of t's own shape: by the cheaper call)."""
+    return torch.empty_like(t) if t.is_contiguous() and t.shape == shape else t.new_empty(shape)
 
 
 def _flat(t: torch.Tensor, name: str, shape, dtype, dev: int) -> None:
@@ -123,7 +127,7 @@ def packed_attn_fwd(cfg, q, k, v, cu_seqlens, o=None, lse=None, workspace=None, 
     T, Hq, dev, flags = cfg.total, cfg.Hq, q.get_device(), cfg.flags
     if o is None and lse is None:
         flags |= C.HGA_PACKED_FILL_TAIL
-        o = q.new_empty((T, Hq, _D))
+        o = _like(q, (T, Hq, _D))
         lse = q.new_empty((Hq, T), dtype=torch.float32)
     elif o is None or lse is None:
         raise ValueError("o and lse are given together or not at all")
@@ -133,10 +137,9 @@ def packed_attn_fwd(cfg, q, k, v, cu_seqlens, o=None, lse=None, workspace=None, 
     if o_lo is not None:
         _flat(o_lo, "o_lo", (T, Hq, _D), q.dtype, dev)
     workspace, flags = _workspace(cfg, workspace, q, flags)
-    with _on(dev):
-        C.packed_attn_fwd(_with_flags(cfg, flags), q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(),
-                          o.data_ptr(), None if o_lo is None else o_lo.data_ptr(), lse.data_ptr(),
-                          workspace.data_ptr(), _raw_stream(dev))
+    _launch(C.packed_attn_fwd, dev, _with_flags(cfg, flags), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            cu_seqlens.data_ptr(), o.data_ptr(), None if o_lo is None else o_lo.data_ptr(), lse.data_ptr(),
+            workspace.data_ptr())
     return o, lse
 
 
@@ -146,9 +149,9 @@ def packed_attn_bwd(cfg, q, k, v, cu_seqlens, o, lse, d_o, dq=None, dk=None, dv=
     T, Hq, Hkv, dev, flags = cfg.total, cfg.Hq, cfg.Hkv, q.get_device(), cfg.flags
     if dq is None and dk is None and dv is None:
         flags |= C.HGA_PACKED_FILL_TAIL
-        dq = q.new_empty((T, Hq, _D))
-        dk = q.new_empty((T, Hkv, _D))
-        dv = q.new_empty((T, Hkv, _D))
+        dq = _like(q, (T, Hq, _D))
+        dk = _like(k, (T, Hkv, _D))
+        dv = _like(v, (T, Hkv, _D))
     elif dq is None or dk is None or dv is None:
         raise ValueError("dq, dk and dv are given together or not at all")
     else:
@@ -160,10 +163,9 @@ def packed_attn_bwd(cfg, q, k, v, cu_seqlens, o, lse, d_o, dq=None, dk=None, dv=
     if o_lo is not None:
         _flat(o_lo, "o_lo", (T, Hq, _D), q.dtype, dev)
     workspace, flags = _workspace(cfg, workspace, q, flags)
-    with _on(dev):
-        C.packed_attn_bwd(_with_flags(cfg, flags), q.data_ptr(), k.data_ptr(), v.data_ptr(), cu_seqlens.data_ptr(),
-                          o.data_ptr(), None if o_lo is None else o_lo.data_ptr(), lse.data_ptr(), d_o.data_ptr(),
-                          dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr(), _raw_stream(dev))
+    _launch(C.packed_attn_bwd, dev, _with_flags(cfg, flags), q.data_ptr(), k.data_ptr(), v.data_ptr(),
+            cu_seqlens.data_ptr(), o.data_ptr(), None if o_lo is None else o_lo.data_ptr(), lse.data_ptr(),
+            d_o.data_ptr(), dq.data_ptr(), dk.data_ptr(), dv.data_ptr(), workspace.data_ptr())
     return dq, dk, dv
 
 
@@ -174,7 +176,7 @@ class _PackedAttention(torch.autograd.Function):
     @staticmethod
     def forward(ctx, q, k, v, cu_seqlens, softmax_scale):
         cfg = make_packed_config(q, k, v, cu_seqlens, softmax_scale, _NEW)
-        o_lo = q.new_empty((cfg.total, cfg.Hq, _D)) if cfg.dtype == C.HGA_BF16 else None
+        o_lo = _like(q, (cfg.total, cfg.Hq, _D)) if cfg.dtype == C.HGA_BF16 else None
         o, lse = packed_attn_fwd(cfg, q, k, v, cu_seqlens, o_lo=o_lo)
         ctx.cfg = cfg
         ctx.save_for_backward(q, k, v, cu_seqlens, o, lse, o_lo)
@@ -296,8 +298,7 @@ class PagedKVCache:
         return layer
 
     def _call(self, fn, *args) -> None:
-        with _on(self._dev):
-            fn(self.cfg, *args, self._ws, _raw_stream(self._dev))
+        _launch(fn, self._dev, self.cfg, *args, self._ws)
 
     def reserve(self, rows, add) -> torch.Tensor:
         """Room for add[i] tokens behind sequence row rows[i] (int32 [n]): takes the pages, grows seq_len.
@@ -332,7 +333,7 @@ class PagedKVCache:
         if sh != _D or sn < Hq * _D:
             raise ValueError(f"q: the heads of a token must be contiguous, got strides {tuple(q.stride())}")
         if o is None:
-            o = q.new_empty((n, Hq, _D))
+            o = _like(q, (n, Hq, _D))
         else:
             _flat(o, "o", (n, Hq, _D), self.dtype, self._dev)
         if lse is None:
@@ -370,5 +371,5 @@ class PagedKVCache:
     def status(self) -> int:
         """Status of the calls since the last one (synchronises): HGA_OK, HGA_ERR_ARG, HGA_ERR_PAGES or
         HGA_ERR_TIMEOUT."""
-        with _on(self._dev):
+        with torch.cuda.device(self._dev):
             return read_status(self.workspace)
