@@ -369,7 +369,7 @@ class PagedKVCache:
         self._call(C.pages_copy, n, src.data_ptr(), dst.data_ptr(), *self._pools)
 
     def status(self) -> int:
-        """Status of the calls since the last one (synchronises): HGA_OK, HGA_ERR_ARG, HGA_ERR_PAGES or
-        HGA_ERR_TIMEOUT."""
+        """Status of the calls since the last one, of those on the current stream and before it (synchronises that
+        stream): HGA_OK, HGA_ERR_ARG, HGA_ERR_PAGES or HGA_ERR_TIMEOUT."""
         with torch.cuda.device(self._dev):
             return read_status(self.workspace)

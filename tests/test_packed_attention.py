@@ -360,6 +360,49 @@ def test_bad_bounds_fill_everything(hga, dtype, n_seqs):
         assert hga.read_status(ws) == hga._capi.HGA_ERR_ARG
 
 
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("which", ["q", "k", "v", "qv"])
+def test_gradients_of_some_inputs(hga, dtype, which):
+    lens = [70, 5, 200]
+    q, k, v, d_o = make(lens, 4, 2, dtype)
+    cu = ends(lens)
+    want = run(hga, q, k, v, d_o, cu)
+    x = {"q": q.clone(), "k": k.clone(), "v": v.clone()}
+    for n in which:
+        x[n].requires_grad_()
+    o, lse = hga.packed_attention(x["q"], x["k"], x["v"], cu)
+    assert not lse.requires_grad
+    o.backward(d_o)
+    for n in "qkv":
+        if n in which:
+            assert torch.equal(x[n].grad, want["d" + n])
+        else:
+            assert x[n].grad is None
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_shared_workspace_in_two_graphs(hga, dtype):
+    """Two captured problems over one workspace, replayed in turn, one of each kind of work list."""
+    probs, graphs, outs = [], [], []
+    for seed, lens in ((0, [33, 20]), (1, [5] * 40 + [300])):
+        q, k, v, _ = make(lens, 8, 2, dtype, seed=seed)
+        probs.append((q, k, v, ends(lens)))
+    cfgs = [hga.make_packed_config(*p) for p in probs]
+    ws = torch.zeros(max(hga._capi.packed_workspace_size(c) for c in cfgs), dtype=torch.uint8, device="cuda")
+    want = [hga.packed_attention(*p) for p in probs]
+    torch.cuda.synchronize()
+    for c, p in zip(cfgs, probs):
+        outs.append((torch.full_like(p[0], 7), torch.full((8, p[0].shape[0]), 7.0, device="cuda")))
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            hga.packed_attn_fwd(c, *p, *outs[-1], workspace=ws)
+    for i in (0, 1, 1, 0, 0, 1):
+        outs[i][0].fill_(7)
+        graphs[i].replay()
+        assert torch.equal(outs[i][0], want[i][0]) and torch.equal(outs[i][1], want[i][1])
+    assert hga.read_status(ws) == 0
+
+
 def test_two_at_once(hga):
     """Two problems on two streams, each with its own workspace, over and over."""
     probs = []
