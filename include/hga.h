@@ -416,8 +416,9 @@ typedef struct hga_packed_config {
 HGA_API int hga_packed_workspace_size(const hga_packed_config_t* cfg, size_t* bytes_out);
 
 /* o_lo (may be NULL): for a backward pass in bf16, what rounding took from o, as bf16 [total, Hq, D]: the
- * backward forms rowsum(d_o * o) from o + o_lo.  Without it dq and dk of short sequences are about twice
- * as far from the exact gradients (5 + 3 tokens: 4.0e-3 against 2.6e-3 of the norm; 4096: 2.52 against 2.40).
+ * backward forms rowsum(d_o * o) from o + o_lo.  Without it dq and dk of short sequences are further
+ * from the exact gradients (5 and 3 tokens: dq 3.3e-3 of the norm against 1.8e-3, dk 3.6e-3 against 2.4e-3;
+ * 4096 tokens: dq 2.16e-3 against 2.09e-3).
  * float32 does not use it. */
 HGA_API int hga_packed_attn_fwd(const hga_packed_config_t* cfg, const void* q, const void* k, const void* v,
                                 const int32_t* cu_seqlens, void* o, void* o_lo, float* lse, void* workspace,
