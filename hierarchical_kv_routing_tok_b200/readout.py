@@ -37,6 +37,12 @@ def _like(t: torch.Tensor, shape) -> torch.Tensor:
     return torch.empty_like(t) if t.is_contiguous() and t.shape == shape else t.new_empty(shape)
 
 
+def _dense(t: torch.Tensor) -> torch.Tensor:
+    """t, contiguous and on a 16-byte boundary."""
+    t = t.contiguous()
+    return t.clone() if t.data_ptr() & 15 else t
+
+
 def _flat(t: torch.Tensor, name: str, shape, dtype, dev: int) -> None:
     """t is contiguous, of this shape and type, on CUDA device dev."""
     if t.dtype is not dtype or t.get_device() != dev or not t.is_contiguous() or t.shape != shape:
@@ -178,7 +184,7 @@ class _PackedAttention(torch.autograd.Function):
         cfg = make_packed_config(q, k, v, cu_seqlens, softmax_scale, _NEW)
         o_lo = _like(q, (cfg.total, cfg.Hq, _D)) if cfg.dtype == C.HGA_BF16 else None
         o, lse = packed_attn_fwd(cfg, q, k, v, cu_seqlens, o_lo=o_lo)
-        ctx.cfg = cfg
+        ctx.softmax_scale = softmax_scale
         ctx.save_for_backward(q, k, v, cu_seqlens, o, lse, o_lo)
         ctx.mark_non_differentiable(lse)
         ctx.set_materialize_grads(False)
@@ -189,11 +195,13 @@ class _PackedAttention(torch.autograd.Function):
     def backward(ctx, d_o, _dlse):
         if d_o is None:
             return None, None, None, None, None
+        # saved-tensor hooks may hand back tensors of the same values with other strides (save_on_cpu makes the slices of
+        # a fused projection dense): the configuration describes what is here, not what the forward had
         q, k, v, cu_seqlens, o, lse, o_lo = ctx.saved_tensors
-        d_o = d_o.contiguous()
-        if d_o.data_ptr() & 15:
-            d_o = d_o.clone()
-        dq, dk, dv = packed_attn_bwd(ctx.cfg, q, k, v, cu_seqlens, o, lse, d_o, o_lo=o_lo)
+        cfg = make_packed_config(q, k, v, cu_seqlens, ctx.softmax_scale, _NEW)
+        o, lse, d_o = _dense(o), _dense(lse), _dense(d_o)
+        o_lo = None if o_lo is None else _dense(o_lo)
+        dq, dk, dv = packed_attn_bwd(cfg, q, k, v, cu_seqlens, o, lse, d_o, o_lo=o_lo)
         return dq, dk, dv, None, None
 
 

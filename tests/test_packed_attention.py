@@ -491,3 +491,18 @@ def test_refusals(hga):
         hga.packed_attn_fwd(cfg, q, k, v, cu, workspace=torch.zeros(16, dtype=torch.uint8, device="cuda"))
     with pytest.raises(ValueError):
         hga.packed_attn_fwd(cfg, q, k, v, cu, o=torch.empty_like(q))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("layout", ["fused", "heads", "wide"])
+@pytest.mark.parametrize("pin", [False, True])
+def test_saved_tensors_on_the_host(hga, dtype, layout, pin):
+    """Tensors kept on the host between the passes come back with other strides: the same gradients."""
+    lens = [129, 0, 70, 3]
+    q, k, v, d_o = make(lens, 4, 2, dtype, layout, tail=9)
+    want = run(hga, q, k, v, d_o, ends(lens))
+    leaves = [x.detach().requires_grad_() for x in (q, k, v)]
+    with torch.autograd.graph.save_on_cpu(pin_memory=pin):
+        o, _ = hga.packed_attention(*leaves, ends(lens))
+    for got, n in zip(torch.autograd.grad(o, leaves, d_o), ("dq", "dk", "dv")):
+        assert torch.equal(got, want[n]), n

@@ -1,0 +1,72 @@
+"""What the readout's Python side hands to the library, and what it refuses before that: on the CPU, with tensors that say
+they are on a device and the library's calls replaced by recorders (no GPU needed)."""
+import pytest
+import torch
+
+from hierarchical_kv_routing_tok_b200 import _capi as C
+from hierarchical_kv_routing_tok_b200 import build as B
+from hierarchical_kv_routing_tok_b200 import readout as RO
+
+BF16, F32 = torch.bfloat16, torch.float32
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    """[(name, positional arguments without the stream)] of the library's calls; nothing runs."""
+    B.build()
+    out = []
+    monkeypatch.setattr(RO, "_launch", lambda fn, device, *args: out.append((fn.__name__, args)))
+    monkeypatch.setattr(RO, "_raw_stream", lambda device: 0)
+    monkeypatch.setattr(torch.Tensor, "get_device", lambda self: 0)
+    monkeypatch.setattr(torch.Tensor, "is_cuda", property(lambda self: True))
+    return out
+
+
+def fused(T=9, Hq=4, Hkv=2, dtype=BF16):
+    q, k, v = torch.randn(T, Hq + 2 * Hkv, 128).to(dtype).split([Hq, Hkv, Hkv], dim=1)
+    return q, k, v, torch.tensor([0, T], dtype=torch.int32)
+
+
+def heads(T=9, Hq=4, Hkv=2, dtype=BF16):
+    q, k, v = (torch.randn(h, T, 128).to(dtype).transpose(0, 1) for h in (Hq, Hkv, Hkv))
+    return q, k, v, torch.tensor([0, T], dtype=torch.int32)
+
+
+def repack(how):
+    """Pack and unpack hooks that keep values and change strides, as activation offload does."""
+    def pack(t):
+        return t.detach().clone(memory_format=torch.contiguous_format)
+
+    def unpack(t):
+        if how == "dense" or t.dim() != 3:
+            return t
+        wide = torch.zeros(t.shape[0] + 1, t.shape[1] + 3, t.shape[2], dtype=t.dtype)
+        wide[:-1, 1:-2] = t
+        return wide[:-1, 1:-2]
+    return torch.autograd.graph.saved_tensors_hooks(pack, unpack)
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("layout", [fused, heads])
+@pytest.mark.parametrize("how", ["dense", "wide"])
+def test_backward_describes_the_tensors_it_gets(calls, dtype, layout, how):
+    q, k, v, cu = layout(dtype=dtype)
+    leaves = [x.detach().requires_grad_() for x in (q, k, v)]
+    with repack(how):
+        o, _ = RO.packed_attention(*leaves, cu, softmax_scale=0.25)
+    seen = []
+    real = RO.packed_attn_bwd
+
+    def bwd(cfg, q, k, v, *args, **kw):
+        seen.extend([q, k, v])
+        return real(cfg, q, k, v, *args, **kw)
+
+    with pytest.MonkeyPatch.context() as m:
+        m.setattr(RO, "packed_attn_bwd", bwd)
+        torch.autograd.grad(o, leaves, torch.ones_like(o))
+    name, args = calls[-1]
+    cfg = args[0]
+    assert name == "packed_attn_bwd" and abs(cfg.softmax_scale - 0.25) < 1e-7
+    got = [(cfg.q_stride_t, cfg.q_stride_h), (cfg.k_stride_t, cfg.k_stride_h), (cfg.v_stride_t, cfg.v_stride_h)]
+    assert got == [t.stride()[:2] for t in seen]
+    assert list(args[1:4]) == [t.data_ptr() for t in seen]
