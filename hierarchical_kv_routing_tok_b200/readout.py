@@ -105,6 +105,20 @@ def make_packed_config(q, k, v, cu_seqlens, softmax_scale: float | None = None, 
                           _scale(softmax_scale), 0, wait_limit_ns)
 
 
+def _check_packed(cfg, q, k, v, cu_seqlens) -> None:
+    """q, k, v and cu_seqlens are what cfg describes."""
+    T, dtype, dev = cfg.total, q.dtype, q.get_device()
+    if _DT.get(dtype) != cfg.dtype:
+        raise ValueError(f"q has dtype {dtype}, which is not the configuration's")
+    for t, name, H, st, sh in ((q, "q", cfg.Hq, cfg.q_stride_t, cfg.q_stride_h),
+                               (k, "k", cfg.Hkv, cfg.k_stride_t, cfg.k_stride_h),
+                               (v, "v", cfg.Hkv, cfg.v_stride_t, cfg.v_stride_h)):
+        want, got = (st or H * _D, sh or _D), _strides(t, name, T, H, dtype, dev)
+        if (T > 1 and got[0] != want[0]) or (T and H > 1 and got[1] != want[1]):
+            raise ValueError(f"{name} has strides {got}, the configuration {want}")
+    _flat(cu_seqlens, "cu_seqlens", (cfg.n_seqs + 1,), torch.int32, dev)
+
+
 def _workspace(cfg, workspace, q, flags: int):
     """The caller's workspace (zeroed once, checked), or a new one whose status the call clears."""
     n = C.packed_workspace_size(cfg)
@@ -126,10 +140,15 @@ def _with_flags(cfg, flags: int):
 
 
 def packed_attn_fwd(cfg, q, k, v, cu_seqlens, o=None, lse=None, workspace=None, o_lo=None):
-    """Forward.  Rows of no sequence are left as they were in a given o / lse, and hold zeros / -inf in a new
-    one.  o_lo: an output like o for a backward pass in bfloat16, what rounding took from o.  workspace: at least
+    """Forward, for a cfg of these tensors' shapes and strides (checked).  Rows of no sequence are left as they
+    were in a given o / lse, and hold zeros / -inf in a new one.  o_lo: an output like o for a backward pass in bfloat16, what rounding took from o.  workspace: at least
     ``_capi.packed_workspace_size(cfg)`` bytes, zeroed once (``read_status`` tells of a cu_seqlens that is not
     valid); without one the call makes its own."""
+    _check_packed(cfg, q, k, v, cu_seqlens)
+    return _fwd(cfg, q, k, v, cu_seqlens, o, lse, workspace, o_lo)
+
+
+def _fwd(cfg, q, k, v, cu_seqlens, o=None, lse=None, workspace=None, o_lo=None):
     T, Hq, dev, flags = cfg.total, cfg.Hq, q.get_device(), cfg.flags
     if o is None and lse is None:
         flags |= C.HGA_PACKED_FILL_TAIL
@@ -152,6 +171,11 @@ def packed_attn_fwd(cfg, q, k, v, cu_seqlens, o=None, lse=None, workspace=None, 
 def packed_attn_bwd(cfg, q, k, v, cu_seqlens, o, lse, d_o, dq=None, dk=None, dv=None, workspace=None, o_lo=None):
     """Gradients (contiguous) for d_o, from the forward's o, lse and, in bfloat16 for the accuracy of short
     sequences, o_lo.  Rows of no sequence: as in ``packed_attn_fwd`` (zeros in new gradients)."""
+    _check_packed(cfg, q, k, v, cu_seqlens)
+    return _bwd(cfg, q, k, v, cu_seqlens, o, lse, d_o, dq, dk, dv, workspace, o_lo)
+
+
+def _bwd(cfg, q, k, v, cu_seqlens, o, lse, d_o, dq=None, dk=None, dv=None, workspace=None, o_lo=None):
     T, Hq, Hkv, dev, flags = cfg.total, cfg.Hq, cfg.Hkv, q.get_device(), cfg.flags
     if dq is None and dk is None and dv is None:
         flags |= C.HGA_PACKED_FILL_TAIL
@@ -183,7 +207,7 @@ class _PackedAttention(torch.autograd.Function):
     def forward(ctx, q, k, v, cu_seqlens, softmax_scale):
         cfg = make_packed_config(q, k, v, cu_seqlens, softmax_scale, _NEW)
         o_lo = _like(q, (cfg.total, cfg.Hq, _D)) if cfg.dtype == C.HGA_BF16 else None
-        o, lse = packed_attn_fwd(cfg, q, k, v, cu_seqlens, o_lo=o_lo)
+        o, lse = _fwd(cfg, q, k, v, cu_seqlens, o_lo=o_lo)
         ctx.softmax_scale = softmax_scale
         ctx.save_for_backward(q, k, v, cu_seqlens, o, lse, o_lo)
         ctx.mark_non_differentiable(lse)
@@ -201,7 +225,7 @@ class _PackedAttention(torch.autograd.Function):
         cfg = make_packed_config(q, k, v, cu_seqlens, ctx.softmax_scale, _NEW)
         o, lse, d_o = _dense(o), _dense(lse), _dense(d_o)
         o_lo = None if o_lo is None else _dense(o_lo)
-        dq, dk, dv = packed_attn_bwd(cfg, q, k, v, cu_seqlens, o, lse, d_o, o_lo=o_lo)
+        dq, dk, dv = _bwd(cfg, q, k, v, cu_seqlens, o, lse, d_o, o_lo=o_lo)
         return dq, dk, dv, None, None
 
 
@@ -236,7 +260,7 @@ def packed_attention(q, k, v, cu_seqlens, softmax_scale: float | None = None):
         out = _PackedAttention.apply(q, k, v, cu_seqlens, softmax_scale)
         _check_accumulators(out[0].grad_fn, q.get_device())
         return out
-    return packed_attn_fwd(make_packed_config(q, k, v, cu_seqlens, softmax_scale, _NEW), q, k, v, cu_seqlens)
+    return _fwd(make_packed_config(q, k, v, cu_seqlens, softmax_scale, _NEW), q, k, v, cu_seqlens)
 
 
 class PagedKVCache:

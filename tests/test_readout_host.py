@@ -55,14 +55,14 @@ def test_backward_describes_the_tensors_it_gets(calls, dtype, layout, how):
     with repack(how):
         o, _ = RO.packed_attention(*leaves, cu, softmax_scale=0.25)
     seen = []
-    real = RO.packed_attn_bwd
+    real = RO._bwd
 
     def bwd(cfg, q, k, v, *args, **kw):
         seen.extend([q, k, v])
         return real(cfg, q, k, v, *args, **kw)
 
     with pytest.MonkeyPatch.context() as m:
-        m.setattr(RO, "packed_attn_bwd", bwd)
+        m.setattr(RO, "_bwd", bwd)
         torch.autograd.grad(o, leaves, torch.ones_like(o))
     name, args = calls[-1]
     cfg = args[0]
@@ -70,3 +70,46 @@ def test_backward_describes_the_tensors_it_gets(calls, dtype, layout, how):
     got = [(cfg.q_stride_t, cfg.q_stride_h), (cfg.k_stride_t, cfg.k_stride_h), (cfg.v_stride_t, cfg.v_stride_h)]
     assert got == [t.stride()[:2] for t in seen]
     assert list(args[1:4]) == [t.data_ptr() for t in seen]
+
+
+@pytest.mark.parametrize("T,Hkv", [(9, 2), (1, 2), (9, 1), (0, 2)])
+def test_config_and_tensors_agree(calls, T, Hkv):
+    """A configuration with the tensors that it was made from, and written by hand with contiguous strides left out."""
+    q, k, v, cu = fused(T, 4, Hkv)
+    o, lse = RO.packed_attn_fwd(RO.make_packed_config(q, k, v, cu), q, k, v, cu)
+    RO.packed_attn_bwd(RO.make_packed_config(q, k, v, cu), q, k, v, cu, o, lse, o)
+    q, k, v = (x.contiguous() for x in (q, k, v))
+    cfg = C.PackedConfig(4, Hkv, 128, 1, T, dtype=C.HGA_BF16)
+    RO.packed_attn_fwd(cfg, q, k, v, cu)
+    assert [n for n, _ in calls] == ["packed_attn_fwd", "packed_attn_bwd", "packed_attn_fwd"]
+
+
+WRONG = {
+    "fewer rows": lambda q, k, v, cu: (q[:8], k[:8], v[:8], cu),
+    "short k": lambda q, k, v, cu: (q, k[:8], v, cu),
+    "heads of q": lambda q, k, v, cu: (q[:, :2], k, v, cu),
+    "heads of v": lambda q, k, v, cu: (q, k, v[:, :1], cu),
+    "dense q": lambda q, k, v, cu: (q.contiguous(), k, v, cu),
+    "dense k": lambda q, k, v, cu: (q, k.contiguous(), v, cu),
+    "dense v": lambda q, k, v, cu: (q, k, v.contiguous(), cu),
+    "float32": lambda q, k, v, cu: (q.float(), k.float(), v.float(), cu),
+    "dtype of k": lambda q, k, v, cu: (q, k.half(), v, cu),
+    "more bounds": lambda q, k, v, cu: (q, k, v, torch.zeros(5, dtype=torch.int32)),
+    "fewer bounds": lambda q, k, v, cu: (q, k, v, cu[:1]),
+    "int64 bounds": lambda q, k, v, cu: (q, k, v, cu.long()),
+    "strided bounds": lambda q, k, v, cu: (q, k, v, torch.zeros(4, dtype=torch.int32)[::2]),
+    "off a boundary": lambda q, k, v, cu: (q, k, torch.zeros(9 * 1024 + 1, dtype=BF16)[1:].view(9, 8, 128)[:, :2], cu),
+}
+
+
+@pytest.mark.parametrize("what", WRONG)
+def test_tensors_that_are_not_the_configurations_are_refused(calls, what):
+    q, k, v, cu = fused()
+    cfg = RO.make_packed_config(q, k, v, cu)
+    o, lse = torch.zeros(9, 4, 128, dtype=BF16), torch.zeros(4, 9)
+    args = WRONG[what](q, k, v, cu)
+    with pytest.raises(ValueError):
+        RO.packed_attn_fwd(cfg, *args)
+    with pytest.raises(ValueError):
+        RO.packed_attn_bwd(cfg, *args, o, lse, o)
+    assert not calls
