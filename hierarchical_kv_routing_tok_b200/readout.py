@@ -288,6 +288,8 @@ class PagedKVCache:
                 raise ValueError(f"{name} must be a CUDA tensor")
             if P and L and not t[0, 0].is_contiguous():
                 raise ValueError(f"{name}: a page of a layer must be contiguous")
+            if (L > 1 and t.stride(0) == 0) or (P > 1 and t.stride(1) == 0):       # (to the library, 0 is contiguous)
+                raise ValueError(f"{name}: layers and pages must not share memory, got strides {t.stride()}")
         dev = k_pool.get_device()
         if v_pool.get_device() != dev:
             raise ValueError(f"v_pool is on {v_pool.device}, expected {k_pool.device}")

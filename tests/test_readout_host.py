@@ -113,3 +113,22 @@ def test_tensors_that_are_not_the_configurations_are_refused(calls, what):
     with pytest.raises(ValueError):
         RO.packed_attn_bwd(cfg, *args, o, lse, o)
     assert not calls
+
+
+def ints(max_seqs, max_pages, n_pages):
+    return [torch.zeros(s, dtype=torch.int32) for s in ((max_seqs, max_pages), (max_seqs,), (n_pages,))]
+
+
+@pytest.mark.parametrize("shape,expand", [((1, 6), (3, 6)), ((2, 1), (2, 6)), ((1, 1), (3, 6))], ids=["layers", "pages", "both"])
+def test_expanded_pools_are_refused(calls, shape, expand):
+    """Layers or pages of one memory, which the library would take for contiguous ones and step behind the pool."""
+    pool = torch.zeros(*shape, 2, 16, 128, dtype=BF16).expand(*expand, 2, 16, 128)
+    with pytest.raises(ValueError, match="must not share memory"):
+        RO.PagedKVCache(pool, pool, *ints(2, 3, expand[1]))
+
+
+def test_pools_of_one_layer_or_page_may_have_any_stride(calls):
+    for shape in ((1, 6), (3, 1), (1, 1)):
+        pools = [torch.zeros(*shape, 2, 16, 128, dtype=BF16) for _ in range(2)]
+        pools = [x.as_strided(x.shape, [0 if n == 1 else s for n, s in zip(x.shape, x.stride())]) for x in pools]
+        RO.PagedKVCache(*pools, *ints(2, 3, shape[1]))
