@@ -128,7 +128,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(qdo_full, 1);
     for (int s = 0; s < KS; ++s) {
       mbar_init(kv_full(s), 2);             // the K and the V producer
-      mbar_init(k_empty(s), 1);
+      mbar_init(k_empty(s), 2);             // the products' commit, and the cleaning warp, which waits for every tile
       mbar_init(k_clean(s), 1);
     }
     for (int s = 0; s < VS; ++s) mbar_init(v_empty(s), 1);
@@ -210,14 +210,16 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       __syncwarp();
       ++loads;
-      for (int j = 0; ok && j < x.T; ++j, ++J) {             // (every tile is waited for: a parity names only
-        const int s = (int)(J % KS);                         // the current phase and the one before)
-        ok = wait_w(kv_full(s), (uint32_t)((J / KS) & 1), abort_flag, p.status, p.wait_ns);
-        if (ok && x.len - j * kBN < kBN) {
+      for (int j = 0; j < x.T; ++j, ++J) {                   // (every tile is waited for, and its stage is free only
+        const int s = (int)(J % KS);                         // behind this warp: a parity names the current phase and
+        ok = wait_w(kv_full(s), (uint32_t)((J / KS) & 1), abort_flag, p.status, p.wait_ns);      // the one before)
+        if (!ok) break;
+        if (x.len - j * kBN < kBN) {
           zero_rows(sbase + L::kK + s * kTileBytes, kBN, kHalfBytes, x.len - j * kBN);
           __syncwarp();
           if (lane == 0) mbar_arrive(k_clean(s));
         }
+        if (lane == 0) mbar_arrive(k_empty(s));
       }
     }
     if (lane == 0 && loads) drain_wait(qdo_full, (loads - 1) & 1, p.status);
@@ -567,7 +569,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int s = 0; s < NS; ++s) {
       mbar_init(q_full(s), 1);
       mbar_init(stat_full(s), 32);          // the 32 lanes' copies of lse and delta
-      mbar_init(q_empty(s), 1);
+      mbar_init(q_empty(s), ragged ? 2 : 1);      // the products' commit, and warp 3 where it waits for every step
       mbar_init(q_clean(s), 1);
     }
     for (int b = 0; b < 2; ++b) {
@@ -649,6 +651,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
         if (lane == 0) mbar_arrive(q_clean(s));
       }
+      if (lane == 0) mbar_arrive(q_empty(s));            // (a parity names only the current phase and the one before)
     }
   } else if (warp == 1) {
     // ======================= MMA issuer: the whole warp runs the loop, one elected lane issues

@@ -186,7 +186,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     mbar_init(q_empty, 1);
     for (int s = 0; s < NS; ++s) {
       mbar_init(full(s), 1);
-      mbar_init(empty(s), 1);
+      mbar_init(empty(s), 2);               // the products' commit, and the checking warp, which waits for every item
       mbar_init(v_clean(s), 1);
     }
     for (int i = 0; i < 2; ++i) {
@@ -256,20 +256,22 @@ __global__ void __launch_bounds__(kThreads, 1)
     for (int k = 0; ok && load_unit<kOwn>(p, own, n_units, k, &x); ++k) {
       const int jd = x.t0 / kBN;
       bool any = false;
-      for (int j = -1; j < x.Tmax; ++j, ++J) {          // (every item is waited for: a parity names only the current
-        const int s = (int)(J % NS);                    // phase and the one before)
+      for (int j = -1; j < x.Tmax; ++j, ++J) {          // (every item is waited for, and its slot is free only behind
+        const int s = (int)(J % NS);                    // this warp: a parity names the current phase and the one before)
         ok = mbar_wait_w(full(s), (uint32_t)((J / NS) & 1), abort_flag, p.status, p.wait_ns);
         if (!ok) break;
-        if (j < jd) continue;
-        const uint32_t tile = sbase + L::kV + s * kTileBytes;
-        if (x.len - j * kBN < kBN) {
-          zero_rows(tile, kBN, kHalfBytes, x.len - j * kBN);
+        if (j >= jd) {
+          const uint32_t tile = sbase + L::kV + s * kTileBytes;
+          if (x.len - j * kBN < kBN) {
+            zero_rows(tile, kBN, kHalfBytes, x.len - j * kBN);
+            __syncwarp();
+          }
+          any |= zero_not_finite(tile, kBN * 16);
+          if (lane == 0) not_finite[k & 3] = any;       // (the first query tile may end before the second)
           __syncwarp();
+          if (lane == 0) mbar_arrive(v_clean(s));
         }
-        any |= zero_not_finite(tile, kBN * 16);
-        if (lane == 0) not_finite[k & 3] = any;         // (the first query tile may end before the second)
-        __syncwarp();
-        if (lane == 0) mbar_arrive(v_clean(s));
+        if (lane == 0) mbar_arrive(empty(s));
       }
     }
   } else if (warp == kMmaWarp) {
