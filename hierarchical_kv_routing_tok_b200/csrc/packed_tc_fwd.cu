@@ -55,10 +55,10 @@ struct FwdSmem {
   static constexpr uint32_t kV = kK + NS * kTileBytes;
   static constexpr uint32_t kO = kV + NS * kTileBytes;          // 2 KB per softmax warp: 32 rows x 32 dims of o
   static constexpr uint32_t kBar = kO + 16 * 2048;
-  // q_full, q_empty, full[NS], empty[NS], v_clean[NS], s_full[2], p_full[2], o_full[2], mma_done
-  static constexpr int kNumBars = 2 + 3 * NS + 6 + 1;
-  static constexpr uint32_t kMisc = kBar + 8 * kNumBars;        // TMEM address, abort, flags of 4 units
-  static constexpr uint32_t kNeed = kMisc + 32;                 // [tile parity][pair of warps][half]
+  // q_full, q_empty, full[NS], empty[NS], v_clean[NS], s_full[2], p_full[2], o_full[2], mma_done, flag_free[2][4]
+  static constexpr int kNumBars = 2 + 3 * NS + 6 + 1 + 8;
+  static constexpr uint32_t kMisc = kBar + 8 * kNumBars;        // TMEM address, abort, flags of 2 x 4 units
+  static constexpr uint32_t kNeed = kMisc + 48;                 // [tile parity][pair of warps][half]
   static constexpr uint32_t kOwn = (kNeed + 2 * 8 * 2 * 4 + 15) & ~15u;
   static constexpr uint32_t kBytes = kOwn + sizeof(Own);
 };
@@ -174,10 +174,11 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto p_full = [&](int i) { return BAR(4 + 3 * NS + i); };
   auto o_full = [&](int i) { return BAR(6 + 3 * NS + i); };
   const uint32_t mma_done = BAR(8 + 3 * NS);
+  auto flag_free = [&](int i, int n) { return BAR(9 + 3 * NS + 4 * i + (n & 3)); };
   uint32_t* tmem_slot = reinterpret_cast<uint32_t*>(smem + L::kMisc);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + L::kMisc + 4);
-  // whether a unit's diagonal tiles hold values that are not finite: unit k in slot k mod 4 (the cleaner is at
-  // most two units ahead of the epilogue, the V ring having two stages)
+  // whether the diagonal tiles hold values that are not finite: of query tile i's n-th output (units without that tile do
+  // not count) in slot 4 i + n mod 4, free when the tile's eight softmax warps have read what output n - 4 left there
   volatile int* not_finite = reinterpret_cast<volatile int*>(smem + L::kMisc + 8);
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -195,6 +196,7 @@ __global__ void __launch_bounds__(kThreads, 1)
       mbar_init(o_full(i), 1);
     }
     mbar_init(mma_done, 1);
+    for (int n = 0; n < 8; ++n) mbar_init(flag_free(n >> 2, n), 8);
     *abort_flag = 0;
     mbar_fence_init();
   }
@@ -252,10 +254,15 @@ __global__ void __launch_bounds__(kThreads, 1)
   } else if (warp == 18) {
     // ======================= check of the V tiles at or behind the unit's first token
     int64_t J = 0;
+    int n1 = 0;                                         // second query tiles so far (every unit has a first)
     bool ok = true;
     for (int k = 0; ok && load_unit<kOwn>(p, own, n_units, k, &x); ++k) {
       const int jd = x.t0 / kBN;
       bool any = false;
+      const bool two = x.T[1] > 0;
+      ok = mbar_wait_w(flag_free(0, k), (uint32_t)((k >> 2) & 1) ^ 1, abort_flag, p.status, p.wait_ns) &&
+           (!two || mbar_wait_w(flag_free(1, n1), (uint32_t)((n1 >> 2) & 1) ^ 1, abort_flag, p.status, p.wait_ns));
+      if (!ok) break;
       for (int j = -1; j < x.Tmax; ++j, ++J) {          // (every item is waited for, and its slot is free only behind
         const int s = (int)(J % NS);                    // this warp: a parity names the current phase and the one before)
         ok = mbar_wait_w(full(s), (uint32_t)((J / NS) & 1), abort_flag, p.status, p.wait_ns);
@@ -267,12 +274,16 @@ __global__ void __launch_bounds__(kThreads, 1)
             __syncwarp();
           }
           any |= zero_not_finite(tile, kBN * 16);
-          if (lane == 0) not_finite[k & 3] = any;       // (the first query tile may end before the second)
+          if (lane == 0) {                              // (the first query tile may end before the second)
+            not_finite[k & 3] = any;
+            if (two) not_finite[4 + (n1 & 3)] = any;
+          }
           __syncwarp();
           if (lane == 0) mbar_arrive(v_clean(s));
         }
         if (lane == 0) mbar_arrive(empty(s));
       }
+      n1 += two;
     }
   } else if (warp == kMmaWarp) {
     // ======================= MMA issuer: the whole warp runs the loop, one elected lane issues.  Per tile it waits for the
@@ -457,7 +468,6 @@ __global__ void __launch_bounds__(kThreads, 1)
       }
       if (!ok) break;
       ok = wait_w(o_full(i), no & 1, abort_flag, p.status, p.wait_ns);
-      ++no;
       if (lane == 0) put(s_need + 64 * (T & 1) + 4 * half, ok ? 0 : 2);
       put(s_row + 8192 * half, __float_as_uint(l));
       pair_sync();
@@ -466,8 +476,12 @@ __global__ void __launch_bounds__(kThreads, 1)
       pair_sync();
       if (!ok) break;
       tc_fence_after();
+      const bool fix = not_finite[4 * i + (no & 3)] != 0;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(flag_free(i, no));
+      ++no;
       write_output(p, OutArgs{x.start, x.len, x.t0, x.kh, x.h0, i * p.tp, quarter * 32, 64 * half, t_pos, tO,
-                              sbase + L::kO + (uint32_t)(st >> 5) * 2048u, 1.f / l, not_finite[k & 3] != 0});
+                              sbase + L::kO + (uint32_t)(st >> 5) * 2048u, 1.f / l, fix});
       if (t_pos < x.len && half == 0)
         p.lse[(x.h0 + (r & (p.pk - 1))) * p.total + (int64_t)x.start + t_pos] = (m + __log2f(l)) * 0.6931471805599453f;
       tc_fence_before();

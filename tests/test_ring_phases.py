@@ -68,3 +68,50 @@ def test_the_cleaning_warp_holds_the_ring(name, bar, ring):
 @pytest.mark.parametrize("ring", [2, 3, 4])
 def test_the_model_sees_a_ring_that_does_not_wait(ring):
     assert sum(late(ring, 1, 200, seed) for seed in range(20)) > 0
+
+
+def stale_flags(guarded, units, seed):
+    """The forward's flags of units (whether their values are all finite), written by the checking warp, read by the warps of two
+    query tiles; units may have no second tile, and pass its warps by.  How many flags are read that another unit's has
+    overwritten: four slots for all, or (guarded) four for each tile's outputs, with a barrier that frees them."""
+    rng = random.Random(seed)
+    has = [(True, rng.random() < 0.3) for _ in range(units)]
+    flag = [[None] * 4, [None] * 4]
+    free = [[Barrier(1) for _ in range(4)] for _ in range(2)]
+    done, outputs, written = [0, 0], [0, 0], [0, 0]    # units and outputs behind each tile's warps; flags written for each
+    at = wrong = steps = 0
+    while min(done) < units:
+        steps += 1
+        assert steps < 1000 * units, "the flags stand still"
+        who = rng.choice([0] * 4 + [1] + [2] * 4)
+        if who == 2:
+            if at == units or at > done[0] + 2:        # the ring lets the check run two units ahead of the first tile
+                continue
+            for i in range(2):
+                n = written[i] if guarded else at
+                if guarded and has[at][i] and not free[i][n % 4].passes(n // 4 & 1 ^ 1):
+                    break
+            else:
+                for i in range(2):
+                    if has[at][i]:
+                        flag[i if guarded else 0][(written[i] if guarded else at) % 4] = at
+                        written[i] += 1
+                at += 1
+        elif done[who] < units:
+            k, n = done[who], outputs[who]
+            if has[k][who]:
+                if k >= at:
+                    continue                           # its output waits for the check
+                wrong += flag[who if guarded else 0][(n if guarded else k) % 4] != k
+                free[who][n % 4].arrive()
+                outputs[who] += 1
+            done[who] += 1
+    return wrong
+
+
+def test_the_flags_of_units_wait_for_their_readers():
+    with open(os.path.join(CSRC, "packed_tc_fwd.cu")) as f:
+        text = f.read()
+    guarded = "mbar_init(flag_free(n >> 2, n), 8)" in text and "mbar_wait_w(flag_free(1, n1)" in text
+    assert sum(stale_flags(guarded, 300, seed) for seed in range(20)) == 0
+    assert sum(stale_flags(False, 300, seed) for seed in range(20)) > 0
