@@ -442,10 +442,12 @@ cudaError_t launch_move(const Cache& c, const Scratch& s, int64_t pairs, void* k
                           static_cast<char*>(k_pool), static_cast<char*>(v_pool), remap ? 1 : 0);
 }
 
+// One CTA with `smem` bytes, which no call has more than `most` of.  The attribute belongs to the process, not to the call: what
+// threads set at the same time must be one value.  (47 KB: what a kernel may have without it, less its static variables.)
 template <typename K, typename... A>
-cudaError_t launch_one(K kernel, size_t smem, cudaStream_t st, A... args) {
-  if (smem > 48 * 1024) {
-    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+cudaError_t launch_one(K kernel, size_t smem, size_t most, cudaStream_t st, A... args) {
+  if (smem > 47 * 1024) {
+    cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)most);
     if (e != cudaSuccess) return e;
   }
   return launch_dependent(kernel, dim3(1), dim3(kPlanThreads), smem, st, 1, args...);
@@ -455,7 +457,7 @@ cudaError_t launch_one(K kernel, size_t smem, cudaStream_t st, A... args) {
 
 cudaError_t launch_reserve(const Cache& c, const Scratch& s, int n, const int32_t* rows, const int32_t* add,
                            int32_t* pos, cudaStream_t st) {
-  return launch_one(reserve_kernel, sizeof(PlanSmem), st, c, s, n, rows, add, pos);
+  return launch_one(reserve_kernel, sizeof(PlanSmem), sizeof(PlanSmem), st, c, s, n, rows, add, pos);
 }
 
 cudaError_t launch_write(const Cache& c, int layer, int n, const int32_t* rows, const int32_t* pos,
@@ -475,12 +477,12 @@ cudaError_t launch_write(const Cache& c, int layer, int n, const int32_t* rows, 
 
 cudaError_t launch_fork(const Cache& c, const Scratch& s, int n, const int32_t* src, const int32_t* dst, void* k_pool,
                         void* v_pool, cudaStream_t st) {
-  cudaError_t e = launch_one(fork_kernel, sizeof(PlanSmem), st, c, s, n, src, dst);
+  cudaError_t e = launch_one(fork_kernel, sizeof(PlanSmem), sizeof(PlanSmem), st, c, s, n, src, dst);
   return e != cudaSuccess ? e : launch_move(c, s, n, k_pool, v_pool, false, st);
 }
 
 cudaError_t launch_free(const Cache& c, int n, const int32_t* rows, cudaStream_t st) {
-  return launch_one(free_kernel, sizeof(PlanSmem), st, c, n, rows);
+  return launch_one(free_kernel, sizeof(PlanSmem), sizeof(PlanSmem), st, c, n, rows);
 }
 
 cudaError_t launch_compact(const Cache& c, const Scratch& s, void* k_pool, void* v_pool, int32_t* n_used,
@@ -491,7 +493,7 @@ cudaError_t launch_compact(const Cache& c, const Scratch& s, void* k_pool, void*
 
 cudaError_t launch_copy(const Cache& c, const Scratch& s, int n, const int32_t* src, const int32_t* dst, void* k_pool,
                         void* v_pool, cudaStream_t st) {
-  cudaError_t e = launch_one(copy_list_kernel, (size_t)((c.n_pages + 31) / 32) * 4, st, c, s, n, src, dst);
+  cudaError_t e = launch_one(copy_list_kernel, (size_t)((c.n_pages + 31) / 32) * 4, kMaxPages / 8, st, c, s, n, src, dst);
   return e != cudaSuccess ? e : launch_move(c, s, n, k_pool, v_pool, false, st);
 }
 

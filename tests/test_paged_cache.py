@@ -3,6 +3,7 @@ its contents against the tokens that were put in, its attention against float64 
 readout_ref."""
 import math
 import random
+import threading
 
 import pytest
 import torch
@@ -555,3 +556,47 @@ def test_refusals(hga):
                                           cache.seq_len, cache.ref_count)):
         with pytest.raises((ValueError, RuntimeError)):
             call()
+
+
+def big_cache(hga, n_pages):
+    pools = [torch.empty(1, n_pages, 1, 16, 128, device="cuda", dtype=BF16) for _ in range(2)]
+    return hga.PagedKVCache(*pools, i32([[0]]), i32([0]), torch.zeros(n_pages, dtype=torch.int32, device="cuda"))
+
+
+@pytest.mark.parametrize("n_pages", [380_000, 385_024, 393_150, 393_200, 393_217, 1 << 20])
+def test_copy_pages_of_large_pools(hga, n_pages):
+    """The list of destinations seen (a bit per page) at and around 48 KB of shared memory."""
+    cache = big_cache(hga, n_pages)
+    src, dst = [n_pages - 1, 5, 5], [7, n_pages - 2, 0]
+    cache.k_pool[:, src] = 3
+    cache.v_pool[:, src] = 4
+    cache.copy_pages(i32(src), i32(dst))
+    assert cache.status() == 0
+    assert (cache.k_pool[:, dst] == 3).all() and (cache.v_pool[:, dst] == 4).all()
+    cache.copy_pages(i32([1, 2]), i32([n_pages - 1, n_pages - 1]))
+    assert cache.status() == hga._capi.HGA_ERR_ARG
+
+
+def test_copy_pages_from_two_threads(hga):
+    """Pools of different sizes, copied from two threads at once: no call takes the other's limit of shared memory."""
+    caches = [big_cache(hga, n) for n in (400_000, 900_000)]
+    streams, errors = [torch.cuda.Stream() for _ in caches], []
+    src, dst = i32([1]), i32([2])
+    torch.cuda.synchronize()
+
+    def work(cache, stream):
+        try:
+            with torch.cuda.stream(stream):
+                for _ in range(3000):
+                    cache.copy_pages(src, dst)
+        except Exception as e:                         # noqa: BLE001 (whatever it is, the test fails with it)
+            errors.append(e)
+
+    threads = [threading.Thread(target=work, args=a) for a in zip(caches, streams)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not errors
+    assert [c.status() for c in caches] == [0, 0]
