@@ -395,6 +395,9 @@ HGA_API int hga_route_groups_cached(const hga_config_t* cfg, const float* qb, co
  * Products accumulate in float32.  bf16: probabilities and dS are rounded to bf16 before their second
  * product (of dS in dQ, what that takes is added back where it counts most).  float32: each operand as the sum of two tf32 numbers, which keeps float32 accuracy (the
  * scores of a q or k row that is not finite are NaN).
+ * Sums are formed before their last factor (1 / sum p for o, the scale for dq and dk) and overflow where they pass the
+ * largest float32: in bf16, whose p is relative to a maximum up to 2^8 too small, for values of v from 2^120 / (attended
+ * tokens) on.
  * total <= 2^31 - 1 - 256 and (total / 16 + n_seqs) * Hq < 2^31; total = 0 or n_seqs = 0 is a valid
  * empty problem.
  * Two calls that may overlap in time need two workspaces. */

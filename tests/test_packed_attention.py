@@ -506,3 +506,40 @@ def test_saved_tensors_on_the_host(hga, dtype, layout, pin):
         o, _ = hga.packed_attention(*leaves, ends(lens))
     for got, n in zip(torch.autograd.grad(o, leaves, d_o), ("dq", "dk", "dv")):
         assert torch.equal(got, want[n]), n
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("at", [0, 1, 63, 130, 299])
+def test_largest_numbers_of_the_type(hga, dtype, at):
+    """The type's largest and lowest values in v and k of token `at`: finite numbers, which no row before it sees and no
+    product with 0 makes infinite.  q and d_o are 0 in those dims, so that scores, dP and delta are what they were."""
+    lens, big = [10, 300, 4], torch.finfo(dtype).max
+    q, k, v, d_o = make(lens, 4, 2, dtype, seed=at)
+    cu, dims = ends(lens), [5, 77]
+    q[..., dims] = 0
+    d_o[..., dims] = 0
+    clean = run(hga, q, k, v, d_o, cu)
+    for x in (k, v):
+        x[10 + at, 0, 5], x[10 + at, 0, 77] = big, -big
+    got = run(hga, q, k, v, d_o, cu)
+    ref = R.packed(q, k, v, lens, d_o=d_o)
+    # sums in float32 before their last factor: infinite, of the right sign, where they pass the largest float32.  dq =
+    # scale (sum ds k): one term of it, ds big, is all that counts here, and dq itself may be less (the scale is 0.088).
+    # o = (sum p v) / sum p: in bf16 p is relative to a maximum that is up to 2^8 too small, in float32 p is at most 1; an
+    # infinite o makes delta, and with it the sequence's gradients, undefined.
+    def over(n, factor):
+        x = ref[n].abs() * factor > 0.99 * torch.finfo(F32).max
+        assert torch.equal(got[n][x & got[n].isinf()].sign().double(), ref[n][x & got[n].isinf()].sign())
+        return x
+    assert torch.equal(got["lse"], clean["lse"])
+    for n, factor in (("o", 1 if dtype == F32 else 2 ** 8), ("dq", math.sqrt(128)))[:2 if dtype == F32 else 1]:
+        hit = torch.zeros_like(got[n], dtype=torch.bool)
+        hit[10 + at:310, :2, dims] = True
+        assert torch.equal(got[n][~hit], clean[n][~hit]), n
+        big_sum = over(n, factor)
+        assert (hit | ~big_sum).all() and torch.isfinite(got[n][~big_sum]).all() and not got[n].isnan().any()
+        big_sum &= got[n].isinf()
+        R.check(got[n].masked_fill(big_sum, 0), {n: ref[n].masked_fill(big_sum, 0), "e_" + n: ref["e_" + n]}, n)
+    if dtype == F32:
+        for n in ("dk", "dv"):
+            assert torch.equal(got[n], clean[n]), n
