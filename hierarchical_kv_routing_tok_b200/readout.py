@@ -10,6 +10,7 @@ needs no host synchronisation and can be captured into a CUDA graph.  Every comp
 from __future__ import annotations
 
 import torch
+import torch.autograd.forward_ad as forward_ad
 
 from . import _capi as C
 from .api import _need, read_status
@@ -244,10 +245,32 @@ def _check_accumulators(node, dev: int) -> None:
 _ACCUMULATE = "torch::autograd::AccumulateGrad"
 
 
+def _tangents(*tensors) -> bool:
+    """Whether one of them carries a forward-mode derivative, which only an autograd function refuses."""
+    return forward_ad._current_level >= 0 and any(forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+
+
+class _NoBackward(torch.autograd.Function):
+    """Outputs of a kernel without a backward pass, in the graph of its input: a backward pass through them raises instead of
+    leaving their part out."""
+
+    @staticmethod
+    def forward(ctx, x, name, fn):
+        ctx.name = name
+        out = fn(x)
+        ctx.mark_non_differentiable(out[1])
+        return out
+
+    @staticmethod
+    def backward(ctx, *_):
+        raise RuntimeError(f"{ctx.name} has no backward pass")
+
+
 def packed_attention(q, k, v, cu_seqlens, softmax_scale: float | None = None):
     """Causal attention over packed sequences: rows cu_seqlens[s] .. cu_seqlens[s+1] - 1 of q [total, Hq,
     128], k, v [total, Hkv, 128] are sequence s (int32, on the device, from 0, not decreasing, at most
-    total).  Returns (o [total, Hq, 128], lse [Hq, total] float32); o is differentiable in q, k and v.
+    total).  Returns (o [total, Hq, 128], lse [Hq, total] float32); o is differentiable in q, k and v, backward
+    and once (forward-mode derivatives are refused: RuntimeError), lse is not.
     Rows of no sequence give zeros and -inf, and zero gradients.
 
     q, k and v may be strided (slices of a fused projection, transposed head-major tensors); float32 or
@@ -256,7 +279,7 @@ def packed_attention(q, k, v, cu_seqlens, softmax_scale: float | None = None):
     Forward and backward can be captured into a CUDA graph.  Where q, k or v is a leaf, no autograd graph of it
     that an earlier call on the default stream made may be alive then: autograd would make that stream wait
     for the captured one, which the capture does not allow.  Such a call is refused (RuntimeError)."""
-    if torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad):
+    if (torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad)) or _tangents(q, k, v):
         out = _PackedAttention.apply(q, k, v, cu_seqlens, softmax_scale)
         _check_accumulators(out[0].grad_fn, q.get_device())
         return out
@@ -345,7 +368,8 @@ class PagedKVCache:
 
     def write(self, layer: int, k, v, cu_new, rows, pos) -> None:
         """K/V rows of one layer into reserved places: rows cu_new[i] .. cu_new[i+1] - 1 of k, v [total, Hkv,
-        128] (may be strided) become the tokens pos[i] .. of sequence row rows[i]."""
+        128] (may be strided) become the tokens pos[i] .. of sequence row rows[i].  The cache holds values: no
+        gradient goes through it."""
         n = self._entries(rows, "rows")
         self._entries(pos, "pos", n)
         self._entries(cu_new, "cu_new", n + 1)
@@ -358,7 +382,16 @@ class PagedKVCache:
     def attend(self, layer: int, q, rows, softmax_scale: float | None = None, o=None, lse=None):
         """Attention of one new token per sequence: q [n, Hq, 128] (rows may be strided), query i over all
         cached tokens of sequence row rows[i].  Returns (o [n, Hq, 128], lse [n, Hq] float32); an empty row
-        gives zeros and -inf."""
+        gives zeros and -inf.
+
+        For generation: there is no backward pass.  One through a new o, for a q that requires a gradient, raises
+        RuntimeError, as a q with a forward-mode derivative does; given outputs hold values only."""
+        if (q.requires_grad and o is None and torch.is_grad_enabled()) or _tangents(q):
+            return _NoBackward.apply(q, "PagedKVCache.attend",
+                                     lambda x: self._attend(layer, x, rows, softmax_scale, o, lse))
+        return self._attend(layer, q, rows, softmax_scale, o, lse)
+
+    def _attend(self, layer, q, rows, softmax_scale, o, lse):
         n = self._entries(rows, "rows")
         if q.dim() != 3:
             raise ValueError("q must be [n, heads, 128]")

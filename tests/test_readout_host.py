@@ -132,3 +132,47 @@ def test_pools_of_one_layer_or_page_may_have_any_stride(calls):
         pools = [torch.zeros(*shape, 2, 16, 128, dtype=BF16) for _ in range(2)]
         pools = [x.as_strided(x.shape, [0 if n == 1 else s for n, s in zip(x.shape, x.stride())]) for x in pools]
         RO.PagedKVCache(*pools, *ints(2, 3, shape[1]))
+
+
+@pytest.mark.parametrize("which", range(3))
+def test_forward_mode_is_refused(calls, which):
+    import torch.autograd.forward_ad as fw
+    q, k, v, cu = fused(dtype=F32)
+    with fw.dual_level():
+        x = [q, k, v]
+        RO.packed_attention(*x, cu)                    # nothing to derive: as outside
+        x[which] = fw.make_dual(x[which], torch.ones_like(x[which]))
+        del calls[:]
+        with pytest.raises(RuntimeError):
+            RO.packed_attention(*x, cu)
+        with torch.no_grad(), pytest.raises(RuntimeError):
+            RO.packed_attention(*x, cu)
+
+
+def cache(Hkv=2):
+    return RO.PagedKVCache(*(torch.zeros(2, 6, Hkv, 16, 128, dtype=BF16) for _ in range(2)), *ints(2, 3, 6))
+
+
+def test_attend_has_no_backward(calls):
+    """A q that requires a gradient: values as ever, and an error where a gradient would be left out."""
+    import torch.autograd.forward_ad as fw
+    c, rows = cache(), torch.zeros(1, dtype=torch.int32)
+    q = torch.randn(1, 4, 128, dtype=BF16)
+    o, lse = c.attend(0, q, rows)
+    assert not o.requires_grad and not lse.requires_grad
+    q.requires_grad_()
+    for grad in (True, False):
+        with torch.set_grad_enabled(grad):
+            o, lse = c.attend(0, q, rows)
+        assert o.requires_grad == grad and not lse.requires_grad
+        assert calls[-1][1][6] == q.data_ptr()
+    o, _ = c.attend(0, q, rows)
+    with pytest.raises(RuntimeError, match="no backward pass"):
+        o.float().sum().backward()
+    assert q.grad is None
+    out, lse = torch.zeros(1, 4, 128, dtype=BF16), torch.zeros(1, 4)
+    for _ in range(3):
+        a, b = c.attend(0, q, rows, o=out, lse=lse)
+        assert a is out and b is lse and not a.requires_grad
+    with fw.dual_level(), pytest.raises(RuntimeError):
+        c.attend(0, fw.make_dual(q.detach(), torch.ones_like(q)), rows)
