@@ -57,7 +57,8 @@ def _tdtype(cfg) -> torch.dtype:
 
 def new_workspace(cfg, device) -> torch.Tensor:
     """Zero-initialised workspace (the leading status word must start at 0)."""
-    return torch.zeros(C.workspace_size(cfg), dtype=torch.uint8, device=device)
+    size = C.packed_workspace_size if isinstance(cfg, C.PackedConfig) else C.workspace_size
+    return torch.zeros(size(cfg), dtype=torch.uint8, device=device)
 
 
 def build_summaries(cfg, k_hist, group_sum=None, chunk_sum=None, workspace=None):

@@ -142,8 +142,8 @@ def _with_flags(cfg, flags: int):
 
 def packed_attn_fwd(cfg, q, k, v, cu_seqlens, o=None, lse=None, workspace=None, o_lo=None):
     """Forward, for a cfg of these tensors' shapes and strides (checked).  Rows of no sequence are left as they
-    were in a given o / lse, and hold zeros / -inf in a new one.  o_lo: an output like o for a backward pass in bfloat16, what rounding took from o.  workspace: at least
-    ``_capi.packed_workspace_size(cfg)`` bytes, zeroed once (``read_status`` tells of a cu_seqlens that is not
+    were in a given o / lse, and hold zeros / -inf in a new one.  o_lo: an output like o for a backward pass in bfloat16, what rounding took from o.  workspace: ``new_workspace(cfg, device)``,
+    zeroed once (``read_status`` tells of a cu_seqlens that is not
     valid); without one the call makes its own."""
     _check_packed(cfg, q, k, v, cu_seqlens)
     return _fwd(cfg, q, k, v, cu_seqlens, o, lse, workspace, o_lo)
@@ -203,13 +203,17 @@ def _bwd(cfg, q, k, v, cu_seqlens, o, lse, d_o, dq=None, dk=None, dv=None, works
 _NEW = C.HGA_PACKED_FILL_TAIL | C.HGA_PACKED_CLEAR_STATUS      # of calls with outputs and workspace of their own
 
 
+def _new_flags(workspace) -> int:
+    return _NEW if workspace is None else C.HGA_PACKED_FILL_TAIL      # (a given workspace keeps its status)
+
+
 class _PackedAttention(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, q, k, v, cu_seqlens, softmax_scale):
-        cfg = make_packed_config(q, k, v, cu_seqlens, softmax_scale, _NEW)
+    def forward(ctx, q, k, v, cu_seqlens, softmax_scale, workspace):
+        cfg = make_packed_config(q, k, v, cu_seqlens, softmax_scale, _new_flags(workspace))
         o_lo = _like(q, (cfg.total, cfg.Hq, _D)) if cfg.dtype == C.HGA_BF16 else None
-        o, lse = _fwd(cfg, q, k, v, cu_seqlens, o_lo=o_lo)
-        ctx.softmax_scale = softmax_scale
+        o, lse = _fwd(cfg, q, k, v, cu_seqlens, workspace=workspace, o_lo=o_lo)
+        ctx.softmax_scale, ctx.workspace = softmax_scale, workspace
         ctx.save_for_backward(q, k, v, cu_seqlens, o, lse, o_lo)
         ctx.mark_non_differentiable(lse)
         ctx.set_materialize_grads(False)
@@ -219,15 +223,15 @@ class _PackedAttention(torch.autograd.Function):
     @torch.autograd.function.once_differentiable
     def backward(ctx, d_o, _dlse):
         if d_o is None:
-            return None, None, None, None, None
+            return None, None, None, None, None, None
         # saved-tensor hooks may hand back tensors of the same values with other strides (save_on_cpu makes the slices of
         # a fused projection dense): the configuration describes what is here, not what the forward had
         q, k, v, cu_seqlens, o, lse, o_lo = ctx.saved_tensors
-        cfg = make_packed_config(q, k, v, cu_seqlens, ctx.softmax_scale, _NEW)
+        cfg = make_packed_config(q, k, v, cu_seqlens, ctx.softmax_scale, _new_flags(ctx.workspace))
         o, lse, d_o = _dense(o), _dense(lse), _dense(d_o)
         o_lo = None if o_lo is None else _dense(o_lo)
-        dq, dk, dv = _bwd(cfg, q, k, v, cu_seqlens, o, lse, d_o, o_lo=o_lo)
-        return dq, dk, dv, None, None
+        dq, dk, dv = _bwd(cfg, q, k, v, cu_seqlens, o, lse, d_o, workspace=ctx.workspace, o_lo=o_lo)
+        return dq, dk, dv, None, None, None
 
 
 def _check_accumulators(node, dev: int) -> None:
@@ -266,7 +270,7 @@ class _NoBackward(torch.autograd.Function):
         raise RuntimeError(f"{ctx.name} has no backward pass")
 
 
-def packed_attention(q, k, v, cu_seqlens, softmax_scale: float | None = None):
+def packed_attention(q, k, v, cu_seqlens, softmax_scale: float | None = None, workspace=None):
     """Causal attention over packed sequences: rows cu_seqlens[s] .. cu_seqlens[s+1] - 1 of q [total, Hq,
     128], k, v [total, Hkv, 128] are sequence s (int32, on the device, from 0, not decreasing, at most
     total).  Returns (o [total, Hq, 128], lse [Hq, total] float32); o is differentiable in q, k and v, backward
@@ -276,14 +280,20 @@ def packed_attention(q, k, v, cu_seqlens, softmax_scale: float | None = None):
     q, k and v may be strided (slices of a fused projection, transposed head-major tensors); float32 or
     bfloat16.
 
+    A cu_seqlens that is not valid gives zeros, -inf and zero gradients; after a device-side wait that expired, rows
+    that were not finished hold anything.  Which of the two happened, if any, ``read_status(workspace)`` tells of a
+    workspace that the caller gives (``new_workspace`` of a ``make_packed_config``, or larger): forward and backward
+    record there and never clear it.  Calls that may overlap in time need one each.  Without one it goes unseen.
+
     Forward and backward can be captured into a CUDA graph.  Where q, k or v is a leaf, no autograd graph of it
     that an earlier call on the default stream made may be alive then: autograd would make that stream wait
     for the captured one, which the capture does not allow.  Such a call is refused (RuntimeError)."""
     if (torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad)) or _tangents(q, k, v):
-        out = _PackedAttention.apply(q, k, v, cu_seqlens, softmax_scale)
+        out = _PackedAttention.apply(q, k, v, cu_seqlens, softmax_scale, workspace)
         _check_accumulators(out[0].grad_fn, q.get_device())
         return out
-    return _fwd(make_packed_config(q, k, v, cu_seqlens, softmax_scale, _NEW), q, k, v, cu_seqlens)
+    return _fwd(make_packed_config(q, k, v, cu_seqlens, softmax_scale, _new_flags(workspace)), q, k, v, cu_seqlens,
+                workspace=workspace)
 
 
 class PagedKVCache:

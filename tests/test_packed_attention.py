@@ -543,3 +543,30 @@ def test_largest_numbers_of_the_type(hga, dtype, at):
     if dtype == F32:
         for n in ("dk", "dv"):
             assert torch.equal(got[n], clean[n]), n
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("n_seqs", [3, 40])
+def test_status_of_packed_attention(hga, dtype, n_seqs):
+    """With a workspace of the caller's, what forward and backward record can be read, and the results are the same."""
+    lens = [9] * n_seqs
+    q, k, v, d_o = make(lens, 4, 2, dtype)
+    cu = ends(lens)
+    want = run(hga, q, k, v, d_o, cu)
+    ws = hga.new_workspace(hga.make_packed_config(q, k, v, cu), "cuda")
+    leaves = [x.detach().requires_grad_() for x in (q, k, v)]
+    o, lse = hga.packed_attention(*leaves, cu, workspace=ws)
+    assert hga.read_status(ws) == 0 and torch.equal(o, want["o"]) and torch.equal(lse, want["lse"])
+    for g, n in zip(torch.autograd.grad(o, leaves, d_o, retain_graph=True), ("dq", "dk", "dv")):
+        assert torch.equal(g, want[n])
+    assert hga.read_status(ws) == 0
+    bad = cu.clone()
+    bad[-1] += 1
+    for x in (q, leaves[0]):                           # without and with a graph
+        o, lse = hga.packed_attention(x, k, v, bad, workspace=ws)
+        hga.packed_attention(q, k, v, cu, workspace=ws)      # (a later call clears nothing)
+        assert hga.read_status(ws) == hga._capi.HGA_ERR_ARG
+        assert not o.any() and (lse == -math.inf).all()
+    dq, = torch.autograd.grad(o, leaves[:1], d_o)
+    assert hga.read_status(ws) == hga._capi.HGA_ERR_ARG and not dq.any()
+    assert hga.read_status(ws) == 0

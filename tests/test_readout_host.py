@@ -176,3 +176,22 @@ def test_attend_has_no_backward(calls):
         assert a is out and b is lse and not a.requires_grad
     with fw.dual_level(), pytest.raises(RuntimeError):
         c.attend(0, fw.make_dual(q.detach(), torch.ones_like(q)), rows)
+
+
+@pytest.mark.parametrize("given", [False, True])
+@pytest.mark.parametrize("grad", [False, True])
+def test_workspace_of_packed_attention(calls, given, grad):
+    """A given workspace goes to forward and backward and is never cleared; without one each call has its own, cleared."""
+    from hierarchical_kv_routing_tok_b200 import new_workspace
+    x = [t.detach().requires_grad_(grad) for t in fused()[:3]]
+    cu = fused()[3]
+    ws = new_workspace(RO.make_packed_config(*x, cu), "cpu") if given else None
+    o, _ = RO.packed_attention(*x, cu, workspace=ws)
+    if grad:
+        torch.autograd.grad(o, x, torch.ones_like(o))
+    assert len(calls) == 1 + grad
+    for _, args in calls:
+        assert args[0].flags == C.HGA_PACKED_FILL_TAIL | (0 if given else C.HGA_PACKED_CLEAR_STATUS)
+        assert not given or args[-1] == ws.data_ptr()
+    with pytest.raises(ValueError):
+        RO.packed_attention(*x, cu, workspace=torch.zeros(16, dtype=torch.uint8))
