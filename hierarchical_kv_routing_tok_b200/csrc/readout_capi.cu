@@ -31,7 +31,7 @@ int from_cuda(cudaError_t e) { return e == cudaSuccess ? HGA_OK : HGA_ERR_CUDA; 
 uint64_t wait_limit(int64_t ns) { return ns > 0 ? (uint64_t)ns : 2000000000ull; }
 int elem_bytes(int dtype) { return dtype == HGA_BF16 ? 2 : 4; }
 size_t round256(size_t x) { return (x + 255) & ~(size_t)255; }
-bool bad_scale(float s) { return !(s >= 0.f) || isinf(s); }
+bool bad_scale(float s) { return !(s >= 0.f) || isinf(s * 1.4426950408889634f); }      // (the kernels take scale * log2(e))
 float eff_scale(float s) { return s > 0.f ? s : 1.0f / sqrtf((float)hga::kD); }
 
 // A stride of an outer dimension: 0 stands for the contiguous one; else whole 16-byte pieces, at

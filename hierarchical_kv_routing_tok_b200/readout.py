@@ -9,6 +9,8 @@ needs no host synchronisation and can be captured into a CUDA graph.  Every comp
 """
 from __future__ import annotations
 
+import ctypes
+
 import torch
 import torch.autograd.forward_ad as forward_ad
 
@@ -78,8 +80,8 @@ def _scale(softmax_scale: float | None) -> float:
     """For the library, to which 0 means 1 / sqrt(128)."""
     if softmax_scale is None:
         return 0.0
-    if not softmax_scale > 0:
-        raise ValueError(f"softmax_scale must be positive, got {softmax_scale}")
+    if not ctypes.c_float(softmax_scale).value > 0:        # (1e-50 would be 0)
+        raise ValueError(f"softmax_scale must be positive (a float32), got {softmax_scale}")
     return float(softmax_scale)
 
 

@@ -195,3 +195,18 @@ def test_workspace_of_packed_attention(calls, given, grad):
         assert not given or args[-1] == ws.data_ptr()
     with pytest.raises(ValueError):
         RO.packed_attention(*x, cu, workspace=torch.zeros(16, dtype=torch.uint8))
+
+
+@pytest.mark.parametrize("scale", [0, 0.0, -1.0, float("nan"), 1e-50, -1e-50, 1e-46, float("inf"), 1e39, 3e38])
+def test_scales_that_float32_cannot_hold_are_refused(calls, scale):
+    """0 means the default to the library: no other number may become it."""
+    q, k, v, cu = fused()
+    c = cache()
+    with pytest.raises((ValueError, C.HGAError)):
+        RO.packed_attention(q, k, v, cu, softmax_scale=scale)
+    del calls[:]
+    with pytest.raises((ValueError, C.HGAError)):
+        c.attend(0, q[:1].contiguous(), torch.zeros(1, dtype=torch.int32), softmax_scale=scale)
+        C.paged_attn(*calls[0][1])                     # (the library's own check, before any launch)
+    c.attend(0, q[:1].contiguous(), torch.zeros(1, dtype=torch.int32), softmax_scale=1e-44)
+    assert calls[-1][1][4] > 0
