@@ -190,6 +190,10 @@ __global__ void __launch_bounds__(kWriteThreads) write_kernel(const Cache c, con
     }
     dst[threadIdx.x] = to;
   }
+  // rows that the list promises and no thread finds (it decreases, or ends past the rows there are) are recorded by one CTA
+  if (blockIdx.x == 0)
+    for (int i = threadIdx.x; i <= a.n; i += kWriteThreads)
+      if (a.cu_new[i] < (i ? a.cu_new[i - 1] : 0) || a.cu_new[i] > a.total) set_status(c.status, kErrArg);
   __syncthreads();
   const int vecs = kD * c.elem / 16;     // 16-byte pieces of a row
   const int per_token = c.Hkv * vecs;

@@ -472,7 +472,9 @@ HGA_API int hga_pages_reserve(const hga_pages_config_t* cfg, int32_t n, const in
 /* Writes new K/V rows of one layer into their pages: packed rows k_new, v_new [total, Hkv, D]
  * (strides as in hga_packed_config), of which rows cu_new[i] .. cu_new[i+1] - 1 become the tokens
  * pos[i] .. of sequence row rows[i].  Entries with pos < 0 are left out.  A token outside its
- * sequence's length or with a page outside the pool is left out and HGA_ERR_ARG recorded. */
+ * sequence's length or with a page outside the pool, or that a cu_new which decreases or passes
+ * [0, total] leaves without a row, is left out and HGA_ERR_ARG recorded; the others are written.
+ * With total = 0 nothing is launched, nor checked on the device. */
 HGA_API int hga_pages_write(const hga_pages_config_t* cfg, int32_t layer, int32_t n, const int32_t* rows,
                             const int32_t* pos, const int32_t* cu_new, int64_t total, const void* k_new,
                             int64_t k_stride_t, int64_t k_stride_h, const void* v_new, int64_t v_stride_t,

@@ -600,3 +600,23 @@ def test_copy_pages_from_two_threads(hga):
     torch.cuda.synchronize()
     assert not errors
     assert [c.status() for c in caches] == [0, 0]
+
+
+@pytest.mark.parametrize("cu", [[0, 3, 9], [0, 5, 3, 6], [2, 1, 6], [0, 7], [-1, 6]], ids=str)
+def test_write_with_bounds_of_rows_that_are_not_there(hga, cu):
+    """Bounds that decrease or pass the rows: recorded, and no byte outside the rows' reserved places is touched."""
+    n = len(cu) - 1
+    cache, _ = filled(hga, [0] * n + [40], 16, 2, BF16, spare=2 * n, room=2)
+    rows = i32(list(range(n)))
+    pos = cache.reserve(rows, i32([20] * n))
+    assert cache.status() == 0
+    own = {p for r in range(n) for p in cache.page_table[r, :2].tolist()}
+    others = [p for p in range(cache.cfg.n_pages) if p not in own]
+    before = cache.k_pool[:, others].clone()
+    x = torch.ones(6, 2, 128, device="cuda", dtype=BF16)
+    cache.write(0, x, x, i32(cu), rows, pos)
+    assert cache.status() == hga._capi.HGA_ERR_ARG
+    assert torch.equal(cache.k_pool[:, others].view(torch.int16), before.view(torch.int16))
+    cache.write(0, x, x, i32([0] * n + [6]), rows, pos)
+    cache.write(0, x, x, i32([1] + [4] * n), rows, pos)          # rows before the first and behind the last entry's: no one's
+    assert cache.status() == 0
