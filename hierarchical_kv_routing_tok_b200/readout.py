@@ -306,8 +306,11 @@ class PagedKVCache:
     two zero in an empty cache).  ``PagedKVCache.new`` allocates them.
 
     Every call is asynchronous on the current stream; calls on one cache must not overlap in time (they share its
-    workspace).  A call with a bad entry, or with too few free pages,
-    changes nothing and says so in ``status()``: HGA_ERR_ARG or HGA_ERR_PAGES of ``_capi``."""
+    workspace).  ``status()`` tells of what they could not do, as HGA_ERR_ARG or HGA_ERR_PAGES of ``_capi``:
+    ``reserve``, ``fork``, ``free`` and ``copy_pages`` with a bad entry, or with too few free pages, change nothing;
+    ``write`` and ``attend`` leave out the tokens (``attend``: the rows, pages) that a bad entry concerns and do the
+    rest; ``compact`` leaves a page id outside the pool, and a row whose length is not valid, as they are and moves the
+    other pages, so that such a row may name pages that have moved."""
 
     def __init__(self, k_pool, v_pool, page_table, seq_len, ref_count, wait_limit_ns: int = 0):
         if k_pool.dtype not in _DT:

@@ -504,6 +504,8 @@ HGA_API int hga_pages_free(const hga_pages_config_t* cfg, int32_t n, const int32
 
 /* Moves the pages in use to the front of the pool: with n_used pages in use, the i-th free page below
  * n_used takes the content of the i-th used page at or above it, and tables and ref follow.
+ * The tables are not checked before the pages move: an id outside the pool, and a row whose length is
+ * not valid, stay as they are and HGA_ERR_ARG is recorded; the other rows follow.
  * *n_used (device int32) is the number of pages in use: pages at or past it are free. */
 HGA_API int hga_pages_compact(const hga_pages_config_t* cfg, int32_t* table, const int32_t* seq_len, int32_t* ref,
                               void* k_pool, void* v_pool, int32_t* n_used, void* workspace, void* stream);

@@ -620,3 +620,23 @@ def test_write_with_bounds_of_rows_that_are_not_there(hga, cu):
     cache.write(0, x, x, i32([0] * n + [6]), rows, pos)
     cache.write(0, x, x, i32([1] + [4] * n), rows, pos)          # rows before the first and behind the last entry's: no one's
     assert cache.status() == 0
+
+
+def test_compact_with_bad_integers(hga):
+    """Rows that are in order follow their pages, whatever the others hold; what is not in order stays and is recorded."""
+    cache, gen = filled(hga, [100, 200, 40, 90], 16, 2, BF16, spare=30)
+    q = torch.randn(2, 4, 128, generator=gen, device="cuda").to(BF16)
+    rows = i32([0, 3])
+    want, _ = cache.attend(0, q, rows)
+    cache.page_table[1, 2] = 10 ** 6
+    cache.page_table[1, 3] = -4
+    cache.seq_len[2] = -9
+    used = int((cache.ref_count > 0).sum())
+    stale = cache.page_table[2].clone()
+    assert cache.compact().item() == used
+    assert cache.status() == hga._capi.HGA_ERR_ARG
+    assert cache.page_table[1, 2:4].tolist() == [10 ** 6, -4] and cache.seq_len[2].item() == -9
+    assert torch.equal(cache.page_table[2], stale)
+    assert (cache.ref_count[:used] > 0).all() and not cache.ref_count[used:].any()
+    got, _ = cache.attend(0, q, rows)
+    assert cache.status() == 0 and torch.equal(got, want)
