@@ -14,6 +14,9 @@
 // queries of a KV head are the rows of a pair (up to 16: more query heads are further pairs).
 //   bf16: 64 tokens per tile, m16n8k16 products with the queries as rows.  Few rows cannot fill a tcgen05 tile, and the
 //         memory is the limit by far.
+//         P enters its product as the sum of two bf16 numbers, so that nothing but the output is rounded (error of o at 131K
+//         2.25e-3 -> 1.66e-3 of the norm): with up to eight rows the low parts are the tile's empty upper half (no time:
+//         170.9 us with and without); with more they take products of their own (32/2 heads, 2 x 131K: 64.6 -> 65.1 us).
 //         48 ragged sequences, 32/8 heads: 70 us, 5.7 TB/s; two of 131K: 169 us, 6.3 TB/s; one of 513: 9.0 us, latency.
 //   float32: 32 tokens per tile, float32 FMAs: a lane holds four dims; the dot products of eight tokens and four rows
 //         are summed over the lanes together, in 31 shuffles that leave one sum on each lane.  The same 48: 125 us, 6.4 TB/s.
@@ -545,7 +548,7 @@ __global__ void __launch_bounds__(kThreads, 2)
             for (int e = 0; e < 4; ++e)
               if (8 * n8 + 2 * tq + (e & 1) >= nvalid) c[n8][e] = -INFINITY;
         }
-        uint32_t pf[4] = {0u, 0u, 0u, 0u};
+        uint32_t pf[4], pl[4];                         // P: its first parts, its low parts
         float alpha[2] = {1.f, 1.f};
         bool moved = false;
 #pragma unroll
@@ -563,12 +566,19 @@ __global__ void __launch_bounds__(kThreads, 2)
           l[x] = l[x] * alpha[x] + ((p0 + p1) + (p2 + p3));        // of this thread's columns
           pf[x] = pack_bf16(p0, p1);
           pf[2 + x] = pack_bf16(p2, p3);
+          pl[x] = pack_bf16(p0 - __uint_as_float(pf[x] << 16), p1 - __uint_as_float(pf[x] & 0xffff0000u));
+          pl[2 + x] = pack_bf16(p2 - __uint_as_float(pf[2 + x] << 16), p3 - __uint_as_float(pf[2 + x] & 0xffff0000u));
+        }
+        if (RH == 1) {                                 // the low parts take the empty upper half of the tile
+          pf[1] = pl[0];
+          pf[3] = pl[2];
+          alpha[1] = alpha[0];
         }
         if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
           for (int i = 0; i < 16; ++i) {
             o[i][0] *= alpha[0]; o[i][1] *= alpha[0];
-            if (RH == 2) { o[i][2] *= alpha[1]; o[i][3] *= alpha[1]; }
+            o[i][2] *= alpha[1]; o[i][3] *= alpha[1];
           }
         }
         {
@@ -582,6 +592,10 @@ __global__ void __launch_bounds__(kThreads, 2)
             ldsm4t(b, rb + (d >> 2) * R * 128 + ((ch ^ (r & 7)) << 4));
             mma16816(o[2 * d], pf, b[0], b[1]);
             mma16816(o[2 * d + 1], pf, b[2], b[3]);
+            if (RH == 2) {
+              mma16816(o[2 * d], pl, b[0], b[1]);
+              mma16816(o[2 * d + 1], pl, b[2], b[3]);
+            }
           }
         }
       }
@@ -608,7 +622,7 @@ __global__ void __launch_bounds__(kThreads, 2)
 #pragma unroll
       for (int i = 0; i < 16; ++i)                     // (columns permuted by row: no bank conflicts)
         *reinterpret_cast<float2*>(&s.merge[warp][fg][(8 * i + 2 * tq) ^ ((fg & 3) << 3)]) =
-            make_float2(o[i][2 * x], o[i][2 * x + 1]);
+            RH == 1 ? make_float2(o[i][0] + o[i][2], o[i][1] + o[i][3]) : make_float2(o[i][2 * x], o[i][2 * x + 1]);
       consumer_sync();
       sum_warps<T, true>(a, g, s, x, whole, part);
     }

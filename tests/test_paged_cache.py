@@ -640,3 +640,16 @@ def test_compact_with_bad_integers(hga):
     assert (cache.ref_count[:used] > 0).all() and not cache.ref_count[used:].any()
     got, _ = cache.attend(0, q, rows)
     assert cache.status() == 0 and torch.equal(got, want)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(4, 1), (8, 1), (16, 1), (40, 2)])
+def test_attend_rounds_its_output_only(hga, Hq, Hkv):
+    """bf16: p is the sum of two bf16 numbers (rest 2^-17), scores and sums are in float32 (below 1e-5 for these): the error is
+    that of rounding the exact output, 1.6e-3 of the norm, where a p of one number would add as much again."""
+    lens = [1000, 33, 5000, 2]
+    cache, gen = filled(hga, lens, 64, Hkv, BF16, seed=Hq)
+    q = torch.randn(4, Hq, 128, generator=gen, device="cuda").to(BF16)
+    o, _ = cache.attend(0, q, i32([0, 1, 2, 3]))
+    ref = dense(cache, [0, 1, 2, 3], q)["o"]
+    rounding = (ref.to(BF16).double() - ref).norm() / ref.norm()
+    assert (o.double() - ref).norm() / ref.norm() <= rounding + 2e-5
