@@ -252,8 +252,8 @@ _ACCUMULATE = "torch::autograd::AccumulateGrad"
 
 
 def _tangents(*tensors) -> bool:
-    """Whether one of them carries a forward-mode derivative, which only an autograd function refuses."""
-    return forward_ad._current_level >= 0 and any(forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+    """Within a level of forward-mode derivatives: whether one of them carries one, which only an autograd function refuses."""
+    return any(forward_ad.unpack_dual(t).tangent is not None for t in tensors)
 
 
 class _NoBackward(torch.autograd.Function):
@@ -288,9 +288,11 @@ def packed_attention(q, k, v, cu_seqlens, softmax_scale: float | None = None, wo
     record there and never clear it.  Calls that may overlap in time need one each.  Without one it goes unseen.
 
     Forward and backward can be captured into a CUDA graph.  Where q, k or v is a leaf, no autograd graph of it
-    that an earlier call on the default stream made may be alive then: autograd would make that stream wait
-    for the captured one, which the capture does not allow.  Such a call is refused (RuntimeError)."""
-    if (torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad)) or _tangents(q, k, v):
+    that was made on the default stream may be alive then: autograd would make that stream wait for the captured
+    one, which the capture does not allow.  Where an earlier call of packed_attention made it, the call is refused
+    (RuntimeError); graphs that other operations made of the leaf are not seen here."""
+    if (torch.is_grad_enabled() and (q.requires_grad or k.requires_grad or v.requires_grad)) \
+            or (forward_ad._current_level >= 0 and _tangents(q, k, v)):
         out = _PackedAttention.apply(q, k, v, cu_seqlens, softmax_scale, workspace)
         _check_accumulators(out[0].grad_fn, q.get_device())
         return out
@@ -401,7 +403,8 @@ class PagedKVCache:
 
         For generation: there is no backward pass.  One through a new o, for a q that requires a gradient, raises
         RuntimeError, as a q with a forward-mode derivative does; given outputs hold values only."""
-        if (q.requires_grad and o is None and torch.is_grad_enabled()) or _tangents(q):
+        if (q.requires_grad and o is None and torch.is_grad_enabled()) \
+                or (forward_ad._current_level >= 0 and _tangents(q)):
             return _NoBackward.apply(q, "PagedKVCache.attend",
                                      lambda x: self._attend(layer, x, rows, softmax_scale, o, lse))
         return self._attend(layer, q, rows, softmax_scale, o, lse)
