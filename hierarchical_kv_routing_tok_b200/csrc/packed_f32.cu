@@ -641,8 +641,8 @@ constexpr size_t kTileBytesF = kTileFloats * sizeof(float);
 }  // namespace
 
 // Whether 64-row tiles leave SMs without work (units: heads of one tile): then tiles of 32.  Forward + backward, 975 tokens
-// in five sequences, 4/1 heads: 73 + 228 us with 64 rows, 47 + 138 with 32; 4096 tokens, 32/8 heads: 2778 + 9356 us against
-// 3429 + 10778 (each tile's keys serve half as many rows).
+// in five sequences, 4/1 heads: 72 + 219 us with 64 rows, 41 + 126 with 32; 4096 tokens, 32/8 heads: 2746 + 8985 us against
+// 3247 + 9885 (each tile's keys serve half as many rows).
 int f32_tile(int64_t total, int n_seqs, int units) {
   int dev = 0, sms = 148;
   if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
@@ -681,7 +681,10 @@ cudaError_t launch_bwd_f32(const void* q, const void* k, const void* v, const vo
   e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  int cs = 1;                              // the largest split of the heads into a portable cluster
+  // The largest split of the heads into a portable cluster, while there are fewer key tiles than SMs.  Whole backward pass with
+  // one CTA per key tile and with the split: the tiny batch above 322 and 126 us (4/1 heads: four CTAs), 300 tokens 8/1 heads
+  // 278 and 65 (eight), 1000 tokens 6/1 heads 682 and 186 (six), 512 tokens 32/8 heads 448 and 201 (four).
+  int cs = 1;
   if (nk < sms)
     for (int c = 2; c <= 8; ++c)
       if (p.G % c == 0) cs = c;

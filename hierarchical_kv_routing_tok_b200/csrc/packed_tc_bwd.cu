@@ -6,8 +6,8 @@
 // Two kernels, each owning its outputs (no atomics on sums): dQ over query tiles, which also forms delta, then
 // dK/dV over key tiles.  Both recompute P, so the pair does seven products where five would do.  Bound by the
 // tensor pipe and the element-wise work between the products (exp, two fused multiply-adds, two packings per
-// score): 16,373 tokens in eleven sequences, 32/8 heads, 2.15 ms, 815 TFLOP/s of the formulas' products; tensor pipe active
-// for 60 % of the cycles.
+// score): 16,373 tokens in eleven sequences, 32/8 heads, 2.15 ms over ten passes,
+// 815 TFLOP/s of the formulas' products (a long run is at the power limit); tensor pipe active for 60 % of the cycles.
 //
 // Rows outside a sequence are in its last tiles (they belong to its neighbours): they are masked where they
 // are rows or columns of S, and zeroed in shared memory where they are summed over (a masked 0 times a value

@@ -4,8 +4,8 @@
 // with the online softmax: running maximum m and sum l per row, o rescaled when m grows by more than 2^8.
 //
 // Bound by the tensor pipe (two 128 x 128 x 128 products per tile) and, about as much, by the exponentials
-// (16 per clock and SM): one sequence of 16K tokens, 32/8 heads, 1.82 ms, 1200 TFLOP/s of the formula's products; tensor pipe
-// active for 55 % of the cycles.  A unit is two query tiles of 128 rows (packed_tc.cuh) that share their K/V tiles of
+// (16 per clock and SM): one sequence of 16K tokens, 32/8 heads, 1.81 ms over ten passes, 1210 TFLOP/s of
+// the formula's products (in a long run, at the power limit, 2.11 ms and 1040); tensor pipe active for 55 % of the cycles.  A unit is two query tiles of 128 rows (packed_tc.cuh) that share their K/V tiles of
 // 128 keys.  One CTA per SM walks the units of the work list, heaviest first; barriers and rings count tiles
 // across units, so the next unit's loads and first products run under the epilogue of the current one.
 // Warps: 16 loads (TMA; a ring of two items, V(j) with K(j+1), so that the issuing warp waits once for both), 17 issues the

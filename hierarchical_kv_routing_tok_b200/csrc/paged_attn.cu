@@ -17,7 +17,7 @@
 //         P enters its product as the sum of two bf16 numbers, so that nothing but the output is rounded (error of o at 131K
 //         2.25e-3 -> 1.66e-3 of the norm): with up to eight rows the low parts are the tile's empty upper half (no time:
 //         170.9 us with and without); with more they take products of their own (32/2 heads, 2 x 131K: 64.6 -> 65.1 us).
-//         48 ragged sequences, 32/8 heads: 70 us, 5.7 TB/s; two of 131K: 169 us, 6.3 TB/s; one of 513: 9.0 us, latency.
+//         48 ragged sequences, 32/8 heads: 70 us, 5.7 TB/s; two of 131K: 169 us, 6.3 TB/s; one of 513: 9.3 us, latency.
 //   float32: 32 tokens per tile, float32 FMAs: a lane holds four dims; the dot products of eight tokens and four rows
 //         are summed over the lanes together, in 31 shuffles that leave one sum on each lane.  The same 48: 125 us, 6.4 TB/s.
 #include <cuda.h>
@@ -39,8 +39,14 @@ constexpr int kThreads = kConsumers + 32;
 constexpr int kStages = 3;
 constexpr uint32_t kTileBytes = 16384; // of K, and of V
 constexpr int kWindow = 32;            // queries whose row and length are kept in shared memory
-// What a pair's start and end cost, in tiles.  Batch of 48 ragged requests, 32/8 heads: 78.8 us with 0, 72.7 with 1, 69.8
-// with 3, 70.2 with 4; 32/4 heads: 50.8, 46.0, 43.1, 42.9; equal lengths: 70 us with any.
+// What a pair's start and end cost, in tiles: us with 0, 1, 3 and 6.
+//                              bf16                          float32
+//   48 ragged, 8/8 heads       74.5  70.4  69.0  68.7        130.6  123.7  123.9  125.2
+//   48 ragged, 32/8            79.9  74.3  69.8  69.9        132.7  125.6  125.9  125.2
+//   48 ragged, 16/1            26.6  25.4  23.2  23.4        117.2  107.1  107.9  114.3
+//   64 of 200 to 600, 32/8     32.5  31.4  30.6  30.8         46.8   45.4   46.0   47.2
+//   64 of 200 to 600, 32/2     18.6  18.3  16.0  16.5         70.8   70.7   76.2   84.3
+// Equal lengths: any.  One number for both: float32 would gain up to 8 % from 1 with wide groups, nothing with others.
 constexpr int kPairCost = 3;
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr int kErrArg = -1;
@@ -463,8 +469,8 @@ __device__ __forceinline__ void produce(const Args& a, Smem& s, const CUtensorMa
 }
 
 // ------------------------------------------------------------------------------------ bf16, tensor cores
-// RH: 1 when a pair has at most 8 query rows (the upper half of the m16 tile is empty), else 2.  One sequence of 513 tokens,
-// 32/8 heads: 9.2 us with 1, 9.5 with 2; long ones the same.
+// RH: 1 when a pair has at most 8 query rows (the upper half of the m16 tile is free for the low parts of P), else 2.  One
+// sequence of 513 tokens, 32/8 heads: 9.3 us with 1, 9.6 with 2; eight of 1000: 14.8 and 15.4; long ones the same.
 template <int RH>
 __global__ void __launch_bounds__(kThreads, 2)
     paged_bf16_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v, const Args a) {

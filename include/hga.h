@@ -393,14 +393,14 @@ HGA_API int hga_route_groups_cached(const hga_config_t* cfg, const float* qb, co
  * not decreasing, at most total; if it is not, no sequence is computed (all rows count as rows of
  * no sequence) and HGA_ERR_ARG is recorded in the workspace status word.
  * Products accumulate in float32.  bf16: probabilities and dS are rounded to bf16 before their second
- * product (of dS in dQ, what that takes is added back where it counts most).  float32: each operand as the sum of two tf32 numbers, which keeps float32 accuracy (the
- * scores of a q or k row that is not finite are NaN).
+ * product (of dS in dQ, what that takes is added back where it counts most).  float32: each operand as the sum of
+ * two tf32 numbers, which keeps float32 accuracy (the scores of a q or k row that is not finite are NaN).
  * Sums are formed before their last factor (1 / sum p for o, the scale for dq and dk) and overflow where they pass the
  * largest float32: in bf16, whose p is relative to a maximum up to 2^8 too small, for values of v from 2^120 / (attended
  * tokens) on.
  * total <= 2^31 - 1 - 256 and (total / 16 + n_seqs) * Hq < 2^31; total = 0 or n_seqs = 0 is a valid
  * empty problem.
- * Two calls that may overlap in time need two workspaces. */
+ * No output overlaps an input or another output.  Two calls that may overlap in time need two workspaces. */
 enum hga_packed_flags {
   HGA_PACKED_FILL_TAIL = 1,   /* rows of no sequence: o, dq, dk, dv zeros, lse -inf */
   HGA_PACKED_CLEAR_STATUS = 2 /* clear the status word first: a workspace need not be zeroed */
