@@ -16,7 +16,7 @@
 //         memory is the limit by far.
 //         P enters its product as the sum of two bf16 numbers, so that nothing but the output is rounded (error of o at 131K
 //         2.25e-3 -> 1.66e-3 of the norm): with up to eight rows the low parts are the tile's empty upper half (no time:
-//         170.9 us with and without); with more they take products of their own (32/2 heads, 2 x 131K: 64.6 -> 65.1 us).
+//         170.4 us with and without); with more they take products of their own (32/2 heads, 2 x 131K: 64.7 -> 65.3 us).
 //         48 ragged sequences, 32/8 heads: 70 us, 5.7 TB/s; two of 131K: 169 us, 6.3 TB/s; one of 513: 9.3 us, latency.
 //   float32: 32 tokens per tile, float32 FMAs: a lane holds four dims; the dot products of eight tokens and four rows
 //         are summed over the lanes together, in 31 shuffles that leave one sum on each lane.  The same 48: 125 us, 6.4 TB/s.
@@ -342,6 +342,14 @@ __device__ __forceinline__ void sum_warps(const Args& a, const Segment& g, const
   }
 }
 
+// p = first part (cut to bf16) + rest.  The rest is never 0 nor negative (2^-126 is far below any sum's rounding): both products
+// with an infinite v then have its sign, where 0 or a change of sign would make their sum NaN.
+__device__ __forceinline__ uint32_t first_parts(float p0, float p1) {
+  return __byte_perm(__float_as_uint(p0), __float_as_uint(p1), 0x7632);
+}
+__device__ __forceinline__ float rest(float p) {
+  return fmaxf(p - __uint_as_float(__float_as_uint(p) & 0xffff0000u), 1.17549435e-38f);
+}
 __device__ __forceinline__ void ldsm4(uint32_t (&r)[4], uint32_t addr) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]) : "r"(addr) : "memory");
@@ -570,10 +578,10 @@ __global__ void __launch_bounds__(kThreads, 2)
           const float p0 = ex2(fmaf(c[0][2 * x], a.c2, -ref)), p1 = ex2(fmaf(c[0][2 * x + 1], a.c2, -ref));
           const float p2 = ex2(fmaf(c[1][2 * x], a.c2, -ref)), p3 = ex2(fmaf(c[1][2 * x + 1], a.c2, -ref));
           l[x] = l[x] * alpha[x] + ((p0 + p1) + (p2 + p3));        // of this thread's columns
-          pf[x] = pack_bf16(p0, p1);
-          pf[2 + x] = pack_bf16(p2, p3);
-          pl[x] = pack_bf16(p0 - __uint_as_float(pf[x] << 16), p1 - __uint_as_float(pf[x] & 0xffff0000u));
-          pl[2 + x] = pack_bf16(p2 - __uint_as_float(pf[2 + x] << 16), p3 - __uint_as_float(pf[2 + x] & 0xffff0000u));
+          pf[x] = first_parts(p0, p1);
+          pf[2 + x] = first_parts(p2, p3);
+          pl[x] = pack_bf16(rest(p0), rest(p1));
+          pl[2 + x] = pack_bf16(rest(p2), rest(p3));
         }
         if (RH == 1) {                                 // the low parts take the empty upper half of the tile
           pf[1] = pl[0];

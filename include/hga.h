@@ -394,7 +394,8 @@ HGA_API int hga_route_groups_cached(const hga_config_t* cfg, const float* qb, co
  * no sequence) and HGA_ERR_ARG is recorded in the workspace status word.
  * Products accumulate in float32.  bf16: probabilities and dS are rounded to bf16 before their second
  * product (of dS in dQ, what that takes is added back where it counts most).  float32: each operand as the sum of
- * two tf32 numbers, which keeps float32 accuracy (the scores of a q or k row that is not finite are NaN).
+ * two tf32 numbers, which keeps float32 accuracy (the scores of a q or k row that is not finite are NaN
+ * or infinite).
  * Sums are formed before their last factor (1 / sum p for o, the scale for dq and dk) and overflow where they pass the
  * largest float32: in bf16, whose p is relative to a maximum up to 2^8 too small, for values of v from 2^120 / (attended
  * tokens) on.

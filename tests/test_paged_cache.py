@@ -644,7 +644,7 @@ def test_compact_with_bad_integers(hga):
 
 @pytest.mark.parametrize("Hq,Hkv", [(4, 1), (8, 1), (16, 1), (40, 2)])
 def test_attend_rounds_its_output_only(hga, Hq, Hkv):
-    """bf16: p is the sum of two bf16 numbers (rest 2^-17), scores and sums are in float32 (below 1e-5 for these): the error is
+    """bf16: p is the sum of two bf16 numbers (of which what is left is 2^-16 at most), scores and sums are in float32 (below 1e-5 for these): the error is
     that of rounding the exact output, 1.6e-3 of the norm, where a p of one number would add as much again."""
     lens = [1000, 33, 5000, 2]
     cache, gen = filled(hga, lens, 64, Hkv, BF16, seed=Hq)
@@ -653,3 +653,26 @@ def test_attend_rounds_its_output_only(hga, Hq, Hkv):
     ref = dense(cache, [0, 1, 2, 3], q)["o"]
     rounding = (ref.to(BF16).double() - ref).norm() / ref.norm()
     assert (o.double() - ref).norm() / ref.norm() <= rounding + 2e-5
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+@pytest.mark.parametrize("Hq,Hkv", [(4, 1), (8, 1), (16, 1), (20, 1), (8, 2)])
+def test_attended_values_that_are_not_finite(hga, dtype, Hq, Hkv):
+    """Infinities and NaN in v of cached tokens: the query heads that attend them get them, with their sign, in their dim, and
+    nothing else changes."""
+    lens = [1, 20, 700, 64]
+    cache, gen = filled(hga, lens, 16, Hkv, dtype, seed=Hq)
+    q = torch.randn(4, Hq, 128, generator=gen, device="cuda").to(dtype)
+    rows = i32([0, 1, 2, 3])
+    clean, lse = cache.attend(0, q, rows)
+    for r, t in ((0, 0), (1, 19), (2, 100), (2, 699)):
+        page = cache.page_table[r, t // 16].long()
+        for d, x in ((5, math.inf), (77, -math.inf), (90, math.nan)):
+            cache.v_pool[0, page, 0, t % 16, d] = x
+    got, lse2 = cache.attend(0, q, rows)
+    assert cache.status() == 0 and torch.equal(lse, lse2)
+    hit = torch.zeros_like(got, dtype=torch.bool)
+    hit[:3, :Hq // Hkv, [5, 77, 90]] = True
+    assert torch.equal(got[~hit], clean[~hit])
+    assert (got[:3, :Hq // Hkv, 5] == math.inf).all() and (got[:3, :Hq // Hkv, 77] == -math.inf).all()
+    assert got[:3, :Hq // Hkv, 90].isnan().all()
