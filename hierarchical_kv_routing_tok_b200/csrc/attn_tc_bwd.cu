@@ -919,6 +919,9 @@ cudaError_t launch_bwd_dq_tc(const void* q, const void* kh, const void* vh, cons
                              void* dq, int B, int Hq, int Hkv, int64_t H, int64_t S, int64_t Hs, int kg, int nsg,
                              float scale, int* status, uint64_t wait_ns, cudaStream_t st) {
   namespace K = tcbwd::dq;
+  const size_t smem = K::Smem::kBytes + 1024;
+  cudaError_t e = set_smem(K::dq_tc_kernel, smem);
+  if (e != cudaSuccess) return e;
   CUtensorMap mq, mdo, mkh, mvh, mks, mvs;
   // with no history the history maps are never used: map the segment instead (maps need rows > 0)
   const void* kh_m = Hs ? kh : ks;
@@ -938,9 +941,6 @@ cudaError_t launch_bwd_dq_tc(const void* q, const void* kh, const void* vh, cons
   if (cudaGetDevice(&dev) != cudaSuccess || cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
     return cudaErrorInvalidValue;
   const int64_t grid = units < sms ? units : sms;
-  const size_t smem = K::Smem::kBytes + 1024;
-  cudaError_t e = cudaFuncSetAttribute(K::dq_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
   e = launch_dependent(K::dq_tc_kernel, dim3((unsigned)grid), dim3(128 + 32 * K::kEWWarps), smem, st, 1, mq, mdo, mkh,
                        mvh, mks, mvs, p);
   if (e != cudaSuccess) return e;
@@ -971,6 +971,9 @@ cudaError_t launch_bwd_dkdv_tc(const void* q, const void* ks, const void* vs, co
                                const float* delta, void* dk, void* dv, float* xchg, int B, int Hq, int Hkv, int64_t S,
                                float scale, int* status, uint64_t wait_ns, cudaStream_t st) {
   namespace K = tcbwd::dkdv;
+  const size_t smem = K::Smem::kBytes + 1024;
+  cudaError_t e = set_smem(K::dkdv_tc_kernel, smem);
+  if (e != cudaSuccess) return e;
   CUtensorMap mq, mdo, mks, mvs, mdk, mdv;
   if (!make_map_bf16_rows(&mq, q, (uint64_t)B * Hq * S, K::BQ) ||
       !make_map_bf16_rows(&mdo, d_o, (uint64_t)B * Hq * S, K::BQ) ||
@@ -984,9 +987,6 @@ cudaError_t launch_bwd_dkdv_tc(const void* q, const void* ks, const void* vs, co
   K::Params p{B, Hq, Hkv, G, cs, G / cs, (int)(S / kQBlock), nkt, S, scale * tcbwd::kLog2e, scale, lse, delta,
               static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv), xchg, status, wait_ns};
   const int64_t grid = (int64_t)B * Hkv * nkt * cs;
-  const size_t smem = K::Smem::kBytes + 1024;
-  cudaError_t e = cudaFuncSetAttribute(K::dkdv_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-  if (e != cudaSuccess) return e;
   e = launch_dependent(K::dkdv_tc_kernel, dim3((unsigned)grid), dim3(640), smem, st, (unsigned)cs, mq, mdo, mks, mvs, mdk,
                        mdv, p);
   if (e != cudaSuccess) return e;

@@ -484,6 +484,11 @@ cudaError_t launch_attn_fwd_tc(const void* q, const void* kh, const void* vh, co
                                const int32_t* gi, void* o, float* lse, int B, int Hq, int Hkv, int64_t H, int64_t S,
                                int64_t Hs, int kg, int nsg, float scale, int* status, uint64_t wait_ns,
                                cudaStream_t st) {
+  const int G = Hq / Hkv;
+  const bool four = G % 4 == 0;            // query heads per CTA: four, else two
+  const size_t smem = (four ? tcfwd::Smem<2>::kBytes : tcfwd::Smem<1>::kBytes) + 1024;
+  cudaError_t e = four ? set_smem(tcfwd::fwd_tc_kernel<2>, smem) : set_smem(tcfwd::fwd_tc_kernel<1>, smem);
+  if (e != cudaSuccess) return e;
   CUtensorMap mq, mkh, mvh, mks, mvs;
   // with no history the history maps are never used: map the segment instead (maps need rows > 0)
   const void* kh_m = Hs ? kh : ks;
@@ -496,22 +501,14 @@ cudaError_t launch_attn_fwd_tc(const void* q, const void* kh, const void* vh, co
       !make_map_bf16_rows(&mks, ks, (uint64_t)B * Hkv * S, tcfwd::BN) ||
       !make_map_bf16_rows(&mvs, vs, (uint64_t)B * Hkv * S, tcfwd::BN))
     return cudaErrorInvalidValue;
-  const int G = Hq / Hkv;
-  tcfwd::Params p{B, Hq, Hkv, G, (G % 4 == 0) ? 4 : 2, kg, (int)(S / kQBlock), nsg, H, S, Hs,
+  tcfwd::Params p{B, Hq, Hkv, G, four ? 4 : 2, kg, (int)(S / kQBlock), nsg, H, S, Hs,
                   scale * 1.4426950408889634f, gi, static_cast<__nv_bfloat16*>(o), lse, status, wait_ns};
   const int64_t grid = (int64_t)B * Hkv * p.nblk * (G / p.hpc);
-  cudaError_t e;
-  if (p.hpc == 4) {
-    const size_t smem = tcfwd::Smem<2>::kBytes + 1024;
-    e = cudaFuncSetAttribute(tcfwd::fwd_tc_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
+  if (four) {
     e = launch_dependent(tcfwd::fwd_tc_kernel<2>, dim3((unsigned)grid), dim3(384), smem, st, 1, mq, mkh, mvh, mks, mvs,
                          mo, p);
     if (e != cudaSuccess) return e;
   } else {
-    const size_t smem = tcfwd::Smem<1>::kBytes + 1024;
-    e = cudaFuncSetAttribute(tcfwd::fwd_tc_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
     e = launch_dependent(tcfwd::fwd_tc_kernel<1>, dim3((unsigned)grid), dim3(256), smem, st, 1, mq, mkh, mvh, mks, mvs,
                          mo, p);
     if (e != cudaSuccess) return e;

@@ -69,6 +69,14 @@ template <> struct Vec16<__nv_bfloat16> {
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// Sets the dynamic shared memory that `kernel` may have.  Before the launch's tensor maps: cuTensorMapEncodeTiled takes the
+// thread's current context, which the runtime makes current at a thread's first call that needs one (this is such a
+// call, cudaGetDevice and cudaDeviceGetAttribute are not).
+template <typename... KArgs>
+inline cudaError_t set_smem(void (*kernel)(KArgs...), size_t bytes) {
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+}
+
 // Launch `kernel` as a dependent of the previous kernel in `st` (programmatic stream
 // serialization), optionally in clusters of `cluster` CTAs.
 template <typename... KArgs, typename... Args>

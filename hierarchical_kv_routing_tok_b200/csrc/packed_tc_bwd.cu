@@ -861,6 +861,10 @@ cudaError_t launch_bwd_tc(const void* q, const void* k, const void* v, const voi
                           const float* lse, const void* d_o, float* stats, void* dq, void* dk, void* dv,
                           const Work& by_query, const Work& by_key, const Problem& p, cudaStream_t st) {
   const int pk = packed_heads(p.G);
+  size_t smem = dq::Smem::kBytes + 1024;
+  auto dq_kernel = by_query.cu ? dq::packed_dq_tc_kernel<true> : dq::packed_dq_tc_kernel<false>;
+  cudaError_t e = set_smem(dq_kernel, smem);
+  if (e != cudaSuccess) return e;
   const Strided so{(int64_t)p.Hq * kD, kD};
   CUtensorMap mq, mdo, mk, mv, mq64, mdo64;
   if (!make_map_packed(&mq, q, p.Hq, p.total, p.q, pk, 128 / pk) ||
@@ -874,12 +878,8 @@ cudaError_t launch_bwd_tc(const void* q, const void* k, const void* v, const voi
               static_cast<__nv_bfloat16*>(dq), static_cast<__nv_bfloat16*>(dk), static_cast<__nv_bfloat16*>(dv),
               by_query, p.fill_tail, p.status, p.wait_ns};
   int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
-  size_t smem = dq::Smem::kBytes + 1024;
-  auto dq_kernel = by_query.cu ? dq::packed_dq_tc_kernel<true> : dq::packed_dq_tc_kernel<false>;
-  e = cudaFuncSetAttribute(dq_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int64_t units = list_capacity(p.total, p.n_seqs, dq_tile(p.G)) * p.Hkv * (p.G / pk);
   e = launch_dependent(dq_kernel, dim3((unsigned)(units < 1 ? 1 : units < sms ? units : sms)),
@@ -888,7 +888,7 @@ cudaError_t launch_bwd_tc(const void* q, const void* k, const void* v, const voi
   a.work = by_key;
   smem = dkdv::Smem::kBytes + 1024;
   auto dkdv_kernel = by_key.cu ? dkdv::packed_dkdv_tc_kernel<true> : dkdv::packed_dkdv_tc_kernel<false>;
-  e = cudaFuncSetAttribute(dkdv_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  e = set_smem(dkdv_kernel, smem);
   if (e != cudaSuccess) return e;
   const int64_t tiles = list_capacity(p.total, p.n_seqs, kKeyTile) * p.Hkv;
   // Two CTAs per unit while there are fewer units than SMs.  Whole backward pass, 32/8 heads: 1024 tokens (64 units) 103 us

@@ -530,6 +530,10 @@ int head_units(int Hkv, int G) { return Hkv * (G / packed_heads(G)); }
 cudaError_t launch_fwd_tc(const void* q, const void* k, const void* v, void* o, void* o_lo, float* lse,
                           const Work& work, const Problem& p, cudaStream_t st) {
   const int pk = packed_heads(p.G);
+  const size_t smem = FwdSmem::kBytes + 1024;
+  auto kernel = work.cu ? packed_fwd_tc_kernel<true> : packed_fwd_tc_kernel<false>;
+  cudaError_t e = set_smem(kernel, smem);
+  if (e != cudaSuccess) return e;
   CUtensorMap mq, mk, mv;
   if (!make_map_packed(&mq, q, p.Hq, p.total, p.q, pk, 128 / pk) || !make_map_packed(&mk, k, p.Hkv, p.total, p.k, 1, kBN) ||
       !make_map_packed(&mv, v, p.Hkv, p.total, p.v, 1, kBN))
@@ -538,12 +542,8 @@ cudaError_t launch_fwd_tc(const void* q, const void* k, const void* v, void* o, 
               static_cast<const __nv_bfloat16*>(v), p.v, static_cast<__nv_bfloat16*>(o), static_cast<__nv_bfloat16*>(o_lo), lse,
               work, p.fill_tail, p.status, p.wait_ns};
   int dev = 0, sms = 0;
-  cudaError_t e = cudaGetDevice(&dev);
+  e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
-  if (e != cudaSuccess) return e;
-  const size_t smem = FwdSmem::kBytes + 1024;
-  auto kernel = work.cu ? packed_fwd_tc_kernel<true> : packed_fwd_tc_kernel<false>;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const int64_t units = list_capacity(p.total, p.n_seqs, fwd_tile(p.G)) * a.hu;
   return launch_dependent(kernel, dim3((unsigned)(units < 1 ? 1 : units < sms ? units : sms)),

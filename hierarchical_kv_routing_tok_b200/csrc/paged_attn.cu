@@ -842,16 +842,16 @@ cudaError_t launch_paged_attn(bool bf16, const Cache& c, int layer, int n, int H
   cudaError_t e = cudaGetDevice(&dev);
   if (e == cudaSuccess) e = cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev);
   if (e != cudaSuccess) return e;
-  CUtensorMap mk, mv;
-  if (!make_pool_map(&mk, static_cast<const char*>(k_pool) + layer * c.layer_bytes, c) ||
-      !make_pool_map(&mv, static_cast<const char*>(v_pool) + layer * c.layer_bytes, c))
-    return cudaErrorInvalidValue;
   auto kernel = bf16       ? (a.G <= 8 ? paged_bf16_kernel<1> : paged_bf16_kernel<2>)
                 : a.G <= 4 ? paged_f32_kernel<1>
                 : a.G <= 8 ? paged_f32_kernel<2>
                            : paged_f32_kernel<4>;
-  e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)sizeof(Smem));
+  e = set_smem(kernel, sizeof(Smem));
   if (e != cudaSuccess) return e;
+  CUtensorMap mk, mv;
+  if (!make_pool_map(&mk, static_cast<const char*>(k_pool) + layer * c.layer_bytes, c) ||
+      !make_pool_map(&mv, static_cast<const char*>(v_pool) + layer * c.layer_bytes, c))
+    return cudaErrorInvalidValue;
   // two CTAs per SM, and no more than there can be units of work
   const int64_t tile = bf16 ? kTileOf<__nv_bfloat16> : kTileOf<float>;
   const int64_t units = (int64_t)n * c.Hkv * a.subs * (((int64_t)c.max_pages * c.page + tile - 1) / tile + kPairCost);
