@@ -14,9 +14,11 @@
 // that is not finite would not be 0).
 //
 // P and dS are rounded to bf16 for their second products, the operand type that takes K, Q and dO as they are: each adds
-// about as much as the rounding of the result (dk, dv: 2.4e-3 and 2.3e-3 of the norm, 1.7e-3 from rounding the exact ones).
-// In dQ, whose norm lies most in a sequence's first tokens, the diagonal tile takes what the rounding left as a further
-// operand: 2.5e-3 -> 2.05e-3, for 2130 -> 2150 us of the packed 16K batch (every tile: 1.8e-3 and 2370).
+// about as much as the rounding of the result (dv: 2.3e-3 of the norm, 1.7e-3 from rounding the exact one).
+// In dQ and dK, whose norms lie most in a sequence's first tokens, the diagonal takes what the rounding left of dS as a
+// further operand.  dQ: 2.5e-3 -> 2.05e-3, for 2130 -> 2150 us of the packed 16K batch (every tile: 1.8e-3 and 2370).  dK:
+// 2.4e-3 -> 2.0e-3, sequences of one tile 2.4e-3 -> 1.75e-3, for 2170 -> 2200 us (twelve short sequences, 32/4 heads: 128 -> 133;
+// one of 3000, 4/1: 158 -> 149, of itself the split of the loop).
 #include <cuda_bf16.h>
 
 #include "packed_tc.cuh"
@@ -563,6 +565,7 @@ __global__ void __launch_bounds__(kThreads, 1)
   auto pass_of = [&](int j) { return (j * cs + rank) / Tq; };
   auto step_of = [&](int j) { return (j * cs + rank) % Tq; };
   const bool ragged = (len - t0) % tq != 0; // a pass's last step holds rows past the sequence
+  const int diag_steps = (BM + tq - 1) / tq;                // a pass's steps that overlap the key tile
 
   if (threadIdx.x == 0) {
     mbar_init(kv_full, 1);
@@ -687,6 +690,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         mma_ts_w(tmem + 384, tmem + b * 128 + 64 + acol, b2[ks], idesc_g, (j > 0 || ks > 0));
       }
     };
+    // dK += (what rounding took from dS)^T Q, in columns 32h+16..32h+31 of the dS^T region
+    auto issue_low = [&](int j, int b) {
+      uint64_t b2[4];
+      mnmajor_from_base<4>(b2, qmn0 + (uint64_t)((j % NS) * (kQTile >> 4)), 2048u >> 4);
+#pragma unroll
+      for (int ks = 0; ks < BQ / 16; ++ks)
+        mma_ts_w(tmem + 384, tmem + b * 128 + 80 + (ks >> 1) * 32 + (ks & 1) * 8, b2[ks], idesc_g, true);
+    };
     uint32_t clean_phase = 0;               // bit s: parity of the next cleaned step in stage s
     auto step_ready = [&](int j) {
       const int s = j % NS;
@@ -703,17 +714,27 @@ __global__ void __launch_bounds__(kThreads, 1)
       ok = step_ready(j);
       if (ok) issue_sd(j, j & 1);
     }
-    for (int j = 0; ok && j < NJ; ++j) {
+    auto step = [&](int j, bool low) {
       const int b = j & 1;
       ok = wait_w(pd_full(b), (j >> 1) & 1, abort_flag, p.status, p.wait_ns);
-      if (!ok) break;
+      if (!ok) return;
       tc_fence_after();
       issue_grad(j, b);
+      if (low) issue_low(j, b);
       mma_commit_w(q_empty(j % NS));
       if (j + 2 < NJ) {
         ok = step_ready(j + 2);
         if (ok) issue_sd(j + 2, b);
       }
+    };
+    // each pass begins with its steps on the diagonal (loops of their own: a condition in one loop cost 5 %)
+    for (int j = 0; ok && j < NJ;) {
+      const int i = step_of(j);
+      const int d1 = min(NJ, j + (max(min(diag_steps, Tq) - i, 0) + cs - 1) / cs);
+      for (; ok && j < d1; ++j) step(j, true);
+      const int i2 = step_of(j);
+      const int e1 = i2 < diag_steps ? j : min(NJ, j + (Tq - i2 + cs - 1) / cs);
+      for (; ok && j < e1; ++j) step(j, false);
     }
     if (ok) mma_commit_w(done);
     mma_commit_w(mma_done);
@@ -729,7 +750,6 @@ __global__ void __launch_bounds__(kThreads, 1)
     const uint32_t tS = tmem + lane_off + b * 128;
     const uint32_t tP = tS + 64;
     const float* stat_base = reinterpret_cast<const float*>(smem + L::kStat);
-    const int diag_steps = (BM + tq - 1) / tq;                // steps that overlap the key tile
     const uint64_t c2 = pair(p.c2, p.c2);
     bool ok = true;
     int i = step_of(b);
@@ -767,10 +787,16 @@ __global__ void __launch_bounds__(kThreads, 1)
           }
           pp[e >> 1] = pack_bf16(p0, p1);
           pd[e >> 1] = pack_bf16(d0, d1);
+          if (masked)                       // (of the dP registers behind e, none is needed any more)
+            dv[e >> 1] = pack_bf16(d0 - __uint_as_float(pd[e >> 1] << 16), d1 - __uint_as_float(pd[e >> 1] & 0xffff0000u));
         }
       };
-      if (__any_sync(0xffffffffu, dfrom > 0)) pairs(true);
-      else pairs(false);
+      if (i < diag_steps) {
+        pairs(true);
+        tmem_st16(tP + 32 * hc + 16, reinterpret_cast<const uint32_t(&)[16]>(dv));
+      } else {
+        pairs(false);
+      }
       // packed bf16 stays inside this warpgroup's own (already read) column range
       tmem_st16(tS + 32 * hc, pp);
       tmem_st16(tP + 32 * hc, pd);
