@@ -13,8 +13,9 @@
 // the causal diagonal p = 0 meets values that the row does not attend, and 0 * inf is not 0.  Values there that are not
 // finite become 0 before the product, and the epilogue adds them to the rows that do attend them.
 // P is rounded to bf16, the type of V, for its product: o is 2.0e-3 of the norm from exact (16K: 2.2e-3), of which rounding
-// o takes 1.6e-3.  (What the rounding took as a further operand on the diagonal: 1.8e-3 (2.0e-3), but 1810 -> 1970 us at 16K
-// and 52 -> 60 at 2048, the softmax warps having no registers for it.)
+// o takes 1.6e-3.  (What the rounding took as a further operand on the diagonal, as in the backward: 1.8e-3 (1.9e-3), but 37
+// tokens 11.7 -> 12.6 us, 2048 tokens 53 -> 57, the packed batch 668 -> 685, 16K 1843 -> 1855 with a loop of its own, and 1970
+// at 16K without: the softmax warps have no registers to spare.)
 // TMEM: S_0 S_1 O_0 O_1 (128 columns each); P_i as bf16 over the first half of S_i.  Issue order S_0 S_1 |
 // PV_0 S_0' PV_1 S_1' | ...: S_i(j+1) complete implies PV_i(j) complete, so no barrier guards the rescale.
 // (Measured slower: S in two buffers of 64 keys, 2406 against 1903 us at 16K, whose products of 64 columns wait for shared
