@@ -6,8 +6,8 @@
 // Two kernels, each owning its outputs (no atomics on sums): dQ over query tiles, which also forms delta, then
 // dK/dV over key tiles.  Both recompute P, so the pair does seven products where five would do.  Bound by the
 // tensor pipe and the element-wise work between the products (exp, two fused multiply-adds, two packings per
-// score): 16,373 tokens in eleven sequences, 32/8 heads, 2.15 ms over ten passes,
-// 815 TFLOP/s of the formulas' products (a long run is at the power limit); tensor pipe active for 60 % of the cycles.
+// score): 16,373 tokens in eleven sequences, 32/8 heads, 2.18 ms over ten passes,
+// 805 TFLOP/s of the formulas' products (a long run is at the power limit); tensor pipe active for 60 % of the cycles.
 //
 // Rows outside a sequence are in its last tiles (they belong to its neighbours): they are masked where they
 // are rows or columns of S, and zeroed in shared memory where they are summed over (a masked 0 times a value
@@ -17,8 +17,8 @@
 // about as much as the rounding of the result (dv: 2.3e-3 of the norm, 1.7e-3 from rounding the exact one).
 // In dQ and dK, whose norms lie most in a sequence's first tokens, the diagonal takes what the rounding left of dS as a
 // further operand.  dQ: 2.5e-3 -> 2.05e-3, for 2130 -> 2150 us of the packed 16K batch (every tile: 1.8e-3 and 2370).  dK:
-// 2.4e-3 -> 2.0e-3, sequences of one tile 2.4e-3 -> 1.75e-3, for 2170 -> 2200 us (twelve short sequences, 32/4 heads: 128 -> 133;
-// one of 3000, 4/1: 158 -> 149, of itself the split of the loop).
+// 2.4e-3 -> 2.0e-3, sequences of one tile 2.4e-3 -> 1.75e-3, for 2165 -> 2177 us (twelve short sequences, 32/4 heads: 127 -> 133;
+// one of 3000, 4/1: 158 -> 147, which is the split of the loop).
 #include <cuda_bf16.h>
 
 #include "packed_tc.cuh"
