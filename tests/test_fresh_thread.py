@@ -122,3 +122,46 @@ for g in torch.autograd.grad(o, (q, k, v), torch.randn_like(o)):
 """
     subprocess.run([sys.executable, "-c", code], check=True, timeout=300,
                    cwd=os.path.dirname(os.path.dirname(os.path.abspath(__file__))))
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16])
+def test_two_threads_at_once(hga, dtype):
+    """Forward, backward and decoding from two threads, each with its own stream, tensors and cache."""
+    work = []
+    for lens in ([9, 40, 2, 6], [1500, 700]):
+        q, k, v = (randn(sum(lens), h, 128, dtype=dtype).requires_grad_() for h in (8, 2, 2))
+        cu = torch.tensor([0, *torch.tensor(lens).cumsum(0).tolist()], dtype=torch.int32, device="cuda")
+        cache = hga.PagedKVCache.new(1, 256, 16, 2, len(lens), 2048, dtype)
+        rows = torch.arange(len(lens), dtype=torch.int32, device="cuda")
+        add = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        cache.write(0, k.detach(), v.detach(), cu, rows, cache.reserve(rows, add))
+        new, d_o = randn(len(lens), 8, 128, dtype=dtype), torch.randn_like(q)
+
+        def step(q=q, k=k, v=v, cu=cu, cache=cache, rows=rows, new=new, d_o=d_o):
+            o, lse = hga.packed_attention(q, k, v, cu)
+            return [o.detach(), lse, *torch.autograd.grad(o, (q, k, v), d_o), *cache.attend(0, new, rows)]
+
+        work.append((step, torch.cuda.Stream()))
+    want = [step() for step, _ in work]
+    torch.cuda.synchronize()
+    errors = []
+
+    def run(i):
+        try:
+            step, stream = work[i]
+            with torch.cuda.stream(stream):
+                for _ in range(40):
+                    got = step()
+                    stream.synchronize()
+                    assert all(torch.equal(a, b) for a, b in zip(got, want[i]))
+        except BaseException as e:                     # noqa: BLE001 (raised again below)
+            errors.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    if errors:
+        raise errors[0]
