@@ -144,9 +144,9 @@ def _with_flags(cfg, flags: int):
 
 def packed_attn_fwd(cfg, q, k, v, cu_seqlens, o=None, lse=None, workspace=None, o_lo=None):
     """Forward, for a cfg of these tensors' shapes and strides (checked).  Rows of no sequence are left as they
-    were in a given o / lse, and hold zeros / -inf in a new one.  o_lo: an output like o for a backward pass in bfloat16, what rounding took from o.  workspace: ``new_workspace(cfg, device)``,
-    zeroed once (``read_status`` tells of a cu_seqlens that is not
-    valid); without one the call makes its own."""
+    were in a given o / lse, and hold zeros / -inf in a new one.  o_lo: an output like o for a backward pass in
+    bfloat16, what rounding took from o.  workspace: ``new_workspace(cfg, device)``, zeroed once
+    (``read_status`` tells of a cu_seqlens that is not valid); without one the call makes its own."""
     _check_packed(cfg, q, k, v, cu_seqlens)
     return _fwd(cfg, q, k, v, cu_seqlens, o, lse, workspace, o_lo)
 
